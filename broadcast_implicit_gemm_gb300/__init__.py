@@ -23,6 +23,10 @@ __all__ = [
     "conv2d_nchw_plan", "conv2d_nchw_plan_ex", "conv2d_nchw_run", "conv2d_nchw_plan_destroy",
     "conv2d_nchw_plan_describe", "conv2d_nchw_run_noalloc", "bcast_nchw_run",
     "bcast_nchw_run_flat", "bcast_run",
+    "MXF8", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "ACT_NAMES",
+    "COMBINE_NONE", "COMBINE_ADD", "COMBINE_MUL", "COMBINE_NAMES",
+    "matmul_run", "matmul_mx_run", "rmsnorm_run", "mx_quantize_run", "bigemm_mx_scale_bytes",
+    "matmul", "matmul_mx", "rmsnorm", "mx_quantize", "mx_scale_shape",
     "bigemm_status_string", "bigemm_last_device_error", "bigemm_clear_device_error",
     "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout", "bigemm_profile_enable",
     "bigemm_profile_read", "bigemm_version", "conv2d", "bcast", "out_size",
@@ -36,6 +40,11 @@ MODE_NHWC, MODE_DIRECT, MODE_HALO, MODE_SUB, MODE_STACK, MODE_STRIDED, MODE_IM2C
 EPI_NAMES = {"none": EPI_NONE, "bias": EPI_BIAS, "bias_exp": EPI_BIAS_EXP,
              "bias_rsqrt": EPI_BIAS_RSQRT, "bias_recip": EPI_BIAS_RECIP, "bias_relu": EPI_BIAS_RELU}
 DTYPE_CODES = {"f32": F32, "f16": F16, "bf16": BF16}
+MXF8 = 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACT_NAMES = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+COMBINE_NONE, COMBINE_ADD, COMBINE_MUL = 0, 1, 2
+COMBINE_NAMES = {"none": COMBINE_NONE, "add": COMBINE_ADD, "mul": COMBINE_MUL}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -92,6 +101,13 @@ def _declare(lib):
     lib.bcast_nchw_run.argtypes = [i, i, i, i, i, p, f, p, i, p]
     lib.bcast_nchw_run_flat.argtypes = [i, i, i, i, i, p, f, p, i, p]
     lib.bcast_run.argtypes = [i, i, i, i, p, f, p, i, p]
+    i64 = ctypes.c_int64
+    lib.matmul_run.argtypes = [i, i, i, i, p, i64, p, i64, p, i, i, i, p, i64, i, p, i64, p]
+    lib.matmul_mx_run.argtypes = [i, i, i, p, i64, p, p, i64, p, p, i, i, i, p, i64, i, p, i64, p, p]
+    lib.rmsnorm_run.argtypes = [i, i, i, p, i64, p, i64, p, f, p, i64, i, p, i64, p, p]
+    lib.mx_quantize_run.argtypes = [i, i, i, p, i64, p, i64, p, p]
+    lib.bigemm_mx_scale_bytes.argtypes = [i, i]
+    lib.bigemm_mx_scale_bytes.restype = u64
     lib.bigemm_status_string.argtypes = [i]
     lib.bigemm_status_string.restype = ctypes.c_char_p
     lib.bigemm_last_device_error.argtypes = []
@@ -105,7 +121,8 @@ def _declare(lib):
     for name in ("conv2d_nchw_plan", "conv2d_nchw_plan_ex", "conv2d_nchw_run",
                  "conv2d_nchw_run_noalloc",
                  "conv2d_nchw_plan_destroy", "conv2d_nchw_plan_describe", "bcast_nchw_run",
-                 "bcast_nchw_run_flat", "bcast_run", "bigemm_last_device_error",
+                 "bcast_nchw_run_flat", "bcast_run", "matmul_run", "matmul_mx_run", "rmsnorm_run",
+                 "mx_quantize_run", "bigemm_last_device_error",
                  "bigemm_clear_device_error",
                  "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout",
                  "bigemm_profile_enable", "bigemm_profile_read"):
@@ -240,6 +257,36 @@ def bcast_run(B0, P, B1, op, var, eps, out, out_dtype, stream=None):
                                     _stream(stream)), "bcast_run")
 
 
+def matmul_run(M, N, K, in_dtype, x, ldx, w, ldw, bias, act, combine, other_dtype, other, ldother,
+               out_dtype, out, ldo, stream=None):
+    _check(load_library().matmul_run(M, N, K, in_dtype, _ptr(x), ldx, _ptr(w), ldw, _ptr(bias), act, combine,
+                                     other_dtype, _ptr(other), ldother, out_dtype, _ptr(out), ldo,
+                                     _stream(stream)), "matmul_run")
+
+
+def matmul_mx_run(M, N, K, x, ldx, x_scale, w, ldw, w_scale, bias, act, combine, other_dtype, other, ldother,
+                  out_dtype, out, ldo, out_scale, stream=None):
+    _check(load_library().matmul_mx_run(M, N, K, _ptr(x), ldx, _ptr(x_scale), _ptr(w), ldw, _ptr(w_scale),
+                                        _ptr(bias), act, combine, other_dtype, _ptr(other), ldother, out_dtype,
+                                        _ptr(out), ldo, _ptr(out_scale), _stream(stream)), "matmul_mx_run")
+
+
+def rmsnorm_run(rows, cols, in_dtype, x, ldx, residual, ldr, weight, eps, sum_out, lds, out_dtype, out, ldo,
+                out_scale, stream=None):
+    _check(load_library().rmsnorm_run(rows, cols, in_dtype, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight),
+                                      float(eps), _ptr(sum_out), lds, out_dtype, _ptr(out), ldo,
+                                      _ptr(out_scale), _stream(stream)), "rmsnorm_run")
+
+
+def mx_quantize_run(rows, cols, in_dtype, x, ldx, out, ldo, scale, stream=None):
+    _check(load_library().mx_quantize_run(rows, cols, in_dtype, _ptr(x), ldx, _ptr(out), ldo, _ptr(scale),
+                                          _stream(stream)), "mx_quantize_run")
+
+
+def bigemm_mx_scale_bytes(rows: int, cols: int) -> int:
+    return load_library().bigemm_mx_scale_bytes(rows, cols)
+
+
 def bigemm_last_device_error() -> int:
     return load_library().bigemm_last_device_error()
 
@@ -321,3 +368,210 @@ def bcast(var, N, H, W, op=BC_EXP, eps=1e-5, out_dtype=None, out=None, stream=No
         out = torch.empty((N, C, H, W), dtype=odt, device=var.device)
     bcast_nchw_run(N, C, H, W, op, var, eps, out, _dtype_code(odt), stream)
     return out
+
+
+# ------------------------------------------------------------ transformer layer
+#
+# Matrices are 2-D CUDA tensors whose last axis is contiguous.  MXFP8 matrices
+# are a float8_e4m3fn tensor and its scales, a contiguous float8_e8m0fnu (or
+# uint8) tensor of mx_scale_shape(rows, cols).
+
+_LAYER_CODES: dict = {}
+
+
+def _layer_code(dtype) -> int:
+    if not _LAYER_CODES:
+        import torch
+        _LAYER_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
+                             torch.float8_e4m3fn: MXF8})
+    code = _LAYER_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _matrix(t, name, rows=None, cols=None, device=None):
+    """The row stride of a CUDA matrix, checked."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-D CUDA tensor")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got ({r}, {c})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    s = t.stride()
+    if c > 1 and s[1] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    # a single row's stride may be anything
+    if r > 1 and s[0] < c:
+        raise ValueError(f"{name}: rows overlap")
+    return s[0] if r > 1 else max(s[0], c)
+
+
+def _vector(t, name, n, device):
+    import torch
+    if t is None:
+        return
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous float32 vector of {n} elements on {device}")
+
+
+def mx_scale_shape(rows: int, cols: int) -> tuple:
+    """Shape of the scales of a rows x cols MXFP8 matrix: the scale of (r, k) is at
+    [r // 128, k // 128, r % 32, (r % 128) // 32, (k % 128) // 32]."""
+    return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
+
+
+def _scales(t, name, rows, cols, device):
+    import torch
+    n = 1
+    for d in mx_scale_shape(rows, cols):
+        n *= d
+    if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous scales of shape {mx_scale_shape(rows, cols)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _new_scales(rows, cols, device):
+    import torch
+    return torch.zeros(mx_scale_shape(rows, cols), dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+
+
+def _run_on(device, stream, call):
+    """call(stream) with `device` current, on the given stream or torch's current one there."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _product(x, xs, w, ws, bias, act, other, combine, out_dtype, out, out_scale, stream):
+    import torch
+    mx = xs is not None
+    dev = x.device
+    ldx = _matrix(x, "x")
+    M, K = x.shape
+    ldw = _matrix(w, "w", None, K, dev)
+    N = w.shape[0]
+    if w.dtype != x.dtype:
+        raise TypeError(f"x is {x.dtype} and w is {w.dtype}")
+    in_code = _layer_code(x.dtype)
+    if mx != (in_code == MXF8):
+        raise TypeError("matmul_mx takes float8_e4m3fn matrices, matmul 16-bit ones")
+    if mx:
+        _scales(xs, "x_scale", M, K, dev)
+        _scales(ws, "w_scale", N, K, dev)
+    _vector(bias, "bias", N, dev)
+    if combine is None:
+        combine = COMBINE_NONE if other is None else COMBINE_ADD
+    ldother, other_code = 0, F32
+    if combine != COMBINE_NONE:
+        if other is None:
+            raise ValueError("combine needs other")
+        ldother, other_code = _matrix(other, "other", M, N, dev), _layer_code(other.dtype)
+    if out is None:
+        odt = out_dtype if out_dtype is not None else (torch.bfloat16 if mx else x.dtype)
+        out = torch.empty((M, N), dtype=odt, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    ldo, out_code = _matrix(out, "out", M, N, dev), _layer_code(out.dtype)
+    if out_code == MXF8:
+        if out_scale is None:
+            out_scale = _new_scales(M, N, dev)
+        else:
+            _scales(out_scale, "out_scale", M, N, dev)
+    else:
+        out_scale = None
+    if mx:
+        _run_on(dev, stream, lambda s: matmul_mx_run(M, N, K, x, ldx, xs, w, ldw, ws, bias, act, combine, other_code,
+                                                     other if combine else None, ldother, out_code, out, ldo,
+                                                     out_scale, s))
+    else:
+        _run_on(dev, stream, lambda s: matmul_run(M, N, K, in_code, x, ldx, w, ldw, bias, act, combine, other_code,
+                                                  other if combine else None, ldother, out_code, out, ldo, s))
+    return out if out_scale is None else (out, out_scale)
+
+
+def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=None, out=None, stream=None):
+    """combine(act(x @ w.T + bias), other): x [M, K] and w [N, K] float16 or bfloat16, bias [N] float32.
+
+    `combine` is COMBINE_ADD (a residual; the default when `other` is given) or COMBINE_MUL (a gate).
+    Sums in fp32; out is x's type unless out_dtype (float32, float16, bfloat16) or out says otherwise.
+    """
+    return _product(x, None, w, None, bias, act, other, combine, out_dtype, out, None, stream)
+
+
+def matmul_mx(x, x_scale, w, w_scale, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=None, out=None,
+              out_scale=None, stream=None):
+    """matmul of MXFP8 matrices.  out is bfloat16 unless out_dtype or out says otherwise; for
+    float8_e4m3fn the result is (elements, scales)."""
+    return _product(x, x_scale, w, w_scale, bias, act, other, combine, out_dtype, out, out_scale, stream)
+
+
+def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, out_scale=None, sum_out=None,
+            stream=None):
+    """h = x + residual; y = h * rsqrt(mean(h * h) + eps) * weight over the last axis of a matrix.
+
+    Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.
+    """
+    import torch
+    dev = x.device
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    code = _layer_code(x.dtype)
+    if code == MXF8:
+        raise TypeError("rmsnorm takes float32, float16 or bfloat16")
+    ldr = lds = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", rows, cols, dev)
+        if residual.dtype != x.dtype:
+            raise TypeError(f"x is {x.dtype} and residual is {residual.dtype}")
+        if sum_out is None:
+            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    if sum_out is not None:
+        lds = _matrix(sum_out, "sum_out", rows, cols, dev)
+        if sum_out.dtype != x.dtype:
+            raise TypeError(f"x is {x.dtype} and sum_out is {sum_out.dtype}")
+    _vector(weight, "weight", cols, dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else x.dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    ldo, out_code = _matrix(out, "out", rows, cols, dev), _layer_code(out.dtype)
+    if out_code == MXF8:
+        if out_scale is None:
+            out_scale = _new_scales(rows, cols, dev)
+        else:
+            _scales(out_scale, "out_scale", rows, cols, dev)
+    else:
+        out_scale = None
+    _run_on(dev, stream, lambda s: rmsnorm_run(rows, cols, code, x, ldx, residual, ldr, weight, eps, sum_out, lds,
+                                               out_code, out, ldo, out_scale, s))
+    got = (out,) if out_scale is None else (out, out_scale)
+    if residual is not None:
+        got += (sum_out,)
+    return got if len(got) > 1 else out
+
+
+def mx_quantize(x, out=None, scale=None, stream=None):
+    """(float8_e4m3fn elements, scales) of a float32, float16 or bfloat16 matrix."""
+    import torch
+    dev = x.device
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    code = _layer_code(x.dtype)
+    if code == MXF8:
+        raise TypeError("mx_quantize takes float32, float16 or bfloat16")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    elif out.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"out is {out.dtype}")
+    ldo = _matrix(out, "out", rows, cols, dev)
+    if scale is None:
+        scale = _new_scales(rows, cols, dev)
+    else:
+        _scales(scale, "scale", rows, cols, dev)
+    _run_on(dev, stream, lambda s: mx_quantize_run(rows, cols, code, x, ldx, out, ldo, scale, s))
+    return out, scale

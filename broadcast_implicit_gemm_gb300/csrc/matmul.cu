@@ -1,0 +1,128 @@
+// matmul.cu -- entry points of the matrix products (16-bit and MXFP8 operands):
+// argument checks, tensor maps, and the choice of kernel.
+#include <algorithm>
+
+#include "matmul.cuh"
+
+using namespace bigemm;
+
+namespace {
+
+bool on_grid(const void *p, long long ld, long long size, long long to)
+{
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0 && (ld * size) % to == 0;
+}
+
+// A row-major operand as boxes of `rows` rows by 128 bytes, 128-byte swizzle.
+bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows, long long cols, long long ld, int box_rows)
+{
+    const size_t es = dt == BIGEMM_MXF8 ? 1 : 2;
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)ld * es};
+    const uint32_t box[2] = {(uint32_t)(kRow / es), (uint32_t)box_rows};
+    const uint32_t ones[2] = {1, 1};
+    const CUtensorMapDataType t = dt == BIGEMM_MXF8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : dt == BIGEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode_tiled(map, t, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Tokens per tile: the smallest that holds them all (each tile reads the
+// weights again), at most 64 for a 32-bit output, whose running sums are in
+// registers.  K is shared among CTAs until two per SM are busy, as long as each
+// keeps four stages.
+FewCut choose_few(const MatmulArgs &a, int sms)
+{
+    FewCut c;
+    c.bn = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || a.out_dt == BIGEMM_F32 ? 64 : 128;
+    const long long tiles = ((a.N + 127ll) / 128) * ((a.M + (long long)c.bn - 1) / c.bn);
+    const long long want = std::min<long long>(std::min<long long>(8, a.k_blocks / 4), 2ll * sms / tiles);
+    const int s = (int)std::max<long long>(1, want);
+    const int per = (a.k_blocks + s - 1) / s;
+    c.split = (a.k_blocks + per - 1) / per;
+    return c;
+}
+
+constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bits
+
+// Elements of K that one tensor-memory accumulator sums for a 32-bit output.
+constexpr int kFullSegment = 1024;
+
+bigemm_status product(MatmulArgs &a, void *stream)
+{
+    if (a.M < 0 || a.N < 1 || a.K < 1) return BIGEMM_ERR_INVALID_ARG;
+    const bool mx = a.in_dt == BIGEMM_MXF8;
+    if (a.act < BIGEMM_ACT_NONE || a.act > BIGEMM_ACT_SILU) return BIGEMM_ERR_INVALID_ARG;
+    if (a.combine < BIGEMM_COMBINE_NONE || a.combine > BIGEMM_COMBINE_MUL) return BIGEMM_ERR_INVALID_ARG;
+    if (a.M == 0) return BIGEMM_OK;
+    if (a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize) return BIGEMM_ERR_UNSUPPORTED;
+    if (!a.x || !a.w || !a.out || (mx && (!a.xs || !a.ws))) return BIGEMM_ERR_INVALID_ARG;
+    if ((a.out_dt == BIGEMM_MXF8) != (a.outs != nullptr)) return BIGEMM_ERR_INVALID_ARG;
+    if (a.ldx < a.K || a.ldw < a.K || a.ldo < a.N) return BIGEMM_ERR_INVALID_ARG;
+    const long long es = mx ? 1 : 2, os = a.out_dt == BIGEMM_MXF8 ? 1 : (long long)dtype_size(a.out_dt);
+    if (!on_grid(a.x, 0, 1, es) || !on_grid(a.w, 0, 1, es) || !on_grid(a.out, 0, 1, os)) return BIGEMM_ERR_INVALID_ARG;
+    if (!on_grid(a.xs, 0, 1, 16) || !on_grid(a.ws, 0, 1, 16) || !on_grid(a.outs, 0, 1, 16) ||
+        !on_grid(a.bias, 0, 1, 4))
+        return BIGEMM_ERR_INVALID_ARG;
+    if (a.combine != BIGEMM_COMBINE_NONE) {
+        if (a.other_dt < BIGEMM_F32 || a.other_dt > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
+        const long long ts = (long long)dtype_size(a.other_dt);
+        if (!a.other || a.ldother < a.N || !on_grid(a.other, 0, 1, ts)) return BIGEMM_ERR_INVALID_ARG;
+        a.vec_other = on_grid(a.other, a.ldother, ts, 16);
+    }
+    DeviceState *ds = device_state();
+    if (!ds) return BIGEMM_ERR_CUDA;
+    a.vec_out = on_grid(a.out, a.ldo, os, a.out_dt == BIGEMM_MXF8 ? 8 : 16);
+    a.k_blocks = (int)((a.K * es + kRow - 1) / kRow);
+    a.timeout_ns = wait_timeout_ns();
+    a.err = ds->err;
+    // TMA: rows on the 16-byte grid, strides below 2^40 bytes
+    const long long far = 1ll << 40;
+    const bool gather = !on_grid(a.x, a.ldx, es, 16) || !on_grid(a.w, a.ldw, es, 16) || a.ldx * es >= far ||
+                        a.ldw * es >= far;
+    const FewCut cut = choose_few(a, ds->sm_count);
+    if ((a.M + (long long)cut.bn - 1) / cut.bn > 65535) return BIGEMM_ERR_UNSUPPORTED;
+    a.kb_per = (a.k_blocks + cut.split - 1) / cut.split;
+    a.seg_blocks = a.out_dt == BIGEMM_F32 ? (int)(kFullSegment * es / kRow) : a.kb_per;
+    CUtensorMap mw = {}, mxm = {};
+    if (!gather && (!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
+                    !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn)))
+        return BIGEMM_ERR_CUDA;
+    const cudaError_t e = launch_matmul_few(a, cut, gather, mw, mxm, (cudaStream_t)stream);
+    return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx, const void *w,
+                         int64_t ldw, const float *bias, int act, int combine, bigemm_dtype other_dtype,
+                         const void *other, int64_t ldother, bigemm_dtype out_dtype, void *out, int64_t ldo,
+                         void *stream)
+{
+    if (in_dtype < BIGEMM_F32 || in_dtype > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
+    if (out_dtype < BIGEMM_F32 || out_dtype > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
+    if (in_dtype == BIGEMM_F32) return BIGEMM_ERR_UNSUPPORTED;
+    MatmulArgs a = {};
+    a.M = M, a.N = N, a.K = K, a.in_dt = in_dtype, a.out_dt = out_dtype, a.other_dt = other_dtype;
+    a.act = act, a.combine = combine, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.ldo = ldo, a.ldother = ldother;
+    a.bias = bias, a.other = other, a.out = out;
+    return product(a, stream);
+}
+
+bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, const void *x_scale, const void *w,
+                            int64_t ldw, const void *w_scale, const float *bias, int act, int combine,
+                            bigemm_dtype other_dtype, const void *other, int64_t ldother, bigemm_dtype out_dtype,
+                            void *out, int64_t ldo, void *out_scale, void *stream)
+{
+    if (out_dtype < BIGEMM_F32 || out_dtype > BIGEMM_MXF8) return BIGEMM_ERR_INVALID_ARG;
+    MatmulArgs a = {};
+    a.M = M, a.N = N, a.K = K, a.in_dt = BIGEMM_MXF8, a.out_dt = out_dtype, a.other_dt = other_dtype;
+    a.act = act, a.combine = combine, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.ldo = ldo, a.ldother = ldother;
+    a.xs = static_cast<const uint8_t *>(x_scale), a.ws = static_cast<const uint8_t *>(w_scale);
+    a.bias = bias, a.other = other, a.out = out, a.outs = static_cast<uint8_t *>(out_scale);
+    return product(a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,248 @@
+// matmul.cuh -- pieces shared by the matrix-product kernels: the problem as a
+// kernel sees it, the epilogue's arithmetic, and the tcgen05 wrappers that only
+// these kernels use (block-scaled MMA, the copy of scales into tensor memory).
+//
+//   out[m,n] = combine(act(sum_k x[m,k] w[n,k] + bias[n]), other[m,n])
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace bigemm {
+
+struct MatmulArgs {
+    int M, N, K;                     // tokens, output channels, the summed length
+    int in_dt, out_dt, other_dt;     // bigemm_dtype
+    int act, combine;
+    const void *x, *w;               // [M,K], [N,K]; rows ldx and ldw elements apart
+    long long ldx, ldw, ldo, ldother;
+    const uint8_t *xs, *ws;          // MXFP8: blocked scales
+    const float *bias;               // [N] or null
+    const void *other;               // [M,N] or null
+    void *out;
+    uint8_t *outs;                   // MXFP8 output: blocked scales
+    bool vec_out, vec_other;         // rows start on 16-byte boundaries (8 for e4m3 outputs)
+    int k_blocks;                    // 128-byte pieces of a row
+    int seg_blocks;                  // of them, how many one tensor-memory accumulator sums
+    int kb_per;                      // of them, how many one CTA of a split takes
+    unsigned long long timeout_ns;
+    int *err;
+};
+
+namespace {
+
+constexpr int kRow = 128;            // bytes of one row in a stage: a 128-byte swizzle row
+
+// act(z).  silu and the tanh form of gelu are both z / (1 + exp(-t)): with
+// tanh(u) = 2 / (1 + exp(-2u)) - 1, gelu's 0.5 z (1 + tanh(u)) is
+// z / (1 + exp(-2u)).  The quotient is the approximate one (2 ulp; a divisor
+// above 2^126 gives 0, which is z's sigmoid to within 2^-126).
+__device__ __forceinline__ float mm_act(int act, float z)
+{
+    switch (act) {
+    case BIGEMM_ACT_RELU: return z < 0.f ? 0.f : z;
+    case BIGEMM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case BIGEMM_ACT_GELU_TANH:
+        return __fdividef(z, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    case BIGEMM_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float mm_combine(int how, float z, float o)
+{
+    return how == BIGEMM_COMBINE_ADD ? z + o : how == BIGEMM_COMBINE_MUL ? z * o : z;
+}
+
+__device__ __forceinline__ float mm_load1(const void *p, long long i, int dt)
+{
+    if (dt == BIGEMM_F32) return static_cast<const float *>(p)[i];
+    if (dt == BIGEMM_F16) return __half2float(static_cast<const __half *>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+// 8 consecutive values from element i on, i * element size on a 16-byte boundary.
+__device__ __forceinline__ void mm_load8(const void *p, long long i, int dt, float (&v)[8])
+{
+    if (dt == BIGEMM_F32) {
+        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float2 f;
+        if (dt == BIGEMM_F16)
+            f = __half22float2(*reinterpret_cast<const __half2 *>(&q[j]));
+        else
+            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q[j]));
+        v[2 * j] = f.x, v[2 * j + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t mm_pack2(float a, float b, int dt)
+{
+    if (dt == BIGEMM_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void mm_store1(void *p, long long i, int dt, float v)
+{
+    if (dt == BIGEMM_F32) static_cast<float *>(p)[i] = v;
+    else if (dt == BIGEMM_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// bias, act and combine of 8 consecutive channels from n on of token m, in
+// place; channels past N become 0.
+__device__ __forceinline__ void mm_epilogue8(const MatmulArgs &a, int m, int n, float (&v)[8])
+{
+    float b[8], o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = a.bias && n + j < a.N ? __ldg(a.bias + n + j) : 0.f;
+    if (a.combine != BIGEMM_COMBINE_NONE) {
+        const long long at = (long long)m * a.ldother + n;
+        if (a.vec_other && n + 8 <= a.N) {
+            mm_load8(a.other, at, a.other_dt, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = n + j < a.N ? mm_load1(a.other, at + j, a.other_dt) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float z = mm_act(a.act, v[j] + b[j]);
+        v[j] = n + j < a.N ? mm_combine(a.combine, z, a.combine != BIGEMM_COMBINE_NONE ? o[j] : 0.f) : 0.f;
+    }
+}
+
+// 8 channels of a 32- or 16-bit output.
+__device__ __forceinline__ void mm_store8(const MatmulArgs &a, int m, int n, const float (&v)[8])
+{
+    const long long at = (long long)m * a.ldo + n;
+    if (a.vec_out && n + 8 <= a.N) {
+        if (a.out_dt == BIGEMM_F32) {
+            float *p = static_cast<float *>(a.out) + at;
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
+                make_uint4(mm_pack2(v[0], v[1], a.out_dt), mm_pack2(v[2], v[3], a.out_dt),
+                           mm_pack2(v[4], v[5], a.out_dt), mm_pack2(v[6], v[7], a.out_dt));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (n + j < a.N) mm_store1(a.out, at + j, a.out_dt, v[j]);
+    }
+}
+
+// 8 channels of an e4m3 output, 1 / scale given.
+__device__ __forceinline__ void mm_store8_mx(const MatmulArgs &a, int m, int n, const float (&v)[8], float inv)
+{
+    const uint32_t lo = mx_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    const uint32_t hi = mx_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    uint8_t *p = static_cast<uint8_t *>(a.out) + (long long)m * a.ldo + n;
+    if (a.vec_out && n + 8 <= a.N) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (n + j < a.N) p[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+    }
+}
+
+// ------------------------------------------------------------------ wrappers
+// Untiled bulk copy into shared memory: both addresses on 16-byte boundaries,
+// a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 512 bytes of scales (a block of 128 rows by 4 groups) from shared memory into
+// four tensor-memory columns: 32 rows of 16 bytes, repeated for the four lane
+// quadrants.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// D (+)= (A scaled) * (B scaled), e4m3 operands with an E8M0 scale per 32
+// elements of K; the scales' byte within their tensor-memory column is in idesc.
+__device__ __forceinline__ void umma_mx(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "mov.b64 ad, {%1, %2};\n\t"
+        "mov.b64 bd, {%3, %4};\n\t"
+        "setp.ne.b32 p, %8, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], ad, bd, %5, [%6], [%7], p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sa), "r"(sb), "r"(accum)
+        : "memory");
+}
+
+// Instruction descriptor of the block-scaled MMA for K-major e4m3 operands and
+// E8M0 scales: bit 23 the scales' type, N >> 3 at bit 17, M >> 7 at bit 27; the
+// scales' byte goes to bits 4 (B) and 29 (A).
+__host__ __device__ constexpr uint32_t make_idesc_mx(uint32_t M, uint32_t N)
+{
+    return (1u << 23) | ((N >> 3) << 17) | ((M >> 7) << 27);
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// Shared memory of CTA `rank` of the cluster (address from mapa_shared).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+}  // namespace
+
+// The kernel for few tokens (matmul_few.cu).  How a product is cut: tokens per
+// tile (16, 32, 64 or 128) and CTAs that share one tile's K.
+struct FewCut {
+    int bn, split;
+};
+cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
+                              const CUtensorMap &map_x, cudaStream_t stream);
+
+}  // namespace bigemm

@@ -1,0 +1,408 @@
+// matmul_few.cu -- the matrix product for few tokens: 128 output channels by
+// BN tokens per CTA, the K axis shared by a cluster of CTAs.
+//
+// The weights are the 128-row operand of the MMA and the tokens its N side, so
+// a handful of tokens wastes tensor work (which is free here) and no memory
+// traffic.  Such a product is bound by the weights' bytes; one CTA per 128
+// channels would leave most SMs without any, so `split` CTAs take a slice of K
+// each, and as a cluster add up their fp32 partial sums through distributed
+// shared memory: in rank order, so that the result does not depend on timing,
+// without a workspace and without a second launch.
+//
+// GATHER: rows that TMA cannot address (a stride or base off the 16-byte grid)
+// are brought into the same swizzled stages by six more warps with plain loads.
+//
+// MX: e4m3 operands; a stage's 128 bytes of a row are 128 elements, whose
+// scales are one block of 512 bytes per operand.  They land beside the stage
+// and go to tensor memory columns of that stage before its MMAs.
+//
+// FULL: a 32-bit output.  The tensor core cuts each addition into its fp32
+// accumulator short, so the error of one long sum grows with K (measured
+// 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 1024 elements
+// are added up in registers instead, two accumulators taking turns.
+#include "matmul.cuh"
+
+namespace bigemm {
+
+namespace {
+
+constexpr int kFewThreads = 256;               // producer, MMA, two idle warps, four that drain
+constexpr int kGatherWarps = 6;
+constexpr int kFewA = 128 * kRow;              // bytes of weights per stage
+
+template <int BN>
+struct FewCfg {
+    // 110 KB, so that two CTAs share an SM and no third kernel that
+    // allocates tensor memory fits beside them: a cluster whose CTAs could wait
+    // for tensor memory held by another cluster's would not end
+    static constexpr int stage = kFewA + BN * kRow + 2 * kMxBlockBytes;
+    static constexpr int stages = BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr int smem = 110 * 1024;
+    static_assert(stages * stage + 256 <= 109 * 1024 && BN * 512 <= stages * stage, "fits");
+};
+
+template <int BN, bool MX, bool FULL>
+constexpr uint32_t few_cols()
+{
+    const int n = (FULL ? 2 : 1) * BN + (MX ? 8 * FewCfg<BN>::stages : 0);
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+}
+
+// One 16-byte piece of a row's 128-byte block, byte by byte where it has to
+// be: `size`-byte elements, `have` of them inside the row.
+__device__ __forceinline__ uint4 gather16(const uint8_t *p, int size, int have)
+{
+    uint32_t q[4] = {0, 0, 0, 0};
+    if (size == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < have) q[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < have) q[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+template <bool GATHER>
+constexpr int few_threads() { return kFewThreads + (GATHER ? 32 * kGatherWarps : 0); }
+
+template <int BN, bool MX, bool GATHER, bool FULL>
+__global__ void __launch_bounds__(few_threads<GATHER>())
+    matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const MatmulArgs p)
+{
+    using C = FewCfg<BN>;
+    constexpr int S = C::stages;
+    constexpr int ACC = FULL ? 2 : 1;
+    constexpr uint32_t kCols = few_cols<BN, MX, FULL>();
+    static_assert(ACC * BN + (MX ? 8 * S : 0) <= (int)kCols, "tensor memory");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sa = smem, *sb = smem + S * kFewA, *ss = sb + S * BN * kRow;   // weights, tokens, scales
+    uint64_t *full = reinterpret_cast<uint64_t *>(ss + S * 2 * kMxBlockBytes);
+    uint64_t *empty = full + S, *tfull = empty + S, *tempty = tfull + 2, *drain = tempty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    float *part = reinterpret_cast<float *>(smem);   // [BN][128] sums, over the stages once they are done
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = (int)((p.k_blocks + p.kb_per - 1) / p.kb_per);   // CTAs of the cluster
+    const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+    const int ct = (int)blockIdx.x / split, n0 = ct * 128;
+    const int m0 = (int)blockIdx.y * BN;
+    const int kb0 = rank * p.kb_per, kb1 = min(p.k_blocks, kb0 + p.kb_per);
+    const int xblocks = p.k_blocks;                  // MX: blocks of scales per block row
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], GATHER ? 32 * kGatherWarps : 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if (!GATHER) {
+            tma_prefetch_desc(&map_w);
+            tma_prefetch_desc(&map_x);
+        }
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(tmem_holder, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    griddep_enter();
+
+    bool good = true;
+    float acc[FULL ? BN : 1];       // FULL, warps 4-7: the sums over finished segments
+    if (FULL) {
+#pragma unroll
+        for (int i = 0; i < (FULL ? BN : 1); ++i) acc[i] = 0.f;
+    }
+
+    if (GATHER ? warp >= 8 : warp == 0) {
+        // ------------------------------------------------------ producers
+        const int esize = MX ? 1 : 2, per = kRow / esize;      // elements per stage row
+        int stage = 0;
+        uint32_t phase = 0, last_parity[S];
+        bool issued[S];
+        for (int i = 0; i < S; ++i) issued[i] = false, last_parity[i] = 0;
+        for (int kb = kb0; good && kb < kb1; ++kb) {
+            uint8_t *a_dst = sa + stage * kFewA, *b_dst = sb + stage * BN * kRow;
+            uint8_t *s_dst = ss + stage * 2 * kMxBlockBytes;
+            good = mbar_wait_warp(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
+            if (!good) break;
+            if (GATHER) {
+                const int t = (int)threadIdx.x - kFewThreads;
+                const long long e0 = (long long)kb * per;
+                for (int i = t; i < (128 + BN) * 8; i += 32 * kGatherWarps) {
+                    const bool is_w = i < 128 * 8;
+                    const int j = is_w ? i : i - 128 * 8, row = j >> 3, c16 = j & 7;
+                    const long long r = is_w ? (long long)n0 + row : (long long)m0 + row;
+                    const int have = r < (is_w ? p.N : p.M)
+                                         ? (int)min((long long)(16 / esize), max(0ll, p.K - e0 - c16 * (16 / esize)))
+                                         : 0;
+                    const uint8_t *src = static_cast<const uint8_t *>(is_w ? p.w : p.x) +
+                                         (r * (is_w ? p.ldw : p.ldx) + e0 + c16 * (16 / esize)) * esize;
+                    uint8_t *dst = (is_w ? a_dst : b_dst) + row * kRow + ((c16 ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst) = gather16(src, esize, have);
+                }
+                if (MX) {
+                    for (int i = t; i < 64; i += 32 * kGatherWarps) {
+                        const bool is_w = i < 32;
+                        const long long blk = (is_w ? n0 >> 7 : m0 >> 7) * (long long)xblocks + kb;
+                        *reinterpret_cast<uint4 *>(s_dst + i * 16) = *reinterpret_cast<const uint4 *>(
+                            (is_w ? p.ws : p.xs) + blk * kMxBlockBytes + (i & 31) * 16);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&full[stage]);
+            } else if (lane == 0) {
+                mbar_arrive_expect_tx(&full[stage], (uint32_t)(kFewA + BN * kRow + (MX ? 2 * kMxBlockBytes : 0)));
+                issued[stage] = true;
+                last_parity[stage] = phase;
+                tma_load_2d(a_dst, &map_w, &full[stage], kb * per, n0);
+                tma_load_2d(b_dst, &map_x, &full[stage], kb * per, m0);
+                if (MX) {
+                    bulk_load(s_dst, p.ws + ((long long)(n0 >> 7) * xblocks + kb) * kMxBlockBytes, kMxBlockBytes,
+                              &full[stage]);
+                    bulk_load(s_dst + kMxBlockBytes, p.xs + ((long long)(m0 >> 7) * xblocks + kb) * kMxBlockBytes,
+                              kMxBlockBytes, &full[stage]);
+                }
+            }
+            if (++stage == S) stage = 0, phase ^= 1u;
+        }
+        if (!GATHER && !good && lane == 0) {
+            int local_abort = 0;
+            for (int i = 0; i < S; ++i)
+                if (issued[i]) mbar_wait(&full[i], last_parity[i], p.timeout_ns, &local_abort, p.err);
+        }
+        __syncwarp();
+    }
+    if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = MX ? make_idesc_mx(128, BN)
+                                      : make_idesc(p.in_dt == BIGEMM_BF16 ? 1u : 0u, 0u, 0u, 128, BN);
+            const uint32_t hi = desc_hi(1024u, 2u);
+            // scales: rows of 16 bytes without a swizzle, 8-row groups 128 bytes apart
+            const uint32_t s_hi = desc_hi(128u, 0u);
+            // a 64-token tile's scales are the first or the second half of their block's columns
+            const uint32_t sb_shift = (uint32_t)((m0 & 127) >> 5);
+            int stage = 0, a = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, any = false;
+            for (int k0 = kb0; ok && k0 < kb1; k0 += p.seg_blocks) {
+                ok = mbar_wait(&tempty[a], acc_phase ^ 1u, p.timeout_ns, abort_flag, p.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(a * BN);
+                const int k1 = min(kb1, k0 + p.seg_blocks);
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_lo = desc_lo(smem_u32(sa + stage * kFewA), 16u);
+                    const uint32_t b_lo = desc_lo(smem_u32(sb + stage * BN * kRow), 16u);
+                    if (MX) {
+                        const uint32_t s_lo = desc_lo(smem_u32(ss + stage * 2 * kMxBlockBytes), 0u);
+                        const uint32_t sf = tmem_base + (uint32_t)(ACC * BN + 8 * stage);
+                        tmem_copy_scales(sf, (uint64_t)s_hi << 32 | s_lo);
+                        tmem_copy_scales(sf + 4, (uint64_t)s_hi << 32 | (s_lo + (kMxBlockBytes >> 4)));
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            umma_mx(d, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc | (k << 4) | (k << 29), sf,
+                                    sf + 4 + sb_shift, (kb > k0 || k > 0) ? 1u : 0u);
+                    } else {
+                        umma4_kmajor<false>(d, a_lo, hi, b_lo, hi, idesc, kb > k0 ? 1u : 0u);
+                    }
+                    any = true;
+                    umma_commit(&empty[stage]);
+                    if (++stage == S) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                umma_commit(&tfull[a]);
+                if (++a == ACC) a = 0, acc_phase ^= 1u;
+            }
+            if (!ok && any) {
+                int local_abort = 0;
+                umma_commit(drain);
+                mbar_wait(drain, 0, p.timeout_ns, &local_abort, p.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------ drain: lane = channel, column = token
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+        float *dst = part + q * 32 + lane;
+        int a = 0;
+        uint32_t acc_phase = 0;
+        for (int k0 = kb0; good && k0 < kb1; k0 += p.seg_blocks) {
+            good = mbar_wait_warp(&tfull[a], acc_phase, p.timeout_ns, abort_flag, p.err);
+            if (!good) break;
+            tc_fence_after();
+            const bool last = k0 + p.seg_blocks >= kb1;
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(lane_base + (uint32_t)(a * BN + c), r);
+                tmem_wait_ld16(r);
+                if (FULL) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[(FULL ? c : 0) + (FULL ? i : 0)] += __uint_as_float(r[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) dst[(c + i) * 128] = __uint_as_float(r[i]);
+                }
+            }
+            if (FULL && last) {
+                // the last segment's accumulator is full, so every stage has been read
+#pragma unroll
+                for (int i = 0; i < BN; ++i) dst[i * 128] = acc[FULL ? i : 0];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[a]);
+            if (++a == ACC) a = 0, acc_phase ^= 1u;
+        }
+    }
+
+    tc_fence_before();
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync_all();
+    } else {
+        __syncthreads();
+    }
+    tc_fence_after();
+
+    // ---------------------------------------------------------- sum over the ranks and epilogue
+    // pieces of 8 channels, 16 to a token; a rank takes a run of whole tokens
+    const int tokens = min(BN, p.M - m0);
+    const int per_rank = (tokens + split - 1) / split;
+    const int t0 = rank * per_rank, t1 = min(tokens, t0 + per_rank);
+    for (int i0 = t0 * 16; i0 < t1 * 16; i0 += few_threads<GATHER>()) {
+        const int i = i0 + (int)threadIdx.x;
+        const bool live = i < t1 * 16;
+        const int t = live ? i >> 4 : t0, c = (i & 15) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        if (live) {
+            const uint32_t at = smem_u32(part + t * 128 + c);
+            for (int s = 0; s < split; ++s) {
+                float4 u0, u1;
+                if (split > 1) {
+                    const uint32_t peer = mapa_shared(at, (uint32_t)s);
+                    u0 = ld_cluster_f4(peer), u1 = ld_cluster_f4(peer + 16);
+                } else {
+                    u0 = *reinterpret_cast<const float4 *>(part + t * 128 + c);
+                    u1 = *reinterpret_cast<const float4 *>(part + t * 128 + c + 4);
+                }
+                v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
+                v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
+            }
+            mm_epilogue8(p, m0 + t, n0 + c, v);
+        }
+        if (p.out_dt == BIGEMM_MXF8) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = mx_amax(m, v[j]);
+            m = mx_amax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = mx_amax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t code = mx_scale_code(m);
+            if (live) {
+                if ((lane & 3) == 0)
+                    p.outs[mx_scale_offset(m0 + t, (n0 + c) / kMxGroup, (int)((p.N + 127ll) / 128))] = (uint8_t)code;
+                mm_store8_mx(p, m0 + t, n0 + c, v, mx_inv_scale(code));
+            }
+        } else if (live) {
+            mm_store8(p, m0 + t, n0 + c, v);
+        }
+    }
+
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync_all();   // no CTA leaves while a peer may still read its sums
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem_base, kCols);
+    }
+}
+
+template <int BN, bool MX, bool GATHER, bool FULL>
+cudaError_t launch_one(const MatmulArgs &a, int split, const CUtensorMap &mw, const CUtensorMap &mx,
+                       cudaStream_t stream)
+{
+    auto kern = matmul_few_kernel<BN, MX, GATHER, FULL>;
+    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !(attr_set >> dev & 1ull)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<BN>::smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set |= 1ull << dev;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.N + 127ll) / 128 * split), (unsigned)((a.M + (long long)BN - 1) / BN));
+    cfg.blockDim = dim3(few_threads<GATHER>());
+    cfg.dynamicSmemBytes = FewCfg<BN>::smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+}
+
+template <int BN>
+cudaError_t launch_bn(const MatmulArgs &a, int split, bool gather, const CUtensorMap &mw, const CUtensorMap &mx,
+                      cudaStream_t s)
+{
+    if (a.out_dt == BIGEMM_F32) {
+        if constexpr (BN <= 64) {
+            if (a.in_dt == BIGEMM_MXF8)
+                return gather ? launch_one<BN, true, true, true>(a, split, mw, mx, s)
+                              : launch_one<BN, true, false, true>(a, split, mw, mx, s);
+            return gather ? launch_one<BN, false, true, true>(a, split, mw, mx, s)
+                          : launch_one<BN, false, false, true>(a, split, mw, mx, s);
+        }
+        return cudaErrorInvalidValue;   // 128 running sums per thread would spill
+    }
+    if (a.in_dt == BIGEMM_MXF8)
+        return gather ? launch_one<BN, true, true, false>(a, split, mw, mx, s)
+                      : launch_one<BN, true, false, false>(a, split, mw, mx, s);
+    return gather ? launch_one<BN, false, true, false>(a, split, mw, mx, s)
+                  : launch_one<BN, false, false, false>(a, split, mw, mx, s);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
+                              const CUtensorMap &map_x, cudaStream_t stream)
+{
+    ProfScope prof("matmul_few", stream);
+    switch (cut.bn) {
+    case 16: return launch_bn<16>(a, cut.split, gather, map_w, map_x, stream);
+    case 32: return launch_bn<32>(a, cut.split, gather, map_w, map_x, stream);
+    case 64: return launch_bn<64>(a, cut.split, gather, map_w, map_x, stream);
+    case 128: return launch_bn<128>(a, cut.split, gather, map_w, map_x, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace bigemm

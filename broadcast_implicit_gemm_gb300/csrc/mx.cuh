@@ -1,0 +1,65 @@
+// mx.cuh -- MXFP8: e4m3 elements with one power-of-two scale per 32 elements
+// of a row, shared by the kernels that write it (norm.cu, the matrix products).
+//
+// The scale of a group is the smallest power of two s with amax <= 448 s (448
+// is e4m3's largest value), so no element saturates; it is stored as the byte
+// code with s = 2^(code - 127) (E8M0).  A group that holds a NaN or an infinity
+// gets code 255, E8M0's NaN, and NaN elements.
+//
+// Scales are kept in blocks of 128 rows by 128 columns, 512 bytes each, the
+// blocks of one block row next to each other.  Within a block, the byte of row
+// r and group g is (r % 32) * 16 + (r / 32) * 4 + g: the order in which tensor
+// memory takes a block's scales from shared memory in one copy.
+#pragma once
+#include <cstdint>
+#include <cuda_fp8.h>
+
+namespace bigemm {
+
+constexpr int kMxGroup = 32;        // elements per scale
+constexpr int kMxBlock = 128;       // rows, and columns, per block of scales
+constexpr int kMxBlockBytes = 512;
+
+// Byte offset of the scale of (row, group) in a matrix with col_blocks blocks
+// per block row.
+__device__ __forceinline__ long long mx_scale_offset(long long row, int group, int col_blocks)
+{
+    const int r = (int)(row & 127);
+    return ((row >> 7) * col_blocks + (group >> 2)) * kMxBlockBytes + (r & 31) * 16 + (r >> 5) * 4 +
+           (group & 3);
+}
+
+// The scale's code from a group's largest magnitude: its exponent less 8, one
+// more where the fraction exceeds 448's (1.75); at least 0 (2^-127).
+__device__ __forceinline__ uint32_t mx_scale_code(float amax)
+{
+    const uint32_t b = __float_as_uint(amax) & 0x7fffffffu;
+    if (b >= 0x7f800000u) return 255u;
+    const int code = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return (uint32_t)max(code, 0);
+}
+
+// 1 / s = 2^(127 - code), exact (codes of finite groups are at most 247).
+__device__ __forceinline__ float mx_inv_scale(uint32_t code)
+{
+    if (code >= 255u) return __uint_as_float(0x7fffffffu);
+    return __uint_as_float(code >= 254u ? 0x00400000u : (254u - code) << 23);
+}
+
+// The largest magnitude of two values, NaN if either is.
+__device__ __forceinline__ float mx_amax(float a, float b)
+{
+    const uint32_t x = __float_as_uint(a) & 0x7fffffffu, y = __float_as_uint(b) & 0x7fffffffu;
+    return __uint_as_float(max(x, y));
+}
+
+// Four floats, already divided by the scale, as e4m3 (nearest even), the first
+// in the low byte.
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+}  // namespace bigemm

@@ -50,7 +50,9 @@
 extern "C" {
 #endif
 
-typedef enum { BIGEMM_F32 = 0, BIGEMM_F16 = 1, BIGEMM_BF16 = 2 } bigemm_dtype;
+/* MXF8 (the transformer-layer operators below alone): e4m3 elements with one
+ * power-of-two scale (E8M0) per 32 elements of a row, kept apart. */
+typedef enum { BIGEMM_F32 = 0, BIGEMM_F16 = 1, BIGEMM_BF16 = 2, BIGEMM_MXF8 = 3 } bigemm_dtype;
 
 /* Fused epilogue: out = acc (NONE), acc + bias[f] (BIAS),
  * exp(acc + bias[f]) (BIAS_EXP), 1/sqrt(acc + bias[f] + eps) (BIAS_RSQRT),
@@ -279,6 +281,87 @@ bigemm_status conv2d_nchw_run_noalloc(int N, int H, int W, int CO, int CI, int K
                                       bigemm_dtype out_dtype, bigemm_epilogue epi,
                                       const void *data, const void *kernel, const float *bias,
                                       float eps, void *out, int *timeout_flag, void *stream);
+
+/* ------------------------------------------------ transformer-layer operators
+ *
+ * Matrices are row-major in device memory, rows `ld` elements apart (ld at
+ * least the row's length), each base on a boundary of its element size.  Rows
+ * on 16-byte boundaries take the fast paths; any other alignment is served too.
+ * The calls keep no state, need no workspace and allocate nothing; they are
+ * asynchronous on `stream`, and calls may overlap on different streams.  rows
+ * or M = 0 is a call that does nothing.
+ *
+ * MXF8 matrices: e4m3 elements, and a buffer of scales (16-byte aligned,
+ * bigemm_mx_scale_bytes(rows, cols) bytes): the byte `code` of element (r, k)
+ * stands for 2^(code - 127) and is at
+ *   ((r/128) * ceil(cols/128) + k/128) * 512 + (r%32)*16 + ((r%128)/32)*4 + (k%128)/32.
+ * Writers use the smallest power of two s >= 2^-127 with amax <= 448 s over the
+ * group's 32 elements and round each element / s to nearest even; a group with
+ * a NaN or an infinity gets code 255 and NaN elements.  They write the codes of
+ * every group of the rows' last 128-column block (0 past the last column), and
+ * leave the codes of rows past the last alone.  Readers ignore those rows' codes
+ * and expect finite codes (not 255) in groups past the last column.
+ */
+typedef enum {
+    BIGEMM_ACT_NONE = 0,
+    BIGEMM_ACT_RELU = 1,
+    BIGEMM_ACT_GELU = 2,        /* 0.5 z (1 + erf(z / sqrt 2))                          */
+    BIGEMM_ACT_GELU_TANH = 3,   /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))      */
+    BIGEMM_ACT_SILU = 4         /* z / (1 + exp(-z))                                    */
+} bigemm_act;
+
+typedef enum {
+    BIGEMM_COMBINE_NONE = 0,
+    BIGEMM_COMBINE_ADD = 1,     /* + other: the residual                                */
+    BIGEMM_COMBINE_MUL = 2      /* * other: the other half of a gated layer             */
+} bigemm_combine;
+
+/*
+ * matmul_run -- out[m,n] = combine(act(sum_k x[m,k] w[n,k] + bias[n]), other[m,n])
+ *   x [M,K], w [N,K] of in_dtype (F16 or BF16), fp32 sums; bias [N] fp32 or NULL
+ *   other [M,N] of other_dtype (F32, F16, BF16), read unless combine is NONE; it
+ *   may be out itself (same type and rows)
+ *   out [M,N] of out_dtype (F32, F16, BF16), rounded once.  For F32 at most 1024
+ *   products at a time are summed in the tensor core, the rest in fp32 adds.
+ * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum),
+ * UNSUPPORTED (in_dtype F32; N or K above 2^30, more than 4 million tokens), CUDA.
+ */
+bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx,
+                         const void *w, int64_t ldw, const float *bias, int act, int combine,
+                         bigemm_dtype other_dtype, const void *other, int64_t ldother,
+                         bigemm_dtype out_dtype, void *out, int64_t ldo, void *stream);
+
+/*
+ * matmul_mx_run -- the same product of MXF8 matrices x [M,K] and w [N,K] with
+ * their scales.  out_dtype F32, F16, BF16 (out_scale NULL), or MXF8: e4m3 into
+ * out and its scales into out_scale.
+ */
+bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, const void *x_scale,
+                            const void *w, int64_t ldw, const void *w_scale, const float *bias,
+                            int act, int combine, bigemm_dtype other_dtype, const void *other,
+                            int64_t ldother, bigemm_dtype out_dtype, void *out, int64_t ldo,
+                            void *out_scale, void *stream);
+
+/*
+ * rmsnorm_run -- h = x + residual; out = h * rsqrt(mean(h^2) + eps) * weight,
+ * row by row over `cols` columns, in fp32 from the inputs to one rounding of
+ * each output.
+ *   x, residual (NULL: none), sum_out (NULL: not wanted; receives h; it may be
+ *   x or residual itself) of in_dtype (F32, F16, BF16); weight [cols] fp32 or
+ *   NULL (ones); out of in_dtype, F32, or MXF8 (then out_scale, else NULL)
+ * Errors: INVALID_ARG, UNSUPPORTED (another out_dtype; cols above 2^30), CUDA.
+ */
+bigemm_status rmsnorm_run(int rows, int cols, bigemm_dtype in_dtype, const void *x, int64_t ldx,
+                          const void *residual, int64_t ldr, const float *weight, float eps,
+                          void *sum_out, int64_t lds, bigemm_dtype out_dtype, void *out, int64_t ldo,
+                          void *out_scale, void *stream);
+
+/* mx_quantize_run -- a matrix of in_dtype (F32, F16, BF16) as MXF8. */
+bigemm_status mx_quantize_run(int rows, int cols, bigemm_dtype in_dtype, const void *x, int64_t ldx,
+                              void *out, int64_t ldo, void *scale, void *stream);
+
+/* Bytes of the scales of a rows x cols MXF8 matrix (0 if a size is below 1). */
+uint64_t bigemm_mx_scale_bytes(int rows, int cols);
 
 /* Human-readable text of a status code (static storage). */
 const char *bigemm_status_string(bigemm_status s);
