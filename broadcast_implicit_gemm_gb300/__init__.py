@@ -390,30 +390,39 @@ def _layer_code(dtype) -> int:
     return code
 
 
-def _matrix(t, name, rows=None, cols=None, device=None):
-    """The row stride of a CUDA matrix, checked."""
+def _first(t, name):
+    """(rows, columns, row stride, device index) of the CUDA matrix that a call is about."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 2-D CUDA tensor")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got ({r}, {c})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    s = t.stride()
-    if c > 1 and s[1] != 1:
+    rows, cols = t.shape
+    return rows, cols, _rows_apart(t, name, rows, cols), t.get_device()
+
+
+def _rows_apart(t, name, rows, cols):
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    # a single row's stride may be anything
-    if r > 1 and s[0] < c:
-        raise ValueError(f"{name}: rows overlap")
-    return s[0] if r > 1 else max(s[0], c)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap")
+        return cols    # a single row's stride may be anything
+    return ld
 
 
-def _vector(t, name, n, device):
-    import torch
+def _matrix(t, name, rows, cols, dev):
+    """The row stride of another matrix of the call, rows x cols on device `dev`."""
+    if t.get_device() != dev or t.dim() != 2 or t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}) on cuda:{dev}, got {tuple(t.shape)} on {t.device}")
+    return _rows_apart(t, name, rows, cols)
+
+
+def _vector(t, name, n, dev):
+    """The address of a float32 vector, or None."""
     if t is None:
-        return
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous float32 vector of {n} elements on {device}")
+        return None
+    if _layer_code(t.dtype) != F32 or t.get_device() != dev or t.shape != (n,) or t.stride(0) != 1 and n > 1:
+        raise ValueError(f"{name}: expected a contiguous float32 vector of {n} elements on cuda:{dev}")
+    return t.data_ptr()
 
 
 def mx_scale_shape(rows: int, cols: int) -> tuple:
@@ -422,15 +431,12 @@ def mx_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
 
 
-def _scales(t, name, rows, cols, device):
-    import torch
-    n = 1
-    for d in mx_scale_shape(rows, cols):
-        n *= d
-    if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous scales of shape {mx_scale_shape(rows, cols)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+def _scales(t, name, rows, cols, dev):
+    """The address of the scales of a rows x cols MXFP8 matrix."""
+    if (t.element_size() != 1 or t.numel() != -(-rows // 128) * -(-cols // 128) * 512 or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise ValueError(f"{name}: expected contiguous scales of shape {mx_scale_shape(rows, cols)} on cuda:{dev}")
+    return t.data_ptr()
 
 
 def _new_scales(rows, cols, device):
@@ -438,60 +444,59 @@ def _new_scales(rows, cols, device):
     return torch.zeros(mx_scale_shape(rows, cols), dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
 
 
-def _run_on(device, stream, call):
-    """call(stream) with `device` current, on the given stream or torch's current one there."""
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current, on the given stream or torch's current one there."""
     import torch
-    if device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != 0:
+        raise BigemmError(status, where)
 
 
 def _product(x, xs, w, ws, bias, act, other, combine, out_dtype, out, out_scale, stream):
-    import torch
-    mx = xs is not None
-    dev = x.device
-    ldx = _matrix(x, "x")
-    M, K = x.shape
-    ldw = _matrix(w, "w", None, K, dev)
+    M, K, ldx, dev = _first(x, "x")
     N = w.shape[0]
+    ldw = _matrix(w, "w", N, K, dev)
     if w.dtype != x.dtype:
         raise TypeError(f"x is {x.dtype} and w is {w.dtype}")
     in_code = _layer_code(x.dtype)
-    if mx != (in_code == MXF8):
+    if (xs is not None) != (in_code == MXF8):
         raise TypeError("matmul_mx takes float8_e4m3fn matrices, matmul 16-bit ones")
-    if mx:
-        _scales(xs, "x_scale", M, K, dev)
-        _scales(ws, "w_scale", N, K, dev)
-    _vector(bias, "bias", N, dev)
     if combine is None:
         combine = COMBINE_NONE if other is None else COMBINE_ADD
-    ldother, other_code = 0, F32
+    ldother, other_code, other_ptr = 0, F32, None
     if combine != COMBINE_NONE:
         if other is None:
             raise ValueError("combine needs other")
-        ldother, other_code = _matrix(other, "other", M, N, dev), _layer_code(other.dtype)
+        ldother, other_code, other_ptr = _matrix(other, "other", M, N, dev), _layer_code(other.dtype), other.data_ptr()
     if out is None:
-        odt = out_dtype if out_dtype is not None else (torch.bfloat16 if mx else x.dtype)
-        out = torch.empty((M, N), dtype=odt, device=dev)
+        import torch
+        odt = out_dtype if out_dtype is not None else (torch.bfloat16 if in_code == MXF8 else x.dtype)
+        out = torch.empty((M, N), dtype=odt, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     ldo, out_code = _matrix(out, "out", M, N, dev), _layer_code(out.dtype)
+    lib = _lib or load_library()
+    if in_code != MXF8:
+        _call(lib.matmul_run, "matmul_run", dev, stream, M, N, K, in_code, x.data_ptr(), ldx, w.data_ptr(), ldw,
+              _vector(bias, "bias", N, dev), act, combine, other_code, other_ptr, ldother, out_code, out.data_ptr(), ldo)
+        return out
+    scale_ptr = None
     if out_code == MXF8:
         if out_scale is None:
-            out_scale = _new_scales(M, N, dev)
-        else:
-            _scales(out_scale, "out_scale", M, N, dev)
-    else:
-        out_scale = None
-    if mx:
-        _run_on(dev, stream, lambda s: matmul_mx_run(M, N, K, x, ldx, xs, w, ldw, ws, bias, act, combine, other_code,
-                                                     other if combine else None, ldother, out_code, out, ldo,
-                                                     out_scale, s))
-    else:
-        _run_on(dev, stream, lambda s: matmul_run(M, N, K, in_code, x, ldx, w, ldw, bias, act, combine, other_code,
-                                                  other if combine else None, ldother, out_code, out, ldo, s))
-    return out if out_scale is None else (out, out_scale)
+            out_scale = _new_scales(M, N, x.device)
+        scale_ptr = _scales(out_scale, "out_scale", M, N, dev)
+    _call(lib.matmul_mx_run, "matmul_mx_run", dev, stream, M, N, K, x.data_ptr(), ldx, _scales(xs, "x_scale", M, K, dev),
+          w.data_ptr(), ldw, _scales(ws, "w_scale", N, K, dev), _vector(bias, "bias", N, dev), act, combine, other_code,
+          other_ptr, ldother, out_code, out.data_ptr(), ldo, scale_ptr)
+    return out if scale_ptr is None else (out, out_scale)
 
 
 def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=None, out=None, stream=None):
@@ -516,62 +521,54 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, o
 
     Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.
     """
-    import torch
-    dev = x.device
-    ldx = _matrix(x, "x")
-    rows, cols = x.shape
+    rows, cols, ldx, dev = _first(x, "x")
     code = _layer_code(x.dtype)
     if code == MXF8:
         raise TypeError("rmsnorm takes float32, float16 or bfloat16")
     ldr = lds = 0
+    res_ptr = sum_ptr = scale_ptr = None
     if residual is not None:
-        ldr = _matrix(residual, "residual", rows, cols, dev)
+        ldr, res_ptr = _matrix(residual, "residual", rows, cols, dev), residual.data_ptr()
         if residual.dtype != x.dtype:
             raise TypeError(f"x is {x.dtype} and residual is {residual.dtype}")
         if sum_out is None:
-            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            import torch
+            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
     if sum_out is not None:
-        lds = _matrix(sum_out, "sum_out", rows, cols, dev)
+        lds, sum_ptr = _matrix(sum_out, "sum_out", rows, cols, dev), sum_out.data_ptr()
         if sum_out.dtype != x.dtype:
             raise TypeError(f"x is {x.dtype} and sum_out is {sum_out.dtype}")
-    _vector(weight, "weight", cols, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else x.dtype, device=dev)
+        import torch
+        out = torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     ldo, out_code = _matrix(out, "out", rows, cols, dev), _layer_code(out.dtype)
     if out_code == MXF8:
         if out_scale is None:
-            out_scale = _new_scales(rows, cols, dev)
-        else:
-            _scales(out_scale, "out_scale", rows, cols, dev)
-    else:
-        out_scale = None
-    _run_on(dev, stream, lambda s: rmsnorm_run(rows, cols, code, x, ldx, residual, ldr, weight, eps, sum_out, lds,
-                                               out_code, out, ldo, out_scale, s))
-    got = (out,) if out_scale is None else (out, out_scale)
-    if residual is not None:
-        got += (sum_out,)
-    return got if len(got) > 1 else out
+            out_scale = _new_scales(rows, cols, x.device)
+        scale_ptr = _scales(out_scale, "out_scale", rows, cols, dev)
+    _call((_lib or load_library()).rmsnorm_run, "rmsnorm_run", dev, stream, rows, cols, code, x.data_ptr(), ldx, res_ptr,
+          ldr, _vector(weight, "weight", cols, dev), eps, sum_ptr, lds, out_code, out.data_ptr(), ldo, scale_ptr)
+    if residual is None:
+        return out if scale_ptr is None else (out, out_scale)
+    return (out, sum_out) if scale_ptr is None else (out, out_scale, sum_out)
 
 
 def mx_quantize(x, out=None, scale=None, stream=None):
     """(float8_e4m3fn elements, scales) of a float32, float16 or bfloat16 matrix."""
-    import torch
-    dev = x.device
-    ldx = _matrix(x, "x")
-    rows, cols = x.shape
+    rows, cols, ldx, dev = _first(x, "x")
     code = _layer_code(x.dtype)
     if code == MXF8:
         raise TypeError("mx_quantize takes float32, float16 or bfloat16")
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
-    elif out.dtype != torch.float8_e4m3fn:
+        import torch
+        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+    elif _layer_code(out.dtype) != MXF8:
         raise TypeError(f"out is {out.dtype}")
     ldo = _matrix(out, "out", rows, cols, dev)
     if scale is None:
-        scale = _new_scales(rows, cols, dev)
-    else:
-        _scales(scale, "scale", rows, cols, dev)
-    _run_on(dev, stream, lambda s: mx_quantize_run(rows, cols, code, x, ldx, out, ldo, scale, s))
+        scale = _new_scales(rows, cols, x.device)
+    _call((_lib or load_library()).mx_quantize_run, "mx_quantize_run", dev, stream, rows, cols, code, x.data_ptr(), ldx,
+          out.data_ptr(), ldo, _scales(scale, "scale", rows, cols, dev))
     return out, scale

@@ -13,7 +13,36 @@ bool on_grid(const void *p, long long ld, long long size, long long to)
     return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0 && (ld * size) % to == 0;
 }
 
-// A row-major operand as boxes of `rows` rows by 128 bytes, 128-byte swizzle.
+// The scales of a rows x cols MXFP8 matrix as boxes of `blocks` blocks, one below the other.
+bool scale_map(CUtensorMap *map, const void *p, long long rows, long long cols, int blocks)
+{
+    const uint64_t cb = (uint64_t)((cols + kMxBlock - 1) / kMxBlock);
+    const uint64_t dims[3] = {kMxBlockBytes / 4, cb, (uint64_t)((rows + kMxBlock - 1) / kMxBlock)};
+    const uint64_t strides[2] = {kMxBlockBytes, cb * kMxBlockBytes};
+    const uint32_t box[3] = {kMxBlockBytes / 4, 1, (uint32_t)blocks};
+    const uint32_t ones[3] = {1, 1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The output as boxes of 32 tokens by 32 channels, swizzled over the box's rows.
+bool out_map(CUtensorMap *map, const MatmulArgs &a)
+{
+    const uint64_t es = a.out_dt == BIGEMM_MXF8 ? 1 : dtype_size(a.out_dt);
+    const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M};
+    const uint64_t strides[1] = {(uint64_t)a.ldo * es};
+    const uint32_t box[2] = {32, 32};
+    const uint32_t ones[2] = {1, 1};
+    const CUtensorMapDataType t = a.out_dt == BIGEMM_MXF8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : a.out_dt == BIGEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : a.out_dt == BIGEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode_tiled(map, t, 2, a.out, dims, strides, box, ones,
+                        es == 4   ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : es == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+// A row-major operand as boxes of box_rows rows by 128 bytes, 128-byte swizzle.
 bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows, long long cols, long long ld, int box_rows)
 {
     const size_t es = dt == BIGEMM_MXF8 ? 1 : 2;
@@ -41,6 +70,16 @@ FewCut choose_few(const MatmulArgs &a, int sms)
     const int per = (a.k_blocks + s - 1) / s;
     c.split = (a.k_blocks + per - 1) / per;
     return c;
+}
+
+// Channels per tile of the pair kernel: the width whose waves of tiles over the
+// SM pairs take less time, 128 if they are not more than 256's.
+int choose_many(const MatmulArgs &a, int sms)
+{
+    const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, pairs = sms / 2;
+    const long long wide = (mt * ((a.N + 255ll) / 256) + pairs - 1) / pairs * 256;
+    const long long narrow = (mt * ((a.N + 127ll) / 128) + pairs - 1) / pairs * 128;
+    return 14 * narrow < 10 * wide ? 128 : 256;
 }
 
 constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bits
@@ -74,16 +113,33 @@ bigemm_status product(MatmulArgs &a, void *stream)
     if (!ds) return BIGEMM_ERR_CUDA;
     a.vec_out = on_grid(a.out, a.ldo, os, a.out_dt == BIGEMM_MXF8 ? 8 : 16);
     a.k_blocks = (int)((a.K * es + kRow - 1) / kRow);
+    if (a.M == 1) a.ldx = (a.ldx + 15) / 16 * 16;   // the stride of a single row is free
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
     // TMA: rows on the 16-byte grid, strides below 2^40 bytes
     const long long far = 1ll << 40;
     const bool gather = !on_grid(a.x, a.ldx, es, 16) || !on_grid(a.w, a.ldw, es, 16) || a.ldx * es >= far ||
                         a.ldw * es >= far;
+    a.seg_blocks = a.out_dt == BIGEMM_F32 ? (int)(kFullSegment * es / kRow) : a.k_blocks;
+    if (!gather && a.M > 128) {
+        const int bn = choose_many(a, ds->sm_count);
+        const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, nt = (a.N + bn - 1ll) / bn;
+        if (mt * nt > 0x7fffffff) return BIGEMM_ERR_UNSUPPORTED;
+        a.m_tiles = (int)mt, a.n_tiles = (int)nt;
+        a.by_rows = on_grid(a.out, a.ldo, os, 16) && a.ldo * os < far && (a.combine == BIGEMM_COMBINE_NONE || a.vec_other);
+        ManyMaps maps = {};
+        if (!operand_map(&maps.x, a.x, a.in_dt, a.M, a.K, a.ldx, 128) ||
+            !operand_map(&maps.w, a.w, a.in_dt, a.N, a.K, a.ldw, bn / 2) ||
+            (mx && (!scale_map(&maps.xs, a.xs, a.M, a.K, 1) || !scale_map(&maps.ws, a.ws, a.N, a.K, bn / 128))) ||
+            (a.by_rows && !out_map(&maps.out, a)))
+            return BIGEMM_ERR_CUDA;
+        const cudaError_t e = launch_matmul_many(a, bn, ds->sm_count, maps, (cudaStream_t)stream);
+        return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
+    }
     const FewCut cut = choose_few(a, ds->sm_count);
     if ((a.M + (long long)cut.bn - 1) / cut.bn > 65535) return BIGEMM_ERR_UNSUPPORTED;
     a.kb_per = (a.k_blocks + cut.split - 1) / cut.split;
-    a.seg_blocks = a.out_dt == BIGEMM_F32 ? (int)(kFullSegment * es / kRow) : a.kb_per;
+    if (a.out_dt != BIGEMM_F32) a.seg_blocks = a.kb_per;
     CUtensorMap mw = {}, mxm = {};
     if (!gather && (!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
                     !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn)))

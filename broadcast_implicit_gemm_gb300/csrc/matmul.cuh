@@ -27,7 +27,9 @@ struct MatmulArgs {
     bool vec_out, vec_other;         // rows start on 16-byte boundaries (8 for e4m3 outputs)
     int k_blocks;                    // 128-byte pieces of a row
     int seg_blocks;                  // of them, how many one tensor-memory accumulator sums
-    int kb_per;                      // of them, how many one CTA of a split takes
+    int kb_per;                      // few tokens: of them, how many one CTA of a split takes
+    int m_tiles, n_tiles;            // many tokens: tiles of the output, 256 tokens by BN channels
+    bool by_rows;                    // many tokens: out and other have their rows on the 16-byte grid
     unsigned long long timeout_ns;
     int *err;
 };
@@ -55,6 +57,14 @@ __device__ __forceinline__ float mm_act(int act, float z)
 __device__ __forceinline__ float mm_combine(int how, float z, float o)
 {
     return how == BIGEMM_COMBINE_ADD ? z + o : how == BIGEMM_COMBINE_MUL ? z * o : z;
+}
+
+// The value of an element's bits.
+__device__ __forceinline__ float mm_value(uint32_t bits, int dt)
+{
+    return dt == BIGEMM_F32   ? __uint_as_float(bits)
+           : dt == BIGEMM_F16 ? __half2float(__ushort_as_half((unsigned short)bits))
+                              : __uint_as_float(bits << 16);
 }
 
 __device__ __forceinline__ float mm_load1(const void *p, long long i, int dt)
@@ -204,6 +214,56 @@ __host__ __device__ constexpr uint32_t make_idesc_mx(uint32_t M, uint32_t N)
     return (1u << 23) | ((N >> 3) << 17) | ((M >> 7) << 27);
 }
 
+// The same for a CTA pair: the copy goes from each CTA's shared memory into its
+// own tensor memory, the MMA is the pair's.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                             uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "mov.b64 ad, {%1, %2};\n\t"
+        "mov.b64 bd, {%3, %4};\n\t"
+        "setp.ne.b32 p, %8, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], ad, bd, %5, [%6], [%7], p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sa), "r"(sb), "r"(accum)
+        : "memory");
+}
+
+// A 2-D box into this CTA's shared memory, counted on a barrier of either CTA
+// of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t cluster_bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(cluster_bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
@@ -244,5 +304,13 @@ struct FewCut {
 };
 cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
                               const CUtensorMap &map_x, cudaStream_t stream);
+
+// The kernel for many tokens (matmul_many.cu): tiles of 256 tokens by bn (128 or
+// 256) channels.  maps: x, w, scales of x, scales of w, out.
+constexpr int kManyTokens = 256;
+struct ManyMaps {
+    CUtensorMap x, w, xs, ws, out;
+};
+cudaError_t launch_matmul_many(const MatmulArgs &a, int bn, int sms, const ManyMaps &maps, cudaStream_t stream);
 
 }  // namespace bigemm

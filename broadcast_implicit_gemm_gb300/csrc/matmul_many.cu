@@ -1,0 +1,493 @@
+// matmul_many.cu -- the matrix product for many tokens: a pair of CTAs per tile
+// of 256 tokens by BN output channels.
+//
+// Such a product is bound by the tensor cores.  The pair shares each MMA
+// (M = 256: 128 tokens per CTA, half of the weights' rows in each), which halves
+// what an SM's shared memory has to deliver for the weights: at 256 x 256 a CTA
+// stages 32 KB per 64 elements of K (128 in 8 bits) for 4 MMAs of 128 cycles.
+// Pairs are persistent; one warp loads, one issues MMAs, eight drain: two per
+// quarter of the tokens, each half of the channels, a lane to a token.  Tiles
+// are walked eight token tiles at a time across the channels, so that what runs
+// at once shares its operands in L2.
+//
+// 16-bit operands: two accumulators fill tensor memory, and a tile's epilogue
+// runs beside the next one's MMAs.  MX: the scales take columns too (12 per
+// stage), so there is one accumulator; the drain warps take all of it to
+// registers, hand it back, and go on from there.
+//
+// FULL: a 32-bit output, sums of at most 1024 elements added up in registers
+// (matmul_few.cu says why).
+#include "matmul.cuh"
+
+namespace bigemm {
+
+namespace {
+
+// Three warpgroups: producer, MMA and two idle warps; eight drain warps.  A block
+// launches with 168 registers a thread, 504 over the three; the first group
+// leaves 72 of them and the drain groups take 216 each, 504 again.
+constexpr int kManyThreads = 384;
+constexpr int kLaunchRegs = 168, kLeadRegs = 72, kDrainRegs = 216;
+static_assert(kLeadRegs + 2 * kDrainRegs <= 3 * kLaunchRegs, "a larger sum would wait for ever");
+constexpr int kManyA = 128 * kRow;             // a CTA's tokens per stage
+
+template <int BN, bool MX, bool FULL>
+struct ManyCfg {
+    static constexpr int b_bytes = BN / 2 * kRow;
+    static constexpr int s_bytes = MX ? (1 + BN / 128) * kMxBlockBytes : 0;   // the CTA's tokens, all of BN
+    static constexpr int stage = kManyA + b_bytes + s_bytes;
+    static constexpr int per_warp = FULL ? 4096 : MX ? 2048 : 4096;           // output staging
+    static constexpr int stages = BN == 128 ? 7 : FULL ? 5 : 6;
+    static constexpr int accs = MX ? 1 : 2;
+    static constexpr int smem = stages * stage + 8 * per_warp + 256 + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static constexpr uint32_t cols = accs * BN + (MX ? stages * (4 + BN / 32) : 0) <= 256 ? 256 : 512;
+    static_assert(accs * BN + (MX ? stages * (4 + BN / 32) : 0) <= 512, "tensor memory");
+};
+
+struct Tile {
+    int m, n;
+};
+
+// Eight token tiles share a sweep over the channel tiles.
+__device__ __forceinline__ Tile tile_of(const MatmulArgs &p, int t)
+{
+    constexpr int kGroup = 8;
+    const int per = kGroup * p.n_tiles;
+    const int g = t / per, r = t - g * per;
+    const int rows = min(kGroup, p.m_tiles - g * kGroup);
+    return {g * kGroup + r % rows, r / rows};
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = mm_act(ACT, v[i]);
+}
+
+// 32 channels of one token from channel n on: bias (lane i holds that of
+// channel n + i), act, combine.
+__device__ __forceinline__ void epilogue32(const MatmulArgs &p, long long m, int n, float bias, float (&v)[32])
+{
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+    }
+    switch (p.act) {
+    case BIGEMM_ACT_RELU: act_all<BIGEMM_ACT_RELU>(v); break;
+    case BIGEMM_ACT_GELU: act_all<BIGEMM_ACT_GELU>(v); break;
+    case BIGEMM_ACT_GELU_TANH: act_all<BIGEMM_ACT_GELU_TANH>(v); break;
+    case BIGEMM_ACT_SILU: act_all<BIGEMM_ACT_SILU>(v); break;
+    default: break;
+    }
+    if (p.combine == BIGEMM_COMBINE_NONE || m >= p.M) return;
+    const long long at = m * p.ldother + n;
+    const bool mul = p.combine == BIGEMM_COMBINE_MUL;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+        float o[8];
+        mm_load8(p.other, at + c, p.other_dt, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c + j] = mul ? v[c + j] * o[j] : v[c + j] + o[j];
+    }
+}
+
+// A drain warp's output of 32 tokens by 32 channels, all inside N, a lane's
+// token in v: through shared memory by TMA.  Returns the scale code of the
+// lane's group for an e4m3 output.
+template <int PER_WARP>
+__device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensorMap *map, uint8_t *stage, int &piece,
+                                             int lane, int m_warp, int n, float (&v)[32])
+{
+    uint32_t code = 0;
+    uint32_t w[32];
+    int words;                       // 32-bit words of the lane's row
+    if (p.out_dt == BIGEMM_MXF8) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = mx_amax(top, v[i]);
+        code = mx_scale_code(top);
+        const float inv = mx_inv_scale(code);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = mx_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        words = 8;
+    } else if (p.out_dt == BIGEMM_F32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+        words = 32;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], p.out_dt);
+        words = 16;
+    }
+    const int bytes = words * 128;                 // 32 rows
+    const int bufs = PER_WARP / bytes;
+    uint8_t *buf = stage + (piece % bufs) * bytes;
+    if (lane == 0) {
+        if (bufs == 1) bulk_wait_read<0>();
+        else bulk_wait_read<1>();
+    }
+    __syncwarp();
+    // the swizzle of the output's map: rows of 128, 64 or 32 bytes
+    const int key = words == 32 ? lane & 7 : words == 16 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c * 4 < words)
+            *reinterpret_cast<uint4 *>(buf + lane * words * 4 + ((c ^ key) << 4)) =
+                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && m_warp < p.M) {
+        tma_store_2d(map, buf, n, m_warp);
+        bulk_commit();
+    }
+    ++piece;
+    return code;
+}
+
+// The same 32 by 32 sums where rows are off the 16-byte grid or the channels
+// end inside: they are turned round in shared memory, 16 tokens at a time, so
+// that a lane has one channel of each token and the warp's plain loads and
+// stores cover a token's 32 channels at once.  All of the epilogue is here.
+__device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *stage, int lane, int m_warp, int n,
+                                                float bias, float (&v)[32])
+{
+    float *turn = reinterpret_cast<float *>(stage);
+    const bool in = n + lane < p.N;
+    uint32_t code = 0;
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        if (lane >> 4 == half) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) turn[(lane & 15) * 32 + (i ^ (lane & 15))] = v[i];
+        }
+        __syncwarp();
+        const int m0 = m_warp + half * 16;
+        uint32_t o[16];              // all loads leave before the first is used
+        if (p.combine != BIGEMM_COMBINE_NONE) {
+            const long long at = (long long)m0 * p.ldother + n + lane;
+            if (p.other_dt == BIGEMM_F32) {
+                const uint32_t *src = static_cast<const uint32_t *>(p.other) + at;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] = in && m0 + r < p.M ? src[r * p.ldother] : 0u;
+            } else {
+                const uint16_t *src = static_cast<const uint16_t *>(p.other) + at;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] = in && m0 + r < p.M ? src[r * p.ldother] : 0u;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float z = mm_act(p.act, turn[r * 32 + (lane ^ r)] + bias);
+            if (p.combine != BIGEMM_COMBINE_NONE) z = mm_combine(p.combine, z, mm_value(o[r], p.other_dt));
+            const bool live = in && m0 + r < p.M;
+            const long long at = (long long)(m0 + r) * p.ldo + n + lane;
+            if (p.out_dt == BIGEMM_MXF8) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(z) & 0x7fffffffu : 0u);
+                const uint32_t c = mx_scale_code(__uint_as_float(top));
+                if (lane == half * 16 + r) code = c;
+                if (live) static_cast<uint8_t *>(p.out)[at] = (uint8_t)mx_pack4(z * mx_inv_scale(c), 0.f, 0.f, 0.f);
+            } else if (live) {
+                mm_store1(p.out, at, p.out_dt, z);
+            }
+        }
+        __syncwarp();
+    }
+    return code;
+}
+
+template <int BN, bool MX, bool FULL>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    matmul_many_kernel(const __grid_constant__ ManyMaps maps, const MatmulArgs p)
+{
+    using C = ManyCfg<BN, MX, FULL>;
+    constexpr int S = C::stages, ACC = C::accs;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sa = smem, *sb = sa + S * kManyA, *out_stage = sb + S * C::b_bytes, *ss = out_stage + 8 * C::per_warp;
+    uint64_t *full = reinterpret_cast<uint64_t *>(ss + S * C::s_bytes);
+    uint64_t *empty = full + S, *tfull = empty + S, *tempty = tfull + 2, *drain = tempty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int tiles = p.m_tiles * p.n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        // an accumulator comes back from both CTAs' drain warps
+        for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 16);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.w);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc_pair(tmem_holder, C::cols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();   // both CTAs' barriers initialised and tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    griddep_enter();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeadRegs));
+        if (warp == 0) {
+            // ------------------------------------------------------ producer
+            if (lane == 0) {
+                constexpr int per = MX ? kRow : kRow / 2;         // elements of K per stage
+                const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+                int stage = 0;
+                uint32_t phase = 0, last_parity[S];
+                bool issued[S], ok = true;
+                for (int i = 0; i < S; ++i) issued[i] = false, last_parity[i] = 0;
+                for (int t = pair; ok && t < tiles; t += pairs) {
+                    const Tile tile = tile_of(p, t);
+                    const int m0 = tile.m * kManyTokens + rank * 128;
+                    const int n0 = tile.n * BN + rank * (BN / 2);
+                    for (int kb = 0; kb < p.k_blocks; ++kb) {
+                        ok = mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
+                        if (!ok) break;
+                        if (leader) mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)C::stage);
+                        issued[stage] = true, last_parity[stage] = phase;
+                        const uint32_t bar = full_even + (uint32_t)stage * 8u;
+                        tma_load_2d_pair(sa + stage * kManyA, &maps.x, bar, kb * per, m0);
+                        tma_load_2d_pair(sb + stage * C::b_bytes, &maps.w, bar, kb * per, n0);
+                        if (MX) {
+                            uint8_t *s = ss + stage * C::s_bytes;
+                            tma_load_3d_pair(s, &maps.xs, bar, 0, kb, m0 >> 7);
+                            tma_load_3d_pair(s + kMxBlockBytes, &maps.ws, bar, 0, kb, (tile.n * BN) >> 7);
+                        }
+                        if (++stage == S) stage = 0, phase ^= 1u;
+                    }
+                }
+                if (!ok) {
+                    if (leader) {
+                        int local_abort = 0;
+                        for (int i = 0; i < S; ++i)
+                            if (issued[i]) mbar_wait(&full[i], last_parity[i], p.timeout_ns, &local_abort, p.err);
+                    } else {
+                        // this CTA cannot wait on the even CTA's barriers: give its copies time to land
+                        const uint64_t t0 = globaltimer_ns();
+                        while (globaltimer_ns() - t0 < 20000ull) {
+                        }
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issuer
+            if (leader && lane == 0) {
+                const uint32_t idesc = MX ? make_idesc_mx(256, BN)
+                                          : make_idesc(p.in_dt == BIGEMM_BF16 ? 1u : 0u, 0u, 0u, 256, BN);
+                const uint32_t hi = desc_hi(1024u, 2u), s_hi = desc_hi(128u, 0u);
+                int stage = 0, a = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                bool ok = true, any = false;
+                for (int t = pair; ok && t < tiles; t += pairs) {
+                    for (int k0 = 0; ok && k0 < p.k_blocks; k0 += p.seg_blocks) {
+                        ok = mbar_wait(&tempty[a], acc_phase ^ 1u, p.timeout_ns, abort_flag, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem_base + (uint32_t)(a * BN);
+                        const int k1 = min(p.k_blocks, k0 + p.seg_blocks);
+                        for (int kb = k0; kb < k1; ++kb) {
+                            ok = mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t a_lo = desc_lo(smem_u32(sa + stage * kManyA), 16u);
+                            const uint32_t b_lo = desc_lo(smem_u32(sb + stage * C::b_bytes), 16u);
+                            if (MX) {
+                                const uint32_t s_lo = desc_lo(smem_u32(ss + stage * C::s_bytes), 0u);
+                                const uint32_t sf = tmem_base + (uint32_t)(ACC * BN + (4 + BN / 32) * stage);
+    #pragma unroll
+                                for (uint32_t i = 0; i < 1 + BN / 128; ++i)
+                                    tmem_copy_scales_pair(sf + 4 * i, (uint64_t)s_hi << 32 | (s_lo + i * (kMxBlockBytes >> 4)));
+    #pragma unroll
+                                for (uint32_t k = 0; k < 4; ++k)
+                                    umma_mx_pair(d, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc | (k << 4) | (k << 29), sf,
+                                                 sf + 4, (kb > k0 || k > 0) ? 1u : 0u);
+                            } else {
+                                umma4_kmajor_pair<false>(d, a_lo, hi, b_lo, hi, idesc, kb > k0 ? 1u : 0u);
+                            }
+                            any = true;
+                            umma_commit_pair_mc(&empty[stage], (uint16_t)3u);
+                            if (++stage == S) stage = 0, phase ^= 1u;
+                        }
+                        if (!ok) break;
+                        umma_commit_pair_mc(&tfull[a], (uint16_t)3u);
+                        if (++a == ACC) a = 0, acc_phase ^= 1u;
+                    }
+                }
+                if (!ok && any) {
+                    int local_abort = 0;
+                    umma_commit_pair(drain);
+                    mbar_wait(drain, 0, p.timeout_ns, &local_abort, p.err);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
+        // ------------------------------------------------------ drain and epilogue
+        constexpr bool KEEP = MX || FULL;              // the tile's sums go to registers first
+        constexpr int UNITS = BN / 64;                 // of 32 channels, per warp
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * (BN / 2));
+        const uint32_t tempty_even = mapa_shared(smem_u32(tempty), 0);
+        uint8_t *stage = out_stage + (warp - 4) * C::per_warp;
+        const int col_blocks = (int)((p.N + 127ll) / 128);
+        int a = 0, piece = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            const Tile tile = tile_of(p, t);
+            const int m_warp = tile.m * kManyTokens + rank * 128 + q * 32, n_warp = tile.n * BN + h * (BN / 2);
+            const long long m = m_warp + lane;
+            float bias[UNITS];
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int n = n_warp + u * 32 + lane;
+                bias[u] = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
+            }
+            uint32_t codes = 0;
+            float keep[KEEP ? UNITS : 1][32];
+            for (int k0 = 0; k0 < p.k_blocks; k0 += p.seg_blocks) {
+                ok = mbar_wait_warp(&tfull[a], acc_phase, p.timeout_ns, abort_flag, p.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t base = lane_base + (uint32_t)(a * BN);
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int u = 0; u < UNITS; ++u) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(base + u * 32, r);
+                        tmem_wait_ld32(r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            keep[u][i] = k0 > 0 ? keep[u][i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int u = 0; u < UNITS; ++u) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(base + u * 32, r);
+                        tmem_wait_ld32(r);
+                        const int n = n_warp + u * 32;
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        float b = bias[0];
+#pragma unroll
+                        for (int j = 1; j < UNITS; ++j) b = u == j ? bias[j] : b;
+                        if (p.by_rows && n + 32 <= p.N) {
+                            epilogue32(p, m, n, b, v);
+                            put_rows<C::per_warp>(p, &maps.out, stage, piece, lane, m_warp, n, v);
+                        } else if (n < p.N) {
+                            put_columns(p, stage, lane, m_warp, n, b, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty_even + (uint32_t)a * 8u);
+                if (++a == ACC) a = 0, acc_phase ^= 1u;
+            }
+            if constexpr (KEEP) {
+                if (!ok) break;
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) {
+                    const int n = n_warp + u * 32;
+                    if (p.by_rows && n + 32 <= p.N) {
+                        epilogue32(p, m, n, bias[u], keep[u]);
+                        codes |= put_rows<C::per_warp>(p, &maps.out, stage, piece, lane, m_warp, n, keep[u]) << (8 * u);
+                    } else if (n < p.N) {
+                        codes |= put_columns(p, stage, lane, m_warp, n, bias[u], keep[u]) << (8 * u);
+                    }
+                }
+                if (p.out_dt == BIGEMM_MXF8 && m < p.M && (n_warp >> 7) < col_blocks) {
+                    uint8_t *at = p.outs + mx_scale_offset(m, n_warp / kMxGroup, col_blocks);
+                    if (UNITS == 4) *reinterpret_cast<uint32_t *>(at) = codes;
+                    else *reinterpret_cast<uint16_t *>(at) = (uint16_t)codes;
+                }
+            }
+        }
+        // the staging is read before the block's shared memory goes
+        if (lane == 0) bulk_wait<0>();
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();   // neither CTA leaves while its partner may still use its memory
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, C::cols);
+    }
+}
+
+template <int BN, bool MX, bool FULL>
+cudaError_t launch_one(const MatmulArgs &a, int grid, const ManyMaps &maps, cudaStream_t stream)
+{
+    auto kern = matmul_many_kernel<BN, MX, FULL>;
+    constexpr int smem = ManyCfg<BN, MX, FULL>::smem;
+    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !(attr_set >> dev & 1ull)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        // the split of registers counts on what the block is launched with
+        cudaFuncAttributes fa;
+        const cudaError_t f = cudaFuncGetAttributes(&fa, kern);
+        if (f != cudaSuccess) return f;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        if (dev < 64) attr_set |= 1ull << dev;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kManyThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
+}
+
+template <int BN>
+cudaError_t launch_bn(const MatmulArgs &a, int grid, const ManyMaps &maps, cudaStream_t s)
+{
+    const bool full = a.out_dt == BIGEMM_F32;
+    if (a.in_dt == BIGEMM_MXF8)
+        return full ? launch_one<BN, true, true>(a, grid, maps, s) : launch_one<BN, true, false>(a, grid, maps, s);
+    return full ? launch_one<BN, false, true>(a, grid, maps, s) : launch_one<BN, false, false>(a, grid, maps, s);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_many(const MatmulArgs &a, int bn, int sms, const ManyMaps &maps, cudaStream_t stream)
+{
+    ProfScope prof("matmul_many", stream);
+    const long long tiles = (long long)a.m_tiles * a.n_tiles;
+    const int grid = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
+    return bn == 256 ? launch_bn<256>(a, grid, maps, stream) : launch_bn<128>(a, grid, maps, stream);
+}
+
+}  // namespace bigemm
