@@ -38,19 +38,38 @@ namespace {
 
 constexpr int kRow = 128;            // bytes of one row in a stage: a 128-byte swizzle row
 
-// act(z).  silu and the tanh form of gelu are both z / (1 + exp(-t)): with
+// act(z) of one kind.  silu and the tanh form of gelu are both z / (1 + exp(-t)): with
 // tanh(u) = 2 / (1 + exp(-2u)) - 1, gelu's 0.5 z (1 + tanh(u)) is
 // z / (1 + exp(-2u)).  The quotient is the approximate one (2 ulp; a divisor
 // above 2^126 gives 0, which is z's sigmoid to within 2^-126).
-__device__ __forceinline__ float mm_act(int act, float z)
+template <int ACT>
+__device__ __forceinline__ float mm_act(float z)
+{
+    if (ACT == BIGEMM_ACT_RELU) return z < 0.f ? 0.f : z;
+    if (ACT == BIGEMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if (ACT == BIGEMM_ACT_GELU_TANH)
+        return __fdividef(z, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    if (ACT == BIGEMM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    return z;
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void mm_act_each(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = mm_act<ACT>(v[i]);
+}
+
+// act of N values, chosen once for all of them.
+template <int N>
+__device__ __forceinline__ void mm_act_all(int act, float (&v)[N])
 {
     switch (act) {
-    case BIGEMM_ACT_RELU: return z < 0.f ? 0.f : z;
-    case BIGEMM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case BIGEMM_ACT_GELU_TANH:
-        return __fdividef(z, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    case BIGEMM_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
-    default: return z;
+    case BIGEMM_ACT_RELU: mm_act_each<BIGEMM_ACT_RELU>(v); break;
+    case BIGEMM_ACT_GELU: mm_act_each<BIGEMM_ACT_GELU>(v); break;
+    case BIGEMM_ACT_GELU_TANH: mm_act_each<BIGEMM_ACT_GELU_TANH>(v); break;
+    case BIGEMM_ACT_SILU: mm_act_each<BIGEMM_ACT_SILU>(v); break;
+    default: break;
     }
 }
 
@@ -130,9 +149,12 @@ __device__ __forceinline__ void mm_epilogue8(const MatmulArgs &a, int m, int n, 
         }
     }
 #pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+    mm_act_all(a.act, v);
+#pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float z = mm_act(a.act, v[j] + b[j]);
-        v[j] = n + j < a.N ? mm_combine(a.combine, z, a.combine != BIGEMM_COMBINE_NONE ? o[j] : 0.f) : 0.f;
+        if (a.combine != BIGEMM_COMBINE_NONE) v[j] = mm_combine(a.combine, v[j], o[j]);
+        if (n + j >= a.N) v[j] = 0.f;
     }
 }
 

@@ -59,13 +59,6 @@ __device__ __forceinline__ Tile tile_of(const MatmulArgs &p, int t)
     return {g * kGroup + r % rows, r / rows};
 }
 
-template <int ACT>
-__device__ __forceinline__ void act_all(float (&v)[32])
-{
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = mm_act(ACT, v[i]);
-}
-
 // 32 channels of one token from channel n on: bias (lane i holds that of
 // channel n + i), act, combine.
 __device__ __forceinline__ void epilogue32(const MatmulArgs &p, long long m, int n, float bias, float (&v)[32])
@@ -74,13 +67,7 @@ __device__ __forceinline__ void epilogue32(const MatmulArgs &p, long long m, int
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
     }
-    switch (p.act) {
-    case BIGEMM_ACT_RELU: act_all<BIGEMM_ACT_RELU>(v); break;
-    case BIGEMM_ACT_GELU: act_all<BIGEMM_ACT_GELU>(v); break;
-    case BIGEMM_ACT_GELU_TANH: act_all<BIGEMM_ACT_GELU_TANH>(v); break;
-    case BIGEMM_ACT_SILU: act_all<BIGEMM_ACT_SILU>(v); break;
-    default: break;
-    }
+    mm_act_all(p.act, v);
     if (p.combine == BIGEMM_COMBINE_NONE || m >= p.M) return;
     const long long at = m * p.ldother + n;
     const bool mul = p.combine == BIGEMM_COMBINE_MUL;
@@ -147,6 +134,30 @@ __device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensor
     return code;
 }
 
+// 16 values, a row each, to element 0 of rows ld bytes apart; `rows` of them.
+template <typename T>
+__device__ __forceinline__ void store_down(uint8_t *at, long long ld, int rows, const float (&v)[16])
+{
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        if (r < rows) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float *>(at) = v[r];
+            else *reinterpret_cast<T *>(at) = T(v[r]);
+        }
+        at += ld;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_down(const uint8_t *at, long long ld, int rows, uint32_t (&v)[16])
+{
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        v[r] = r < rows ? *reinterpret_cast<const T *>(at) : 0;
+        at += ld;
+    }
+}
+
 // The same 32 by 32 sums where rows are off the 16-byte grid or the channels
 // end inside: they are turned round in shared memory, 16 tokens at a time, so
 // that a lane has one channel of each token and the warp's plain loads and
@@ -166,34 +177,41 @@ __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *st
             for (int i = 0; i < 32; ++i) turn[(lane & 15) * 32 + (i ^ (lane & 15))] = v[i];
         }
         __syncwarp();
-        const int m0 = m_warp + half * 16;
+        const long long m0 = m_warp + half * 16;
+        const int rows = in ? (int)min(16ll, p.M - m0) : 0;      // that this lane reads and writes
         uint32_t o[16];              // all loads leave before the first is used
         if (p.combine != BIGEMM_COMBINE_NONE) {
-            const long long at = (long long)m0 * p.ldother + n + lane;
-            if (p.other_dt == BIGEMM_F32) {
-                const uint32_t *src = static_cast<const uint32_t *>(p.other) + at;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] = in && m0 + r < p.M ? src[r * p.ldother] : 0u;
-            } else {
-                const uint16_t *src = static_cast<const uint16_t *>(p.other) + at;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] = in && m0 + r < p.M ? src[r * p.ldother] : 0u;
-            }
+            const long long at = m0 * p.ldother + n + lane;
+            if (p.other_dt == BIGEMM_F32)
+                load_down<uint32_t>(static_cast<const uint8_t *>(p.other) + at * 4, p.ldother * 4, rows, o);
+            else
+                load_down<uint16_t>(static_cast<const uint8_t *>(p.other) + at * 2, p.ldother * 2, rows, o);
         }
+        float y[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float z = mm_act(p.act, turn[r * 32 + (lane ^ r)] + bias);
-            if (p.combine != BIGEMM_COMBINE_NONE) z = mm_combine(p.combine, z, mm_value(o[r], p.other_dt));
-            const bool live = in && m0 + r < p.M;
-            const long long at = (long long)(m0 + r) * p.ldo + n + lane;
-            if (p.out_dt == BIGEMM_MXF8) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(z) & 0x7fffffffu : 0u);
+        for (int r = 0; r < 16; ++r) y[r] = turn[r * 32 + (lane ^ r)] + bias;
+        mm_act_all(p.act, y);
+        if (p.combine != BIGEMM_COMBINE_NONE) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) y[r] = mm_combine(p.combine, y[r], mm_value(o[r], p.other_dt));
+        }
+        const long long at = m0 * p.ldo + n + lane;
+        uint8_t *out = static_cast<uint8_t *>(p.out);
+        if (p.out_dt == BIGEMM_MXF8) {
+            out += at;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(y[r]) & 0x7fffffffu : 0u);
                 const uint32_t c = mx_scale_code(__uint_as_float(top));
                 if (lane == half * 16 + r) code = c;
-                if (live) static_cast<uint8_t *>(p.out)[at] = (uint8_t)mx_pack4(z * mx_inv_scale(c), 0.f, 0.f, 0.f);
-            } else if (live) {
-                mm_store1(p.out, at, p.out_dt, z);
+                if (r < rows) out[r * p.ldo] = (uint8_t)mx_pack4(y[r] * mx_inv_scale(c), 0.f, 0.f, 0.f);
             }
+        } else if (p.out_dt == BIGEMM_F32) {
+            store_down<float>(out + at * 4, p.ldo * 4, rows, y);
+        } else if (p.out_dt == BIGEMM_F16) {
+            store_down<__half>(out + at * 2, p.ldo * 2, rows, y);
+        } else {
+            store_down<__nv_bfloat16>(out + at * 2, p.ldo * 2, rows, y);
         }
         __syncwarp();
     }
@@ -359,6 +377,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             for (int u = 0; u < UNITS; ++u) {
                 const int n = n_warp + u * 32 + lane;
                 bias[u] = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
+            }
+            if (p.combine != BIGEMM_COMBINE_NONE && m < p.M && n_warp < p.N) {
+                // the tile's part of other comes to L2 while the MMAs run
+                const long long es = p.other_dt == BIGEMM_F32 ? 4 : 2;
+                const uint8_t *from = static_cast<const uint8_t *>(p.other) + (m * p.ldother + n_warp) * es;
+                const int bytes = (int)(min(BN / 2, p.N - n_warp) * es);
+                for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + bytes - 1));
             }
             uint32_t codes = 0;
             float keep[KEEP ? UNITS : 1][32];
