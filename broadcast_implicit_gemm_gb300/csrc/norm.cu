@@ -46,19 +46,57 @@ struct alignas(16) Piece {
     T e[kPiece];
 };
 
-// 8 elements from column c on; zeros past the row's end.  VEC: the piece starts
-// on a 16-byte boundary.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_piece(const T *row, int c, int cols, float (&v)[kPiece])
+// 8 elements as they lie in memory.
+template <typename T>
+struct Raw {
+    uint4 q[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T> &p, float (&v)[kPiece])
 {
+    const T *e = reinterpret_cast<const T *>(&p);
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) v[i] = to_f32<T>(e[i]);
+}
+
+// 8 elements from column c on; zeros past the row's end.  VEC: the piece starts
+// on a 16-byte boundary.  Otherwise a 16-bit piece is cut out of the two
+// aligned 16-byte words around it where both lie inside the row, which takes 2
+// loads for 8; pieces at the row's ends go element by element.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load_raw(const T *row, int c, int cols)
+{
+    Raw<T> p;
     if (VEC && c + kPiece <= cols) {
-        const Piece<T> p = *reinterpret_cast<const Piece<T> *>(row + c);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) v[i] = to_f32<T>(p.e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) v[i] = c + i < cols ? to_f32<T>(row[c + i]) : 0.f;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) p.q[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+        return p;
     }
+    if (!VEC && sizeof(T) == 2 && c < cols) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c), lo = at & ~(uintptr_t)15;
+        if (lo >= reinterpret_cast<uintptr_t>(row) && lo + 32 <= reinterpret_cast<uintptr_t>(row + cols)) {
+            const uint4 a = reinterpret_cast<const uint4 *>(lo)[0], b = reinterpret_cast<const uint4 *>(lo)[1];
+            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const uint32_t by = (uint32_t)(at - lo);
+            if (by & 8) {
+#pragma unroll
+                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+            }
+            if (by & 4) {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+            }
+            const uint32_t sh = (by & 2) * 8;
+            p.q[0] = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                                __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+            return p;
+        }
+    }
+    T *e = reinterpret_cast<T *>(&p);
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) e[i] = c + i < cols ? row[c + i] : from_f32<T>(0.f);
+    return p;
 }
 
 template <typename T, bool VEC>
@@ -111,9 +149,11 @@ __device__ __forceinline__ void store_mx_piece(uint8_t *row, uint8_t *scale, lon
 
 struct NormArgs {
     int cols, col_blocks, pieces;     // pieces: of a row, padded to whole blocks of scales for MXFP8
+    FastDiv per_row;                  // by pieces
     long long rows, ldx, ldr, ldh, ldo;
     const void *x, *residual;
     const float *weight;
+    bool vec_weight;                  // there, on a 16-byte boundary
     float eps;
     void *h, *out;
     uint8_t *scale;
@@ -121,139 +161,231 @@ struct NormArgs {
 
 enum OutForm { OUT_SAME = 0, OUT_F32 = 1, OUT_MX = 2 };
 
-// One block per row, PPT pieces per thread kept in registers; a row longer than
-// that is read again for its outputs (PPT = 0).
-template <typename T, int FORM, int THREADS, int PPT, bool VEC>
-__global__ void __launch_bounds__(THREADS) rmsnorm_kernel(const NormArgs a)
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int FORM, typename T, bool VEC>
+__device__ __forceinline__ void norm_out(const NormArgs &a, long long r, int p, float inv, const float (&h)[kPiece],
+                                         const float (&g)[kPiece])
+{
+    const int c = p * kPiece;
+    float y[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) y[i] = c + i < a.cols ? h[i] * inv * g[i] : 0.f;
+    if (FORM == OUT_MX)
+        store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r * a.ldo, a.scale, r, c, a.cols, a.col_blocks,
+                            p < a.pieces, y);
+    else if (FORM == OUT_F32)
+        store_piece<float, VEC>(static_cast<float *>(a.out) + r * a.ldo, c, a.cols, y);
+    else
+        store_piece<T, VEC>(static_cast<T *>(a.out) + r * a.ldo, c, a.cols, y);
+}
+
+__device__ __forceinline__ void load_weight(const NormArgs &a, int c, float (&g)[kPiece])
+{
+    if (a.vec_weight && c + kPiece <= a.cols) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(a.weight + c));
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(a.weight + c + 4));
+        g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w, g[4] = w.x, g[5] = w.y, g[6] = w.z, g[7] = w.w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) g[i] = a.weight && c + i < a.cols ? __ldg(a.weight + c + i) : 1.f;
+}
+
+// TPR threads per row, PPT pieces per thread in registers; a block of
+// max(TPR, 128) threads walks over its rows and loads the next one before it
+// sums the present one, so that memory works through the sums and the barrier.
+// (The weights come from L1 again for each row: as registers they cost a third
+// of the rows in flight.)
+template <typename T, int FORM, int TPR, int PPT, bool VEC>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / TPR) rmsnorm_kernel(const NormArgs a)
 {
     griddep_enter();
-    constexpr int KEEP = PPT > 0 ? PPT : 1;
-    __shared__ float part[THREADS / 32];
-    const long long r = blockIdx.x;
-    const T *x = static_cast<const T *>(a.x) + r * a.ldx;
-    const T *res = a.residual ? static_cast<const T *>(a.residual) + r * a.ldr : nullptr;
-    T *h = a.h ? static_cast<T *>(a.h) + r * a.ldh : nullptr;
-    const int steps = PPT > 0 ? PPT : (a.pieces + THREADS - 1) / THREADS;
-    float v[KEEP][kPiece];
-    float sum = 0.f;
-    auto take = [&](int s, float (&w)[kPiece]) {
-        const int c = (s * THREADS + (int)threadIdx.x) * kPiece;
-        load_piece<T, VEC>(x, c, a.cols, w);
-        if (res) {
-            float t[kPiece];
-            load_piece<T, VEC>(res, c, a.cols, t);
+    constexpr int THREADS = TPR < 128 ? 128 : TPR, ROWS = THREADS / TPR;
+    static_assert(TPR == 32 || ROWS == 1, "a row has a warp or the block");
+    __shared__ float part[2][THREADS / 32];
+    const int t = (int)threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * ROWS;
+    long long r = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
+    Raw<T> x[PPT], res[PPT];
+    auto load = [&](long long row) {
+        if (row >= a.rows) return;
 #pragma unroll
-            for (int i = 0; i < kPiece; ++i) w[i] += t[i];
+        for (int s = 0; s < PPT; ++s)
+            x[s] = load_raw<T, VEC>(static_cast<const T *>(a.x) + row * a.ldx, (s * TPR + t) * kPiece, a.cols);
+        if (a.residual) {
+#pragma unroll
+            for (int s = 0; s < PPT; ++s)
+                res[s] = load_raw<T, VEC>(static_cast<const T *>(a.residual) + row * a.ldr, (s * TPR + t) * kPiece,
+                                          a.cols);
         }
     };
+    load(r);
+    // a warp without a row stays for the shuffles; a block's last turn is all of its warps'
+    for (int turn = 0; r - (ROWS > 1 ? threadIdx.x / TPR : 0) < a.rows; ++turn, r += step) {
+        float h[PPT][kPiece];
+        float sum = 0.f;
+        const bool live = r < a.rows;
 #pragma unroll
-    for (int s = 0; s < KEEP; ++s) {
-        if (PPT > 0) take(s, v[s]);
-    }
-    if (PPT > 0) {
+        for (int s = 0; s < PPT; ++s) {
+            unpack<T>(x[s], h[s]);
+            if (a.residual) {
+                float w[kPiece];
+                unpack<T>(res[s], w);
 #pragma unroll
-        for (int s = 0; s < KEEP; ++s) {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i) sum += v[s][i] * v[s][i];
+                for (int i = 0; i < kPiece; ++i) h[s][i] += w[i];
+            }
         }
-    } else {
-        for (int s = 0; s < steps; ++s) {
-            take(s, v[0]);
+        load(r + step);
 #pragma unroll
-            for (int i = 0; i < kPiece; ++i) sum += v[0][i] * v[0][i];
+        for (int s = 0; s < PPT; ++s) {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) sum += h[s][i] * h[s][i];
         }
-    }
+        sum = warp_sum(sum);
+        if (TPR > 32) {
+            if ((threadIdx.x & 31) == 0) part[turn & 1][threadIdx.x >> 5] = sum;
+            __syncthreads();
+            sum = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    float total = 0.f;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) total += part[i];
-    const float inv = 1.0f / sqrtf(total / (float)a.cols + a.eps);
-    auto put = [&](int s, float (&w)[kPiece]) {
-        const int p = s * THREADS + (int)threadIdx.x, c = p * kPiece;
-        if (h) store_piece<T, VEC>(h, c, a.cols, w);
-        float g[kPiece];
-        if (a.weight) {
-            load_piece<float, false>(a.weight, c, a.cols, g);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i) g[i] = 1.f;
+            for (int i = 0; i < THREADS / 32; ++i) sum += part[turn & 1][i];
         }
-        float y[kPiece];
+        const float inv = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+        if (!live) continue;
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) y[i] = c + i < a.cols ? w[i] * inv * g[i] : 0.f;
-        if (FORM == OUT_MX)
-            store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r * a.ldo, a.scale, r, c, a.cols,
-                                a.col_blocks, p < a.pieces, y);
-        else if (FORM == OUT_F32)
-            store_piece<float, VEC>(static_cast<float *>(a.out) + r * a.ldo, c, a.cols, y);
-        else
-            store_piece<T, VEC>(static_cast<T *>(a.out) + r * a.ldo, c, a.cols, y);
-    };
-    if (PPT > 0) {
-#pragma unroll
-        for (int s = 0; s < KEEP; ++s) put(s, v[s]);
-    } else {
-        for (int s = 0; s < steps; ++s) {
-            take(s, v[0]);
-            put(s, v[0]);
+        for (int s = 0; s < PPT; ++s) {
+            const int p = s * TPR + t;
+            if (a.h) store_piece<T, VEC>(static_cast<T *>(a.h) + r * a.ldh, p * kPiece, a.cols, h[s]);
+            float g[kPiece];
+            load_weight(a, p * kPiece, g);
+            norm_out<FORM, T, VEC>(a, r, p, inv, h[s], g);
         }
     }
 }
 
+// Rows too long for registers: one block per row, read a second time for the
+// outputs.
+template <typename T, int FORM, bool VEC>
+__global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
+{
+    griddep_enter();
+    __shared__ float part[16];
+    const long long r = blockIdx.x;
+    const T *x = static_cast<const T *>(a.x) + r * a.ldx;
+    const T *res = a.residual ? static_cast<const T *>(a.residual) + r * a.ldr : nullptr;
+    const int steps = (a.pieces + 511) / 512;
+    auto take = [&](int p, float (&h)[kPiece]) {
+        unpack<T>(load_raw<T, VEC>(x, p * kPiece, a.cols), h);
+        if (res) {
+            float w[kPiece];
+            unpack<T>(load_raw<T, VEC>(res, p * kPiece, a.cols), w);
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) h[i] += w[i];
+        }
+    };
+    float sum = 0.f;
+    for (int s = 0; s < steps; ++s) {
+        float h[kPiece];
+        take(s * 512 + (int)threadIdx.x, h);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) sum += h[i] * h[i];
+    }
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += part[i];
+    const float inv = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+    for (int s = 0; s < steps; ++s) {
+        const int p = s * 512 + (int)threadIdx.x;
+        float h[kPiece], g[kPiece];
+        take(p, h);
+        if (a.h) store_piece<T, VEC>(static_cast<T *>(a.h) + r * a.ldh, p * kPiece, a.cols, h);
+        load_weight(a, p * kPiece, g);
+        norm_out<FORM, T, VEC>(a, r, p, inv, h, g);
+    }
+}
+
+// Four pieces per thread, 256 apart, all loaded before the first is written.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const NormArgs a)
 {
     griddep_enter();
+    constexpr int U = 4;
     const long long total = a.rows * a.pieces;
-    const long long step = (long long)gridDim.x * 256;
     // pieces of a row are a multiple of 16, so a group's lanes stay together
-    for (long long i0 = (long long)blockIdx.x * 256; i0 < total; i0 += step) {
-        const long long i = i0 + threadIdx.x;
-        const bool live = i < total;
-        const long long r = live ? i / a.pieces : 0;
-        const int c = live ? (int)(i - r * a.pieces) * kPiece : 0;
-        float v[kPiece];
-        if (live) {
-            load_piece<T, VEC>(static_cast<const T *>(a.x) + r * a.ldx, c, a.cols, v);
-        } else {
+    for (long long i0 = (long long)blockIdx.x * (256 * U); i0 < total; i0 += (long long)gridDim.x * (256 * U)) {
+        const long long r0 = i0 / a.pieces;
+        const uint32_t p0 = (uint32_t)(i0 - r0 * a.pieces) + threadIdx.x;
+        Raw<T> x[U];
+        long long r[U];
+        int c[U];
+        bool live[U];
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) v[j] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            uint32_t p;
+            r[u] = r0 + fd_divmod(p0 + u * 256, a.per_row, &p);
+            c[u] = (int)p * kPiece;
+            live[u] = r[u] < a.rows;
+            if (live[u]) x[u] = load_raw<T, VEC>(static_cast<const T *>(a.x) + r[u] * a.ldx, c[u], a.cols);
+            else x[u] = Raw<T>{};
         }
-        store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r * a.ldo, a.scale, r, c, a.cols,
-                            a.col_blocks, live, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[kPiece];
+            unpack<T>(x[u], v);
+            store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r[u] * a.ldo, a.scale, r[u], c[u], a.cols, a.col_blocks,
+                                live[u], v);
+        }
     }
 }
 
-template <typename T, int FORM, bool VEC>
-cudaError_t launch_norm_form(const NormArgs &a, cudaStream_t s)
+template <typename T, int FORM, int TPR, int PPT, bool VEC>
+cudaError_t launch_norm_rows(const NormArgs &a, int sms, cudaStream_t s)
 {
-    const dim3 grid((unsigned)a.rows);
+    constexpr int THREADS = TPR < 128 ? 128 : TPR, ROWS = THREADS / TPR;
+    // one wave: 1024 threads per SM fit, whatever the registers
+    const long long most = (long long)sms * (1024 / THREADS), need = (a.rows + ROWS - 1) / ROWS;
+    return launch_pdl(rmsnorm_kernel<T, FORM, TPR, PPT, VEC>, dim3((unsigned)(need < most ? need : most)),
+                      dim3(THREADS), 0, s, a);
+}
+
+// The fewest threads whose two pieces each hold a row, one piece for the
+// shortest rows: 32 up to 512 columns, 1024 up to 16384.
+template <typename T, int FORM, bool VEC>
+cudaError_t launch_norm_form(const NormArgs &a, int sms, cudaStream_t s)
+{
     ProfScope prof("rmsnorm", s);
-    if (a.pieces <= 128) return launch_pdl(rmsnorm_kernel<T, FORM, 128, 1, VEC>, grid, dim3(128), 0, s, a);
-    if (a.pieces <= 256) return launch_pdl(rmsnorm_kernel<T, FORM, 256, 1, VEC>, grid, dim3(256), 0, s, a);
-    if (a.pieces <= 512) return launch_pdl(rmsnorm_kernel<T, FORM, 256, 2, VEC>, grid, dim3(256), 0, s, a);
-    if (a.pieces <= 1024) return launch_pdl(rmsnorm_kernel<T, FORM, 512, 2, VEC>, grid, dim3(512), 0, s, a);
-    if (a.pieces <= 2048) return launch_pdl(rmsnorm_kernel<T, FORM, 512, 4, VEC>, grid, dim3(512), 0, s, a);
-    return launch_pdl(rmsnorm_kernel<T, FORM, 512, 0, VEC>, grid, dim3(512), 0, s, a);
+    if (a.pieces <= 32) return launch_norm_rows<T, FORM, 32, 1, VEC>(a, sms, s);
+    if (a.pieces <= 64) return launch_norm_rows<T, FORM, 32, 2, VEC>(a, sms, s);
+    if (a.pieces <= 128) return launch_norm_rows<T, FORM, 128, 1, VEC>(a, sms, s);
+    if (a.pieces <= 256) return launch_norm_rows<T, FORM, 128, 2, VEC>(a, sms, s);
+    if (a.pieces <= 512) return launch_norm_rows<T, FORM, 256, 2, VEC>(a, sms, s);
+    if (a.pieces <= 1024) return launch_norm_rows<T, FORM, 512, 2, VEC>(a, sms, s);
+    if (a.pieces <= 2048) return launch_norm_rows<T, FORM, 1024, 2, VEC>(a, sms, s);
+    return launch_pdl(rmsnorm_long_kernel<T, FORM, VEC>, dim3((unsigned)a.rows), dim3(512), 0, s, a);
 }
 
 template <typename T>
-cudaError_t launch_norm_type(const NormArgs &a, int form, bool vec, cudaStream_t s)
+cudaError_t launch_norm_type(const NormArgs &a, int form, bool vec, int sms, cudaStream_t s)
 {
     switch (form) {
-    case OUT_SAME: return vec ? launch_norm_form<T, OUT_SAME, true>(a, s) : launch_norm_form<T, OUT_SAME, false>(a, s);
-    case OUT_F32: return vec ? launch_norm_form<T, OUT_F32, true>(a, s) : launch_norm_form<T, OUT_F32, false>(a, s);
-    default: return vec ? launch_norm_form<T, OUT_MX, true>(a, s) : launch_norm_form<T, OUT_MX, false>(a, s);
+    case OUT_SAME: return vec ? launch_norm_form<T, OUT_SAME, true>(a, sms, s) : launch_norm_form<T, OUT_SAME, false>(a, sms, s);
+    case OUT_F32: return vec ? launch_norm_form<T, OUT_F32, true>(a, sms, s) : launch_norm_form<T, OUT_F32, false>(a, sms, s);
+    default: return vec ? launch_norm_form<T, OUT_MX, true>(a, sms, s) : launch_norm_form<T, OUT_MX, false>(a, sms, s);
     }
 }
 
 template <typename T>
 cudaError_t launch_quantize_type(const NormArgs &a, bool vec, cudaStream_t s)
 {
-    const long long blocks = (a.rows * a.pieces + 255) / 256;
+    const long long blocks = (a.rows * a.pieces + 1023) / 1024;
     const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
     ProfScope prof("mx_quantize", s);
     return vec ? launch_pdl(mx_quantize_kernel<T, true>, grid, dim3(256), 0, s, a)
@@ -293,7 +425,8 @@ bigemm_status rmsnorm_run(int rows, int cols, bigemm_dtype in_dtype, const void 
     if (!aligned(x, 0, 1, es) || !aligned(residual, 0, 1, es) || !aligned(sum_out, 0, 1, es) ||
         !aligned(out, 0, 1, os) || !aligned(weight, 0, 1, 4) || !aligned(out_scale, 0, 1, 16))
         return BIGEMM_ERR_INVALID_ARG;
-    if (!device_state()) return BIGEMM_ERR_CUDA;
+    DeviceState *ds = device_state();
+    if (!ds) return BIGEMM_ERR_CUDA;
     NormArgs a = {};
     a.rows = rows;
     a.cols = cols;
@@ -302,14 +435,15 @@ bigemm_status rmsnorm_run(int rows, int cols, bigemm_dtype in_dtype, const void 
                                         : (int)(((long long)cols + kPiece - 1) / kPiece);
     a.ldx = ldx, a.ldr = ldr, a.ldh = lds, a.ldo = ldo;
     a.x = x, a.residual = residual, a.weight = weight, a.eps = eps;
+    a.vec_weight = weight && aligned(weight, 0, 1, 16);
     a.h = sum_out, a.out = out, a.scale = static_cast<uint8_t *>(out_scale);
     const bool vec = aligned(x, ldx, es, 16) && aligned(residual, ldr, es, 16) &&
                      aligned(sum_out, lds, es, 16) && aligned(out, ldo, os, 16);
     const int form = out_dtype == BIGEMM_MXF8 ? OUT_MX : out_dtype == in_dtype ? OUT_SAME : OUT_F32;
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = in_dtype == BIGEMM_F32   ? launch_norm_type<float>(a, form, vec, s)
-                          : in_dtype == BIGEMM_F16 ? launch_norm_type<__half>(a, form, vec, s)
-                                                   : launch_norm_type<__nv_bfloat16>(a, form, vec, s);
+    const cudaError_t e = in_dtype == BIGEMM_F32   ? launch_norm_type<float>(a, form, vec, ds->sm_count, s)
+                          : in_dtype == BIGEMM_F16 ? launch_norm_type<__half>(a, form, vec, ds->sm_count, s)
+                                                   : launch_norm_type<__nv_bfloat16>(a, form, vec, ds->sm_count, s);
     return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
 }
 
@@ -329,6 +463,7 @@ bigemm_status mx_quantize_run(int rows, int cols, bigemm_dtype in_dtype, const v
     a.cols = cols;
     a.col_blocks = (int)(((long long)cols + kMxBlock - 1) / kMxBlock);
     a.pieces = a.col_blocks * (kMxBlock / kPiece);
+    a.per_row = make_fastdiv((uint32_t)a.pieces);
     a.ldx = ldx, a.ldo = ldo, a.x = x, a.out = out, a.scale = static_cast<uint8_t *>(scale);
     const bool vec = aligned(x, ldx, es, 16) && aligned(out, ldo, 1, 8);
     const cudaStream_t s = (cudaStream_t)stream;
