@@ -20,37 +20,42 @@ constexpr int kMxGroup = 32;        // elements per scale
 constexpr int kMxBlock = 128;       // rows, and columns, per block of scales
 constexpr int kMxBlockBytes = 512;
 
-// Byte offset of the scale of (row, group) in a matrix with col_blocks blocks
-// per block row.
+// Byte offset of a row's first scale in a matrix with col_blocks blocks per
+// block row; the row's further blocks follow kMxBlockBytes apart.
+__device__ __forceinline__ long long mx_scale_row(long long row, int col_blocks)
+{
+    const int r = (int)row;
+    return (row >> 7) * col_blocks * kMxBlockBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
 __device__ __forceinline__ long long mx_scale_offset(long long row, int group, int col_blocks)
 {
-    const int r = (int)(row & 127);
-    return ((row >> 7) * col_blocks + (group >> 2)) * kMxBlockBytes + (r & 31) * 16 + (r >> 5) * 4 +
-           (group & 3);
+    return mx_scale_row(row, col_blocks) + (long long)(group >> 2) * kMxBlockBytes + (group & 3);
 }
 
 // The scale's code from a group's largest magnitude: its exponent less 8, one
-// more where the fraction exceeds 448's (1.75); at least 0 (2^-127).
+// more where the fraction exceeds 448's (1.75, fraction bits 0x600000: adding
+// 0x1fffff then carries into the exponent); at least 0 (2^-127).
 __device__ __forceinline__ uint32_t mx_scale_code(float amax)
 {
-    const uint32_t b = __float_as_uint(amax) & 0x7fffffffu;
-    if (b >= 0x7f800000u) return 255u;
-    const int code = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return (uint32_t)max(code, 0);
+    const uint32_t b = __float_as_uint(amax);
+    const int code = max((int)((b + 0x1fffffu) >> 23) - 8, 0);
+    return b >= 0x7f800000u ? 255u : (uint32_t)code;
 }
 
-// 1 / s = 2^(127 - code), exact (codes of finite groups are at most 247).
+// 1 / s = 2^(127 - code), exact (codes of finite groups are at most 248); NaN
+// for 255.
 __device__ __forceinline__ float mx_inv_scale(uint32_t code)
 {
-    if (code >= 255u) return __uint_as_float(0x7fffffffu);
-    return __uint_as_float(code >= 254u ? 0x00400000u : (254u - code) << 23);
+    return __uint_as_float(code == 255u ? 0x7fffffffu : (254u - code) << 23);
 }
 
 // The largest magnitude of two values, NaN if either is.
 __device__ __forceinline__ float mx_amax(float a, float b)
 {
-    const uint32_t x = __float_as_uint(a) & 0x7fffffffu, y = __float_as_uint(b) & 0x7fffffffu;
-    return __uint_as_float(max(x, y));
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return m;
 }
 
 // Four floats, already divided by the scale, as e4m3 (nearest even), the first

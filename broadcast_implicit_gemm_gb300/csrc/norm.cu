@@ -115,26 +115,24 @@ __device__ __forceinline__ void store_piece(T *row, int c, int cols, const float
 }
 
 // One piece of an MXFP8 row: every lane of the warp takes part, `live` lanes
-// hold a piece inside the row padded to whole blocks of scales.  VEC: the e4m3
-// piece starts on an 8-byte boundary.
+// hold a piece inside the row padded to whole blocks of scales.  scale: of the
+// row.  VEC: the e4m3 piece starts on an 8-byte boundary.
 template <bool VEC>
-__device__ __forceinline__ void store_mx_piece(uint8_t *row, uint8_t *scale, long long r, int c,
-                                               int cols, int col_blocks, bool live,
+__device__ __forceinline__ void store_mx_piece(uint8_t *row, uint8_t *scale, int c, int cols, bool live,
                                                const float (&v)[kPiece])
 {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) a = mx_amax(a, v[i]);
-    a = mx_amax(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = mx_amax(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const uint32_t code = mx_scale_code(a);
+    float top = mx_amax(mx_amax(mx_amax(v[0], v[1]), mx_amax(v[2], v[3])),
+                        mx_amax(mx_amax(v[4], v[5]), mx_amax(v[6], v[7])));
+    top = mx_amax(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = mx_amax(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t code = mx_scale_code(top);
     // the four codes of a block of scales leave as one word
     uint32_t word = code << (8 * ((threadIdx.x >> 2) & 3));
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
     if (!live) return;
     if ((threadIdx.x & 15) == 0)
-        *reinterpret_cast<uint32_t *>(scale + mx_scale_offset(r, c / kMxGroup, col_blocks)) = word;
+        *reinterpret_cast<uint32_t *>(scale + (long long)(c / kMxBlock) * kMxBlockBytes) = word;
     const float inv = mx_inv_scale(code);
     const uint32_t lo = mx_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     const uint32_t hi = mx_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
@@ -149,7 +147,6 @@ __device__ __forceinline__ void store_mx_piece(uint8_t *row, uint8_t *scale, lon
 
 struct NormArgs {
     int cols, col_blocks, pieces;     // pieces: of a row, padded to whole blocks of scales for MXFP8
-    FastDiv per_row;                  // by pieces
     long long rows, ldx, ldr, ldh, ldo;
     const void *x, *residual;
     const float *weight;
@@ -177,7 +174,7 @@ __device__ __forceinline__ void norm_out(const NormArgs &a, long long r, int p, 
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) y[i] = c + i < a.cols ? h[i] * inv * g[i] : 0.f;
     if (FORM == OUT_MX)
-        store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r * a.ldo, a.scale, r, c, a.cols, a.col_blocks,
+        store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r * a.ldo, a.scale + mx_scale_row(r, a.col_blocks), c, a.cols,
                             p < a.pieces, y);
     else if (FORM == OUT_F32)
         store_piece<float, VEC>(static_cast<float *>(a.out) + r * a.ldo, c, a.cols, y);
@@ -312,37 +309,35 @@ __global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
     }
 }
 
-// Four pieces per thread, 256 apart, all loaded before the first is written.
+// A warp takes a run of 1024 columns of a row: four pieces per lane, all loaded
+// before the first is written.  The runs of all rows are numbered one after the
+// other, eight to a block.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const NormArgs a)
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const NormArgs a, int runs, FastDiv by_runs)
 {
     griddep_enter();
     constexpr int U = 4;
-    const long long total = a.rows * a.pieces;
-    // pieces of a row are a multiple of 16, so a group's lanes stay together
-    for (long long i0 = (long long)blockIdx.x * (256 * U); i0 < total; i0 += (long long)gridDim.x * (256 * U)) {
-        const long long r0 = i0 / a.pieces;
-        const uint32_t p0 = (uint32_t)(i0 - r0 * a.pieces) + threadIdx.x;
-        Raw<T> x[U];
-        long long r[U];
-        int c[U];
-        bool live[U];
+    const int lane = threadIdx.x & 31;
+    // work items are (row, run); the block's first row in 64 bits, the rest from there
+    const long long first = (long long)blockIdx.x * 8, r0 = first / runs;
+    uint32_t run;
+    const long long r = r0 + fd_divmod((uint32_t)(first - r0 * runs) + (threadIdx.x >> 5), by_runs, &run);
+    if (r >= a.rows) return;
+    const T *row = static_cast<const T *>(a.x) + r * a.ldx;
+    const int p0 = (int)run * 32 * U + lane;
+    Raw<T> x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            uint32_t p;
-            r[u] = r0 + fd_divmod(p0 + u * 256, a.per_row, &p);
-            c[u] = (int)p * kPiece;
-            live[u] = r[u] < a.rows;
-            if (live[u]) x[u] = load_raw<T, VEC>(static_cast<const T *>(a.x) + r[u] * a.ldx, c[u], a.cols);
-            else x[u] = Raw<T>{};
-        }
+    for (int u = 0; u < U; ++u)
+        if (p0 + u * 32 < a.pieces) x[u] = load_raw<T, VEC>(row, (p0 + u * 32) * kPiece, a.cols);
+    uint8_t *out = static_cast<uint8_t *>(a.out) + r * a.ldo, *scale = a.scale + mx_scale_row(r, a.col_blocks);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[kPiece];
-            unpack<T>(x[u], v);
-            store_mx_piece<VEC>(static_cast<uint8_t *>(a.out) + r[u] * a.ldo, a.scale, r[u], c[u], a.cols, a.col_blocks,
-                                live[u], v);
-        }
+    for (int u = 0; u < U; ++u) {
+        const int p = p0 + u * 32;
+        if (p - lane >= a.pieces) return;     // the whole warp is past the row
+        float v[kPiece];
+        if (p >= a.pieces) x[u] = Raw<T>{};
+        unpack<T>(x[u], v);
+        store_mx_piece<VEC>(out, scale, p * kPiece, a.cols, p < a.pieces, v);
     }
 }
 
@@ -385,11 +380,14 @@ cudaError_t launch_norm_type(const NormArgs &a, int form, bool vec, int sms, cud
 template <typename T>
 cudaError_t launch_quantize_type(const NormArgs &a, bool vec, cudaStream_t s)
 {
-    const long long blocks = (a.rows * a.pieces + 1023) / 1024;
-    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+    const int runs = (a.pieces + 127) / 128;
+    const long long blocks = (a.rows * runs + 7) / 8;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const FastDiv by = make_fastdiv((uint32_t)runs);
+    const dim3 grid((unsigned)blocks);
     ProfScope prof("mx_quantize", s);
-    return vec ? launch_pdl(mx_quantize_kernel<T, true>, grid, dim3(256), 0, s, a)
-               : launch_pdl(mx_quantize_kernel<T, false>, grid, dim3(256), 0, s, a);
+    return vec ? launch_pdl(mx_quantize_kernel<T, true>, grid, dim3(256), 0, s, a, runs, by)
+               : launch_pdl(mx_quantize_kernel<T, false>, grid, dim3(256), 0, s, a, runs, by);
 }
 
 // Whether rows of `ld` elements of `size` bytes start on `to`-byte boundaries.
@@ -463,7 +461,6 @@ bigemm_status mx_quantize_run(int rows, int cols, bigemm_dtype in_dtype, const v
     a.cols = cols;
     a.col_blocks = (int)(((long long)cols + kMxBlock - 1) / kMxBlock);
     a.pieces = a.col_blocks * (kMxBlock / kPiece);
-    a.per_row = make_fastdiv((uint32_t)a.pieces);
     a.ldx = ldx, a.ldo = ldo, a.x = x, a.out = out, a.scale = static_cast<uint8_t *>(scale);
     const bool vec = aligned(x, ldx, es, 16) && aligned(out, ldo, 1, 8);
     const cudaStream_t s = (cudaStream_t)stream;
