@@ -69,6 +69,7 @@ FewCut choose_few(const MatmulArgs &a, int sms)
     const int s = (int)std::max<long long>(1, want);
     const int per = (a.k_blocks + s - 1) / s;
     c.split = (a.k_blocks + per - 1) / per;
+    c.alone = tiles * c.split <= sms;
     return c;
 }
 

@@ -28,6 +28,7 @@ struct MatmulArgs {
     int k_blocks;                    // 128-byte pieces of a row
     int seg_blocks;                  // of them, how many one tensor-memory accumulator sums
     int kb_per;                      // few tokens: of them, how many one CTA of a split takes
+    int stages;                      // few tokens: of shared memory
     int m_tiles, n_tiles;            // many tokens: tiles of the output, 256 tokens by BN channels
     bool by_rows;                    // many tokens: out and other have their rows on the 16-byte grid
     unsigned long long timeout_ns;
@@ -306,23 +307,24 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
                  : "memory");
 }
 
-// Shared memory of CTA `rank` of the cluster (address from mapa_shared).
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+// A store into shared memory of a CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+
+// The two halves of a barrier over all threads of the cluster.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 }  // namespace
 
 // The kernel for few tokens (matmul_few.cu).  How a product is cut: tokens per
-// tile (16, 32, 64 or 128) and CTAs that share one tile's K.
+// tile (16, 32, 64 or 128), CTAs that share one tile's K, and whether each has
+// an SM to itself.
 struct FewCut {
     int bn, split;
+    bool alone;
 };
 cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
                               const CUtensorMap &map_x, cudaStream_t stream);

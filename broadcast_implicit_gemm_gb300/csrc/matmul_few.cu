@@ -6,8 +6,11 @@
 // traffic.  Such a product is bound by the weights' bytes; one CTA per 128
 // channels would leave most SMs without any, so `split` CTAs take a slice of K
 // each, and as a cluster add up their fp32 partial sums through distributed
-// shared memory: in rank order, so that the result does not depend on timing,
-// without a workspace and without a second launch.
+// shared memory: each rank sends every other one its sums of the tokens which
+// that one finishes, and adds what it got in rank order, so that the result
+// does not depend on timing, without a workspace and without a second launch.
+// (Sent, not fetched: a fetch waits for each answer, and holds its owner in a
+// second barrier; 4096 x 4096 for one token 8.1 -> @ us.)
 //
 // GATHER: rows that TMA cannot address (a stride or base off the 16-byte grid)
 // are brought into the same swizzled stages by six more warps with plain loads.
@@ -30,21 +33,32 @@ constexpr int kFewThreads = 256;               // producer, MMA, two idle warps,
 constexpr int kGatherWarps = 6;
 constexpr int kFewA = 128 * kRow;              // bytes of weights per stage
 
+constexpr int kFewStages = 8;                  // at most
+// A CTA asks for 110 KB, so that two share an SM and no third kernel that
+// allocates tensor memory fits beside them (a cluster whose CTAs could wait for
+// tensor memory held by another cluster's would not end), or, where the whole
+// grid has an SM per CTA and tiles are large, for most of an SM.
+constexpr int kFewShared = 110 * 1024;
+
 template <int BN>
 struct FewCfg {
-    // 110 KB, so that two CTAs share an SM and no third kernel that
-    // allocates tensor memory fits beside them: a cluster whose CTAs could wait
-    // for tensor memory held by another cluster's would not end
     static constexpr int stage = kFewA + BN * kRow + 2 * kMxBlockBytes;
-    static constexpr int stages = BN == 128 ? 3 : BN == 64 ? 4 : 5;
-    static constexpr int smem = 110 * 1024;
-    static_assert(stages * stage + 256 <= 109 * 1024 && BN * 512 <= stages * stage, "fits");
+    static constexpr int half = BN == 128 ? 3 : BN == 64 ? 4 : BN == 32 ? 4 : 5;   // stages in half an SM
+    static constexpr int whole = BN == 128 ? 6 : BN == 64 ? 8 : half;              // stages of a CTA alone
+    // the sums that a rank gets: at most 7 tokens more than a tile has, since the ranks' shares are
+    // rounded up.  Beside the stages for small tiles, over them for large ones.
+    static constexpr int sums = (BN + 7) * 512;
+    static constexpr bool beside = BN <= 32;
+    static constexpr int bytes(int stages) { return stages * stage + (beside ? sums : 0) + 256 + 1024; }
+    static constexpr int smem(int stages) { return bytes(stages) > kFewShared ? bytes(stages) : kFewShared; }
+    static_assert(bytes(half) <= kFewShared && (beside || sums <= half * stage), "fits");
+    static_assert(whole <= kFewStages && bytes(whole) <= 227 * 1024, "fits");
 };
 
 template <int BN, bool MX, bool FULL>
 constexpr uint32_t few_cols()
 {
-    const int n = (FULL ? 2 : 1) * BN + (MX ? 8 * FewCfg<BN>::stages : 0);
+    const int n = (FULL ? 2 : 1) * BN + (MX ? 8 * FewCfg<BN>::whole : 0);
     return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
@@ -74,10 +88,10 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
                       const MatmulArgs p)
 {
     using C = FewCfg<BN>;
-    constexpr int S = C::stages;
+    const int S = p.stages;
     constexpr int ACC = FULL ? 2 : 1;
     constexpr uint32_t kCols = few_cols<BN, MX, FULL>();
-    static_assert(ACC * BN + (MX ? 8 * S : 0) <= (int)kCols, "tensor memory");
+    static_assert(ACC * BN + (MX ? 8 * C::whole : 0) <= (int)kCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sa = smem, *sb = smem + S * kFewA, *ss = sb + S * BN * kRow;   // weights, tokens, scales
@@ -85,7 +99,8 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
     uint64_t *empty = full + S, *tfull = empty + S, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    float *part = reinterpret_cast<float *>(smem);   // [BN][128] sums, over the stages once they are done
+    // [split][tokens of a rank][128] sums
+    float *part = reinterpret_cast<float *>(C::beside ? ss + S * 2 * kMxBlockBytes + 256 : smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = (int)((p.k_blocks + p.kb_per - 1) / p.kb_per);   // CTAs of the cluster
@@ -118,6 +133,7 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    if (C::beside && split > 1) cluster_arrive();   // this CTA runs: peers may write into its sums
     griddep_enter();
 
     bool good = true;
@@ -131,9 +147,9 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
         // ------------------------------------------------------ producers
         const int esize = MX ? 1 : 2, per = kRow / esize;      // elements per stage row
         int stage = 0;
-        uint32_t phase = 0, last_parity[S];
-        bool issued[S];
-        for (int i = 0; i < S; ++i) issued[i] = false, last_parity[i] = 0;
+        uint32_t phase = 0, last_parity[kFewStages];
+        bool issued[kFewStages];
+        for (int i = 0; i < kFewStages; ++i) issued[i] = false, last_parity[i] = 0;
         for (int kb = kb0; good && kb < kb1; ++kb) {
             uint8_t *a_dst = sa + stage * kFewA, *b_dst = sb + stage * BN * kRow;
             uint8_t *s_dst = ss + stage * 2 * kMxBlockBytes;
@@ -240,33 +256,20 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------ drain: lane = channel, column = token
-        const int q = warp & 3;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
-        float *dst = part + q * 32 + lane;
+        const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
         int a = 0;
         uint32_t acc_phase = 0;
         for (int k0 = kb0; good && k0 < kb1; k0 += p.seg_blocks) {
             good = mbar_wait_warp(&tfull[a], acc_phase, p.timeout_ns, abort_flag, p.err);
-            if (!good) break;
+            if (!good || !FULL) break;           // one segment: its sums stay in tensor memory for now
             tc_fence_after();
-            const bool last = k0 + p.seg_blocks >= kb1;
 #pragma unroll
             for (int c = 0; c < BN; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(lane_base + (uint32_t)(a * BN + c), r);
                 tmem_wait_ld16(r);
-                if (FULL) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[(FULL ? c : 0) + (FULL ? i : 0)] += __uint_as_float(r[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) dst[(c + i) * 128] = __uint_as_float(r[i]);
-                }
-            }
-            if (FULL && last) {
-                // the last segment's accumulator is full, so every stage has been read
-#pragma unroll
-                for (int i = 0; i < BN; ++i) dst[i * 128] = acc[FULL ? i : 0];
+                for (int i = 0; i < 16; ++i) acc[FULL ? c + i : 0] += __uint_as_float(r[i]);
             }
             tc_fence_before();
             __syncwarp();
@@ -274,39 +277,71 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
             if (++a == ACC) a = 0, acc_phase ^= 1u;
         }
     }
+    __syncwarp();
 
-    tc_fence_before();
+    // ---------------------------------------------------------- each token's sums to the rank that finishes it
+    const int tokens = min(BN, p.M - m0);
+    const int per_rank = split > 1 ? (tokens + split - 1) / split : tokens;
     if (split > 1) {
-        __syncwarp();
-        cluster_sync_all();
+        // the sums' memory is free: beside the stages since each peer began, over them since its
+        // drain warps saw the last MMA done
+        if (!C::beside) cluster_arrive();
+        cluster_wait();
+    }
+    if (warp >= 4 && warp < 8) {
+        tc_fence_after();
+        const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+        // slot of this rank in the owner's memory
+        const uint32_t at = smem_u32(part + rank * per_rank * 128 + (warp & 3) * 32 + lane);
+        uint32_t to = split > 1 ? mapa_shared(at, 0u) : at;
+        int owner = 0, t = 0;
+#pragma unroll
+        for (int c = 0; c < BN; c += 16) {
+            if (c >= tokens) break;
+            uint32_t r[16];
+            if (!FULL) {
+                tmem_ld_32x32b_x16(lane_base + (uint32_t)c, r);
+                tmem_wait_ld16(r);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (c + i < tokens) {
+                    const float v = FULL ? acc[FULL ? c + i : 0] : __uint_as_float(r[i]);
+                    if (split > 1) st_cluster_f32(to + (uint32_t)t * 512u, v);
+                    else part[(c + i) * 128 + (warp & 3) * 32 + lane] = v;
+                    if (split > 1 && ++t == per_rank) {
+                        t = 0;
+                        to = mapa_shared(at, (uint32_t)min(++owner, split - 1));
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (split > 1) {
+        cluster_arrive();
+        cluster_wait();
     } else {
         __syncthreads();
     }
-    tc_fence_after();
 
     // ---------------------------------------------------------- sum over the ranks and epilogue
-    // pieces of 8 channels, 16 to a token; a rank takes a run of whole tokens
-    const int tokens = min(BN, p.M - m0);
-    const int per_rank = (tokens + split - 1) / split;
-    const int t0 = rank * per_rank, t1 = min(tokens, t0 + per_rank);
-    for (int i0 = t0 * 16; i0 < t1 * 16; i0 += few_threads<GATHER>()) {
+    // pieces of 8 channels, 16 to a token
+    const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
+    for (int i0 = 0; i0 < mine * 16; i0 += few_threads<GATHER>()) {
         const int i = i0 + (int)threadIdx.x;
-        const bool live = i < t1 * 16;
-        const int t = live ? i >> 4 : t0, c = (i & 15) * 8;
+        const bool live = i < mine * 16;
+        const int t = t0 + (live ? i >> 4 : 0), c = (i & 15) * 8;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
         if (live) {
-            const uint32_t at = smem_u32(part + t * 128 + c);
+            const float4 *from = reinterpret_cast<const float4 *>(part + (i >> 4) * 128 + c);
+#pragma unroll 4
             for (int s = 0; s < split; ++s) {
-                float4 u0, u1;
-                if (split > 1) {
-                    const uint32_t peer = mapa_shared(at, (uint32_t)s);
-                    u0 = ld_cluster_f4(peer), u1 = ld_cluster_f4(peer + 16);
-                } else {
-                    u0 = *reinterpret_cast<const float4 *>(part + t * 128 + c);
-                    u1 = *reinterpret_cast<const float4 *>(part + t * 128 + c + 4);
-                }
+                const float4 u0 = from[0], u1 = from[1];
+                from += per_rank * 32;
                 v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
                 v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
             }
@@ -329,33 +364,32 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
         }
     }
 
-    if (split > 1) {
-        __syncwarp();
-        cluster_sync_all();   // no CTA leaves while a peer may still read its sums
-    }
     if (warp == 1) {
+        tc_fence_after();
         __syncwarp();
         tmem_dealloc(tmem_base, kCols);
     }
 }
 
 template <int BN, bool MX, bool GATHER, bool FULL>
-cudaError_t launch_one(const MatmulArgs &a, int split, const CUtensorMap &mw, const CUtensorMap &mx,
+cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
                        cudaStream_t stream)
 {
+    a.stages = alone ? FewCfg<BN>::whole : FewCfg<BN>::half;
     auto kern = matmul_few_kernel<BN, MX, GATHER, FULL>;
     static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<BN>::smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   FewCfg<BN>::smem(FewCfg<BN>::whole));
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set |= 1ull << dev;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.N + 127ll) / 128 * split), (unsigned)((a.M + (long long)BN - 1) / BN));
     cfg.blockDim = dim3(few_threads<GATHER>());
-    cfg.dynamicSmemBytes = FewCfg<BN>::smem;
+    cfg.dynamicSmemBytes = FewCfg<BN>::smem(a.stages);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -370,24 +404,24 @@ cudaError_t launch_one(const MatmulArgs &a, int split, const CUtensorMap &mw, co
 }
 
 template <int BN>
-cudaError_t launch_bn(const MatmulArgs &a, int split, bool gather, const CUtensorMap &mw, const CUtensorMap &mx,
+cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, bool gather, const CUtensorMap &mw, const CUtensorMap &mx,
                       cudaStream_t s)
 {
     if (a.out_dt == BIGEMM_F32) {
         if constexpr (BN <= 64) {
             if (a.in_dt == BIGEMM_MXF8)
-                return gather ? launch_one<BN, true, true, true>(a, split, mw, mx, s)
-                              : launch_one<BN, true, false, true>(a, split, mw, mx, s);
-            return gather ? launch_one<BN, false, true, true>(a, split, mw, mx, s)
-                          : launch_one<BN, false, false, true>(a, split, mw, mx, s);
+                return gather ? launch_one<BN, true, true, true>(a, split, alone, mw, mx, s)
+                              : launch_one<BN, true, false, true>(a, split, alone, mw, mx, s);
+            return gather ? launch_one<BN, false, true, true>(a, split, alone, mw, mx, s)
+                          : launch_one<BN, false, false, true>(a, split, alone, mw, mx, s);
         }
         return cudaErrorInvalidValue;   // 128 running sums per thread would spill
     }
     if (a.in_dt == BIGEMM_MXF8)
-        return gather ? launch_one<BN, true, true, false>(a, split, mw, mx, s)
-                      : launch_one<BN, true, false, false>(a, split, mw, mx, s);
-    return gather ? launch_one<BN, false, true, false>(a, split, mw, mx, s)
-                  : launch_one<BN, false, false, false>(a, split, mw, mx, s);
+        return gather ? launch_one<BN, true, true, false>(a, split, alone, mw, mx, s)
+                      : launch_one<BN, true, false, false>(a, split, alone, mw, mx, s);
+    return gather ? launch_one<BN, false, true, false>(a, split, alone, mw, mx, s)
+                  : launch_one<BN, false, false, false>(a, split, alone, mw, mx, s);
 }
 
 }  // namespace
@@ -397,10 +431,10 @@ cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, cons
 {
     ProfScope prof("matmul_few", stream);
     switch (cut.bn) {
-    case 16: return launch_bn<16>(a, cut.split, gather, map_w, map_x, stream);
-    case 32: return launch_bn<32>(a, cut.split, gather, map_w, map_x, stream);
-    case 64: return launch_bn<64>(a, cut.split, gather, map_w, map_x, stream);
-    case 128: return launch_bn<128>(a, cut.split, gather, map_w, map_x, stream);
+    case 16: return launch_bn<16>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
+    case 32: return launch_bn<32>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
+    case 64: return launch_bn<64>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
+    case 128: return launch_bn<128>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
     default: return cudaErrorInvalidValue;
     }
 }
