@@ -85,8 +85,9 @@ int choose_many(const MatmulArgs &a, int sms)
 
 constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bits
 
-// Elements of K that one tensor-memory accumulator sums for a 32-bit output.
-constexpr int kFullSegment = 1024;
+// 128-byte pieces of a row that one tensor-memory accumulator sums for a 32-bit
+// output: 64 additions, of 16 products each in 16 bits and of 32 in 8.
+constexpr int kFullSegment = 16;
 
 bigemm_status product(MatmulArgs &a, void *stream)
 {
@@ -121,7 +122,7 @@ bigemm_status product(MatmulArgs &a, void *stream)
     const long long far = 1ll << 40;
     const bool gather = !on_grid(a.x, a.ldx, es, 16) || !on_grid(a.w, a.ldw, es, 16) || a.ldx * es >= far ||
                         a.ldw * es >= far;
-    a.seg_blocks = a.out_dt == BIGEMM_F32 ? (int)(kFullSegment * es / kRow) : a.k_blocks;
+    a.seg_blocks = a.out_dt == BIGEMM_F32 ? kFullSegment : a.k_blocks;
     if (!gather && a.M > 128) {
         const int bn = choose_many(a, ds->sm_count);
         const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, nt = (a.N + bn - 1ll) / bn;

@@ -15,7 +15,7 @@
 // stage), so there is one accumulator; the drain warps take all of it to
 // registers, hand it back, and go on from there.
 //
-// FULL: a 32-bit output, sums of at most 1024 elements added up in registers
+// FULL: a 32-bit output, sums of at most 64 MMAs' depth added up in registers
 // (matmul_few.cu says why).
 #include "matmul.cuh"
 
@@ -393,7 +393,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = lane_base + (uint32_t)(a * BN);
-                if constexpr (KEEP) {
+                if constexpr (KEEP && !FULL) {
+                    uint32_t r[UNITS][32];
+#pragma unroll
+                    for (int u = 0; u < UNITS; ++u) tmem_ld_32x32b_x32(base + u * 32, r[u]);
+#pragma unroll
+                    for (int u = 0; u < UNITS; ++u) {
+                        tmem_wait_ld32(r[u]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) keep[u][i] = __uint_as_float(r[u][i]);
+                    }
+                } else if constexpr (KEEP) {
 #pragma unroll
                     for (int u = 0; u < UNITS; ++u) {
                         uint32_t r[32];

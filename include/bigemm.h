@@ -322,7 +322,8 @@ typedef enum {
  *   other [M,N] of other_dtype (F32, F16, BF16), read unless combine is NONE; it
  *   may be out itself (same type and rows)
  *   out [M,N] of out_dtype (F32, F16, BF16), rounded once.  For F32 at most 1024
- *   products at a time are summed in the tensor core, the rest in fp32 adds.
+ *   products at a time (2048 of MXF8) are summed in the tensor core, the rest in
+ *   fp32 adds.
  * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum),
  * UNSUPPORTED (in_dtype F32; N or K above 2^30, more than 4 million tokens), CUDA.
  */
