@@ -56,38 +56,87 @@ bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows, long l
     return encode_tiled(map, t, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Tokens per tile: the smallest that holds them all (each tile reads the
-// weights again), at most 64 for a 32-bit output, whose running sums are in
-// registers.  K is shared among CTAs until two per SM are busy, as long as each
-// keeps four stages.
-FewCut choose_few(const MatmulArgs &a, int sms)
+// Which kernel, and how it is cut.  The estimates are in hundredths of a
+// microsecond, from sizes measured with 16-bit operands; a block (128 bytes) of
+// K takes 1.3 to 1.4 times as long with MXFP8 ones, in every form alike.
+struct Choice {
+    bool many;
+    int bn;          // many tokens: channels per tile
+    FewCut few;
+};
+
+long long up(long long a, long long b) { return (a + b - 1) / b; }
+
+// Few tokens: tiles of the fewest tokens that hold them all (each tile reads the
+// weights again), K shared by as many CTAs as fit beside each other, two per SM
+// for small tiles, one for large ones, up to the cluster's eight, as long as
+// each keeps four blocks.
+//   64 x 4096 x 4096: 23.3 us with K whole, 15.2 in 2, 11.5 in 4 (128 CTAs), 14.5 in 8
+//   1 x 4096 x 4096: 19.2, 12.1, 8.5 and 8.1 us
+FewCut cut_few(const MatmulArgs &a, int sms, int bn, bool alone)
 {
+    const long long tiles = up(a.N, 128) * up(a.M, bn), room = (alone ? 1 : 2) * (long long)sms;
+    const long long most = std::min<long long>(a.k_blocks / 4, room / tiles);
     FewCut c;
-    c.bn = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || a.out_dt == BIGEMM_F32 ? 64 : 128;
-    const long long tiles = ((a.N + 127ll) / 128) * ((a.M + (long long)c.bn - 1) / c.bn);
-    const long long want = std::min<long long>(std::min<long long>(8, a.k_blocks / 4), 2ll * sms / tiles);
-    const int s = (int)std::max<long long>(1, want);
-    const int per = (a.k_blocks + s - 1) / s;
-    c.split = (a.k_blocks + per - 1) / per;
-    c.alone = tiles * c.split <= sms;
+    c.bn = bn;
+    // clusters of 5 to 7 leave SMs of their processor cluster idle (300 x 1000 x 2048: 13.6 us in 7, 8.9 in 4)
+    c.split = most >= 8 ? 8 : most >= 4 ? 4 : most >= 1 ? (int)most : 1;
+    c.alone = alone && tiles * c.split <= sms;
     return c;
 }
 
-// Channels per tile of the pair kernel: the width whose waves of tiles over the
-// SM pairs take less time, 128 if they are not more than 256's.
-int choose_many(const MatmulArgs &a, int sms)
+// A wave of it: a start and an end of 5.7 us, and per block of K 0.33 us for a
+// CTA alone on its SM with 128 tokens, 0.37 for two with 64 each, 0.52 for two
+// with 128.
+long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 {
-    const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, pairs = sms / 2;
-    const long long wide = (mt * ((a.N + 255ll) / 256) + pairs - 1) / pairs * 256;
-    const long long narrow = (mt * ((a.N + 127ll) / 128) + pairs - 1) / pairs * 128;
-    return 14 * narrow < 10 * wide ? 128 : 256;
+    const long long grid = up(a.N, 128) * up(a.M, c.bn) * c.split, per = up(a.k_blocks, c.split);
+    // rows off the 16-byte grid leave element by element: 0.15 us a token (777 x 5001 x 1000: 34 us against 22 in pairs)
+    const int ragged = a.vec_out && (a.combine == BIGEMM_COMBINE_NONE || a.vec_other) ? 0 : 15 * c.bn;
+    return ragged + (c.alone ? 600 + 33 * per : up(grid, 2ll * sms) * (570 + (c.bn == 128 ? 52 : 37) * per));
+}
+
+// The pair kernel: 3.5 us, and per wave of tiles over the SM pairs and block of
+// K 0.33 us at 256 channels, 0.26 at 128 (where shared memory, not the tensor
+// core, sets the pace).
+long long many_cost(const MatmulArgs &a, int sms, int bn)
+{
+    const long long waves = up(up(a.M, kManyTokens) * up(a.N, bn), sms / 2);
+    return 350 + waves * a.k_blocks * (bn == 256 ? 33 : 26);
+}
+
+// Up to 128 tokens one tile of tokens is enough, and the few-token kernel has
+// no rival: 128 x 4096 x 4096 13 us against 20.  Above, the least estimate:
+// 256 x 4096 x 4096 17.7 us (64 tokens, K in 2) against 20.4 and 24.4 in pairs,
+// 512 x 4096 x 4096 25 against 20.9 and 24.7, 1024 x 1024 x 8192 25.5 against
+// 34.5 and 40.9.
+Choice choose(const MatmulArgs &a, int sms, bool gather)
+{
+    const bool full = a.out_dt == BIGEMM_F32;      // its running sums are in registers: at most 64 tokens
+    Choice c = {};
+    if (a.M <= 128) {
+        c.few = cut_few(a, sms, a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || full ? 64 : 128, a.M > 32);
+        return c;
+    }
+    c.few = cut_few(a, sms, 64, false);
+    long long least = few_cost(a, sms, c.few);
+    if (!full) {
+        const FewCut large = cut_few(a, sms, 128, true);
+        if (gather || few_cost(a, sms, large) < least) c.few = large, least = few_cost(a, sms, large);
+    }
+    for (int bn = 128; bn <= 256 && !gather; bn += 128) {
+        const long long cost = many_cost(a, sms, bn);
+        if (cost < least) c.many = true, c.bn = bn, least = cost;
+    }
+    return c;
 }
 
 constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bits
 
 // 128-byte pieces of a row that one tensor-memory accumulator sums for a 32-bit
-// output: 64 additions, of 16 products each in 16 bits and of 32 in 8.
-constexpr int kFullSegment = 16;
+// output: 512 products of 16-bit operands (32 additions), 2048 of MXFP8 ones
+// (64; they have one accumulator, and each hand-over costs 1 us).
+int full_segment(bool mx) { return mx ? 16 : 8; }
 
 bigemm_status product(MatmulArgs &a, void *stream)
 {
@@ -114,6 +163,7 @@ bigemm_status product(MatmulArgs &a, void *stream)
     DeviceState *ds = device_state();
     if (!ds) return BIGEMM_ERR_CUDA;
     a.vec_out = on_grid(a.out, a.ldo, os, a.out_dt == BIGEMM_MXF8 ? 8 : 16);
+    a.vec_bias = on_grid(a.bias, 0, 1, 16);
     a.k_blocks = (int)((a.K * es + kRow - 1) / kRow);
     if (a.M == 1) a.ldx = (a.ldx + 15) / 16 * 16;   // the stride of a single row is free
     a.timeout_ns = wait_timeout_ns();
@@ -122,9 +172,10 @@ bigemm_status product(MatmulArgs &a, void *stream)
     const long long far = 1ll << 40;
     const bool gather = !on_grid(a.x, a.ldx, es, 16) || !on_grid(a.w, a.ldw, es, 16) || a.ldx * es >= far ||
                         a.ldw * es >= far;
-    a.seg_blocks = a.out_dt == BIGEMM_F32 ? kFullSegment : a.k_blocks;
-    if (!gather && a.M > 128) {
-        const int bn = choose_many(a, ds->sm_count);
+    a.seg_blocks = a.out_dt == BIGEMM_F32 ? full_segment(mx) : a.k_blocks;
+    const Choice pick = choose(a, ds->sm_count, gather);
+    if (pick.many) {
+        const int bn = pick.bn;
         const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, nt = (a.N + bn - 1ll) / bn;
         if (mt * nt > 0x7fffffff) return BIGEMM_ERR_UNSUPPORTED;
         a.m_tiles = (int)mt, a.n_tiles = (int)nt;
@@ -138,10 +189,9 @@ bigemm_status product(MatmulArgs &a, void *stream)
         const cudaError_t e = launch_matmul_many(a, bn, ds->sm_count, maps, (cudaStream_t)stream);
         return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
     }
-    const FewCut cut = choose_few(a, ds->sm_count);
+    const FewCut cut = pick.few;
     if ((a.M + (long long)cut.bn - 1) / cut.bn > 65535) return BIGEMM_ERR_UNSUPPORTED;
-    a.kb_per = (a.k_blocks + cut.split - 1) / cut.split;
-    if (a.out_dt != BIGEMM_F32) a.seg_blocks = a.kb_per;
+    a.split = cut.split;
     CUtensorMap mw = {}, mxm = {};
     if (!gather && (!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
                     !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn)))

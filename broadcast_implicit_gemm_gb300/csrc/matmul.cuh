@@ -25,9 +25,10 @@ struct MatmulArgs {
     void *out;
     uint8_t *outs;                   // MXFP8 output: blocked scales
     bool vec_out, vec_other;         // rows start on 16-byte boundaries (8 for e4m3 outputs)
+    bool vec_bias;                   // bias starts on one
     int k_blocks;                    // 128-byte pieces of a row
     int seg_blocks;                  // of them, how many one tensor-memory accumulator sums
-    int kb_per;                      // few tokens: of them, how many one CTA of a split takes
+    int split;                       // few tokens: CTAs that share a tile's blocks, each at least one
     int stages;                      // few tokens: of shared memory
     int m_tiles, n_tiles;            // many tokens: tiles of the output, 256 tokens by BN channels
     bool by_rows;                    // many tokens: out and other have their rows on the 16-byte grid
@@ -39,18 +40,29 @@ namespace {
 
 constexpr int kRow = 128;            // bytes of one row in a stage: a 128-byte swizzle row
 
-// act(z) of one kind.  silu and the tanh form of gelu are both z / (1 + exp(-t)): with
-// tanh(u) = 2 / (1 + exp(-2u)) - 1, gelu's 0.5 z (1 + tanh(u)) is
-// z / (1 + exp(-2u)).  The quotient is the approximate one (2 ulp; a divisor
-// above 2^126 gives 0, which is z's sigmoid to within 2^-126).
+// act(z) of one kind.  silu and the tanh form of gelu are both z / (1 + exp(-t)):
+// with tanh(u) = 2 / (1 + exp(-2u)) - 1, gelu's 0.5 z (1 + tanh(u)) is
+// z / (1 + exp(-2u)), u = sqrt(2/pi) (z + 0.044715 z^3).  The power of two and
+// the reciprocal are the hardware's (2 and 1 ulp); an overflowing power gives 0.
+__device__ __forceinline__ float mm_sigmoid2(float z, float t)   // z / (1 + 2^-t)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return z * r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float mm_act(float z)
 {
+    constexpr float kLog2e = 1.4426950408889634f;
     if (ACT == BIGEMM_ACT_RELU) return z < 0.f ? 0.f : z;
     if (ACT == BIGEMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    if (ACT == BIGEMM_ACT_GELU_TANH)
-        return __fdividef(z, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    if (ACT == BIGEMM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if (ACT == BIGEMM_ACT_GELU_TANH) {
+        constexpr float c = 2.f * 0.79788456080286536f * kLog2e;      // 2 sqrt(2/pi) log2(e)
+        return mm_sigmoid2(z, z * (c + c * 0.044715f * (z * z)));
+    }
+    if (ACT == BIGEMM_ACT_SILU) return mm_sigmoid2(z, kLog2e * z);
     return z;
 }
 
@@ -94,16 +106,9 @@ __device__ __forceinline__ float mm_load1(const void *p, long long i, int dt)
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-// 8 consecutive values from element i on, i * element size on a 16-byte boundary.
-__device__ __forceinline__ void mm_load8(const void *p, long long i, int dt, float (&v)[8])
+// 8 16-bit values.
+__device__ __forceinline__ void mm_unpack8(const uint4 &u, int dt, float (&v)[8])
 {
-    if (dt == BIGEMM_F32) {
-        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        return;
-    }
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
     const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -114,6 +119,18 @@ __device__ __forceinline__ void mm_load8(const void *p, long long i, int dt, flo
             f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q[j]));
         v[2 * j] = f.x, v[2 * j + 1] = f.y;
     }
+}
+
+// 8 consecutive values from element i on, i * element size on a 16-byte boundary.
+__device__ __forceinline__ void mm_load8(const void *p, long long i, int dt, float (&v)[8])
+{
+    if (dt == BIGEMM_F32) {
+        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+    mm_unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i), dt, v);
 }
 
 __device__ __forceinline__ uint32_t mm_pack2(float a, float b, int dt)

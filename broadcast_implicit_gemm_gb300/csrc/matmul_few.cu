@@ -10,7 +10,8 @@
 // that one finishes, and adds what it got in rank order, so that the result
 // does not depend on timing, without a workspace and without a second launch.
 // (Sent, not fetched: a fetch waits for each answer, and holds its owner in a
-// second barrier; 4096 x 4096 for one token 8.1 -> @ us.)
+// second barrier: one token through 4096 x 4096 bf16 8.1 us against 7.8, 64 tokens
+// 14.4 against 10.9.)
 //
 // GATHER: rows that TMA cannot address (a stride or base off the 16-byte grid)
 // are brought into the same swizzled stages by six more warps with plain loads.
@@ -21,7 +22,7 @@
 //
 // FULL: a 32-bit output.  The tensor core cuts each addition into its fp32
 // accumulator short, so the error of one long sum grows with K (measured
-// 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 1024 elements
+// 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
 #include "matmul.cuh"
 
@@ -103,11 +104,11 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
     float *part = reinterpret_cast<float *>(C::beside ? ss + S * 2 * kMxBlockBytes + 256 : smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = (int)((p.k_blocks + p.kb_per - 1) / p.kb_per);   // CTAs of the cluster
+    const int split = p.split;                       // CTAs of the cluster
     const int rank = split > 1 ? (int)cluster_ctarank() : 0;
     const int ct = (int)blockIdx.x / split, n0 = ct * 128;
     const int m0 = (int)blockIdx.y * BN;
-    const int kb0 = rank * p.kb_per, kb1 = min(p.k_blocks, kb0 + p.kb_per);
+    const int kb0 = (int)((long long)rank * p.k_blocks / split), kb1 = (int)((long long)(rank + 1) * p.k_blocks / split);
     const int xblocks = p.k_blocks;                  // MX: blocks of scales per block row
 
     if (threadIdx.x == 0) {

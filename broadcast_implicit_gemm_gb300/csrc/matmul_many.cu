@@ -5,8 +5,8 @@
 // (M = 256: 128 tokens per CTA, half of the weights' rows in each), which halves
 // what an SM's shared memory has to deliver for the weights: at 256 x 256 a CTA
 // stages 32 KB per 64 elements of K (128 in 8 bits) for 4 MMAs of 128 cycles.
-// Pairs are persistent; one warp loads, one issues MMAs, eight drain: two per
-// quarter of the tokens, each half of the channels, a lane to a token.  Tiles
+// Pairs are persistent; one warp loads, one issues MMAs, 8 or 16 drain: two
+// or four per quarter of the tokens, a lane to a token.  Tiles
 // are walked eight token tiles at a time across the channels, so that what runs
 // at once shares its operands in L2.
 //
@@ -15,7 +15,7 @@
 // stage), so there is one accumulator; the drain warps take all of it to
 // registers, hand it back, and go on from there.
 //
-// FULL: a 32-bit output, sums of at most 64 MMAs' depth added up in registers
+// FULL: a 32-bit output, sums of at most 512 or 2048 elements added up in registers
 // (matmul_few.cu says why).
 #include "matmul.cuh"
 
@@ -23,23 +23,26 @@ namespace bigemm {
 
 namespace {
 
-// Three warpgroups: producer, MMA and two idle warps; eight drain warps.  A block
-// launches with 168 registers a thread, 504 over the three; the first group
-// leaves 72 of them and the drain groups take 216 each, 504 again.
-constexpr int kManyThreads = 384;
-constexpr int kLaunchRegs = 168, kLeadRegs = 72, kDrainRegs = 216;
-static_assert(kLeadRegs + 2 * kDrainRegs <= 3 * kLaunchRegs, "a larger sum would wait for ever");
 constexpr int kManyA = 128 * kRow;             // a CTA's tokens per stage
 
 template <int BN, bool MX, bool FULL>
 struct ManyCfg {
+    static constexpr bool keep = MX || FULL;       // the tile's sums go to registers before the epilogue
+    // A block is a warpgroup with the producer, the MMA warp and two idle ones, and the drain
+    // warps' groups; the registers it launches with are dealt out anew between the two kinds.
+    // Sixteen drain warps hide each other's latencies (8192 x 4096 x 512 bf16: 37 us with eight,
+    // 32 with sixteen), but leave no room for a tile's sums.
+    static constexpr int drain = keep ? 8 : 16, threads = 128 + 32 * drain;
+    static constexpr int launch_regs = keep ? 168 : 96, lead_regs = keep ? 72 : 56, drain_regs = keep ? 216 : 104;
+    static_assert(lead_regs + drain / 4 * drain_regs <= threads / 128 * launch_regs, "a larger sum would wait for ever");
+    static constexpr int units = BN / 32 / (drain / 4);                       // of 32 channels, per drain warp
     static constexpr int b_bytes = BN / 2 * kRow;
     static constexpr int s_bytes = MX ? (1 + BN / 128) * kMxBlockBytes : 0;   // the CTA's tokens, all of BN
     static constexpr int stage = kManyA + b_bytes + s_bytes;
-    static constexpr int per_warp = FULL ? 4096 : MX ? 2048 : 4096;           // output staging
+    static constexpr int per_warp = FULL ? 4096 : 2048;                       // output staging
     static constexpr int stages = BN == 128 ? 7 : FULL ? 5 : 6;
     static constexpr int accs = MX ? 1 : 2;
-    static constexpr int smem = stages * stage + 8 * per_warp + 256 + 1024;
+    static constexpr int smem = stages * stage + drain * per_warp + 256 + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static constexpr uint32_t cols = accs * BN + (MX ? stages * (4 + BN / 32) : 0) <= 256 ? 256 : 512;
     static_assert(accs * BN + (MX ? stages * (4 + BN / 32) : 0) <= 512, "tensor memory");
@@ -59,71 +62,126 @@ __device__ __forceinline__ Tile tile_of(const MatmulArgs &p, int t)
     return {g * kGroup + r % rows, r / rows};
 }
 
-// 32 channels of one token from channel n on: bias (lane i holds that of
-// channel n + i), act, combine.
-__device__ __forceinline__ void epilogue32(const MatmulArgs &p, long long m, int n, float bias, float (&v)[32])
+// A warp's 32 tokens by 32 channels of other come as they lie in memory, 4 (or,
+// of 32 bits, 8) lanes to a token's 64 (128) bytes, and are turned round in
+// shared memory: a lane that loads its own token's bytes makes each load touch
+// 32 lines (8192 x 4096 x 64 bf16 with a gate: 63 us against 48).
+struct Other32 {
+    uint4 q[4];
+};
+
+// 16-bit ones are asked for before the sums are there.
+__device__ __forceinline__ void other_ahead(const MatmulArgs &p, int lane, int m_warp, int n, Other32 &o)
 {
-    if (p.bias) {
+    if (p.combine == BIGEMM_COMBINE_NONE || p.other_dt == BIGEMM_F32 || !p.by_rows || n + 32 > p.N) return;
+    const int m = m_warp + (lane >> 2);
+    const uint16_t *from = static_cast<const uint16_t *>(p.other) + (long long)m * p.ldother + n + (lane & 3) * 8;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+    for (int i = 0; i < 4; ++i)
+        if (m + 8 * i < p.M) o.q[i] = *reinterpret_cast<const uint4 *>(from + 8 * i * p.ldother);
+}
+
+// A warp's part of a tile's other, a row per lane, to L2.
+template <int UNITS>
+__device__ __forceinline__ void other_to_l2(const MatmulArgs &p, Tile tile, int bn, int row, int h)
+{
+    const long long m = (long long)tile.m * kManyTokens + row;
+    const int n = tile.n * bn + h * UNITS * 32;
+    if (p.combine == BIGEMM_COMBINE_NONE || m >= p.M || n >= p.N) return;
+    const int es = p.other_dt == BIGEMM_F32 ? 4 : 2, bytes = min(UNITS * 32, p.N - n) * es;
+    const uint8_t *from = static_cast<const uint8_t *>(p.other) + (m * p.ldother + n) * es;
+    for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(from + bytes - 1));
+}
+
+// To the staging (free of the last output's reader after the wait), for
+// epilogue32 to read a token per lane.
+__device__ __forceinline__ void other_turn(const MatmulArgs &p, uint8_t *stage, int lane, const Other32 &o)
+{
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane >> 2) + 8 * i;
+        *reinterpret_cast<uint4 *>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = o.q[i];
     }
-    mm_act_all(p.act, v);
-    if (p.combine == BIGEMM_COMBINE_NONE || m >= p.M) return;
-    const long long at = m * p.ldother + n;
-    const bool mul = p.combine == BIGEMM_COMBINE_MUL;
+    __syncwarp();
+}
+
+// v * or + 32 values of other: 16-bit ones from the staging, 16 bytes at a time,
+// swizzled by key; 32-bit ones as they are.
+template <int DT, bool MUL>
+__device__ __forceinline__ void combine_each(const void *row, int key, float (&v)[32])
+{
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        float o[8];
-        mm_load8(p.other, at + c, p.other_dt, o);
+    for (int c = 0; c < 4; ++c) {
+        float f[8];
+        if (DT == BIGEMM_F32) mm_load8(row, c * 8, BIGEMM_F32, f);
+        else mm_unpack8(reinterpret_cast<const uint4 *>(row)[c ^ key], DT, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c + j] = mul ? v[c + j] * o[j] : v[c + j] + o[j];
+        for (int j = 0; j < 8; ++j) v[c * 8 + j] = MUL ? v[c * 8 + j] * f[j] : v[c * 8 + j] + f[j];
     }
 }
 
-// A drain warp's output of 32 tokens by 32 channels, all inside N, a lane's
-// token in v: through shared memory by TMA.  Returns the scale code of the
-// lane's group for an e4m3 output.
-template <int PER_WARP>
-__device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensorMap *map, uint8_t *stage, int &piece,
-                                             int lane, int m_warp, int n, float (&v)[32])
+// 32 channels of one token from channel n on, all inside N: bias, act, combine.
+__device__ __forceinline__ void epilogue32(const MatmulArgs &p, uint8_t *stage, int lane, long long m, int n,
+                                           const Other32 &o, float (&v)[32])
 {
-    uint32_t code = 0;
-    uint32_t w[32];
-    int words;                       // 32-bit words of the lane's row
-    if (p.out_dt == BIGEMM_MXF8) {
-        float top = 0.f;
+    if (p.bias) {
+        if (p.vec_bias) {
+            const float4 *b = reinterpret_cast<const float4 *>(p.bias + n);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = mx_amax(top, v[i]);
-        code = mx_scale_code(top);
-        const float inv = mx_inv_scale(code);
+            for (int i = 0; i < 8; ++i) {
+                const float4 f = __ldg(b + i);
+                v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = mx_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-        words = 8;
-    } else if (p.out_dt == BIGEMM_F32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-        words = 32;
+            for (int i = 0; i < 32; ++i) v[i] += __ldg(p.bias + n + i);
+        }
+    }
+    mm_act_all(p.act, v);
+    if (p.combine == BIGEMM_COMBINE_NONE) return;
+    const bool mul = p.combine == BIGEMM_COMBINE_MUL;
+    if (p.other_dt == BIGEMM_F32) {
+        if (m < p.M) {
+            const float *from = static_cast<const float *>(p.other) + m * p.ldother + n;
+            if (mul) combine_each<BIGEMM_F32, true>(from, 0, v);
+            else combine_each<BIGEMM_F32, false>(from, 0, v);
+        }
+        return;
+    }
+    other_turn(p, stage, lane, o);
+    // the type and the operation are chosen once for all 32
+    const uint8_t *row = stage + lane * 64;
+    const int key = (lane >> 1) & 3;
+    if (p.other_dt == BIGEMM_F16) {
+        if (mul) combine_each<BIGEMM_F16, true>(row, key, v);
+        else combine_each<BIGEMM_F16, false>(row, key, v);
     } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], p.out_dt);
-        words = 16;
+        if (mul) combine_each<BIGEMM_BF16, true>(row, key, v);
+        else combine_each<BIGEMM_BF16, false>(row, key, v);
     }
-    const int bytes = words * 128;                 // 32 rows
-    const int bufs = PER_WARP / bytes;
-    uint8_t *buf = stage + (piece % bufs) * bytes;
-    if (lane == 0) {
-        if (bufs == 1) bulk_wait_read<0>();
-        else bulk_wait_read<1>();
-    }
+    __syncwarp();                    // every lane has its token before the output takes the staging
+}
+
+// 32 rows of WORDS 32-bit words, a lane's row in w, to global memory: through the
+// staging (two buffers of it, where two fit) by TMA.
+template <int PER_WARP, int WORDS>
+__device__ __forceinline__ void put_words(const MatmulArgs &p, const CUtensorMap *map, uint8_t *stage, int &piece,
+                                          int lane, int m_warp, int n, const uint32_t (&w)[WORDS])
+{
+    constexpr int bytes = WORDS * 128;
+    constexpr bool two = 2 * bytes <= PER_WARP;
+    uint8_t *buf = stage + (two ? (piece & 1) * bytes : 0);
+    if (lane == 0) bulk_wait_read<two ? 1 : 0>();
     __syncwarp();
     // the swizzle of the output's map: rows of 128, 64 or 32 bytes
-    const int key = words == 32 ? lane & 7 : words == 16 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+    const int key = WORDS == 32 ? lane & 7 : WORDS == 16 ? (lane >> 1) & 3 : (lane >> 2) & 1;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c * 4 < words)
-            *reinterpret_cast<uint4 *>(buf + lane * words * 4 + ((c ^ key) << 4)) =
-                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    for (int c = 0; c < WORDS / 4; ++c)
+        *reinterpret_cast<uint4 *>(buf + lane * WORDS * 4 + ((c ^ key) << 4)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && m_warp < p.M) {
@@ -131,7 +189,44 @@ __device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensor
         bulk_commit();
     }
     ++piece;
-    return code;
+}
+
+// A drain warp's output of 32 tokens by 32 channels, all inside N, a lane's
+// token in v.  Returns the scale code of the lane's group for an e4m3 output.
+template <int PER_WARP, bool MX, bool FULL>
+__device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensorMap *map, uint8_t *stage, int &piece,
+                                             int lane, int m_warp, int n, float (&v)[32])
+{
+    if constexpr (FULL) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+        put_words<PER_WARP, 32>(p, map, stage, piece, lane, m_warp, n, w);
+        return 0;
+    }
+    if (MX && p.out_dt == BIGEMM_MXF8) {
+        uint32_t w[8];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = mx_amax(top, v[i]);
+        const uint32_t code = mx_scale_code(top);
+        const float inv = mx_inv_scale(code);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = mx_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        put_words<PER_WARP, 8>(p, map, stage, piece, lane, m_warp, n, w);
+        return code;
+    }
+    uint32_t w[16];
+    if (p.out_dt == BIGEMM_F16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_F16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_BF16);
+    }
+    put_words<PER_WARP, 16>(p, map, stage, piece, lane, m_warp, n, w);
+    return 0;
 }
 
 // 16 values, a row each, to element 0 of rows ld bytes apart; `rows` of them.
@@ -162,11 +257,13 @@ __device__ __forceinline__ void load_down(const uint8_t *at, long long ld, int r
 // end inside: they are turned round in shared memory, 16 tokens at a time, so
 // that a lane has one channel of each token and the warp's plain loads and
 // stores cover a token's 32 channels at once.  All of the epilogue is here.
+template <bool MX, bool FULL>
 __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *stage, int lane, int m_warp, int n,
-                                                float bias, float (&v)[32])
+                                                float (&v)[32])
 {
     float *turn = reinterpret_cast<float *>(stage);
     const bool in = n + lane < p.N;
+    const float bias = p.bias && in ? __ldg(p.bias + n + lane) : 0.f;
     uint32_t code = 0;
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
@@ -197,7 +294,7 @@ __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *st
         }
         const long long at = m0 * p.ldo + n + lane;
         uint8_t *out = static_cast<uint8_t *>(p.out);
-        if (p.out_dt == BIGEMM_MXF8) {
+        if (MX && p.out_dt == BIGEMM_MXF8) {
             out += at;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
@@ -206,7 +303,7 @@ __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *st
                 if (lane == half * 16 + r) code = c;
                 if (r < rows) out[r * p.ldo] = (uint8_t)mx_pack4(y[r] * mx_inv_scale(c), 0.f, 0.f, 0.f);
             }
-        } else if (p.out_dt == BIGEMM_F32) {
+        } else if (FULL) {
             store_down<float>(out + at * 4, p.ldo * 4, rows, y);
         } else if (p.out_dt == BIGEMM_F16) {
             store_down<__half>(out + at * 2, p.ldo * 2, rows, y);
@@ -219,14 +316,14 @@ __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *st
 }
 
 template <int BN, bool MX, bool FULL>
-__global__ void __launch_bounds__(kManyThreads, 1)
+__global__ void __launch_bounds__(ManyCfg<BN, MX, FULL>::threads, 1)
     matmul_many_kernel(const __grid_constant__ ManyMaps maps, const MatmulArgs p)
 {
     using C = ManyCfg<BN, MX, FULL>;
     constexpr int S = C::stages, ACC = C::accs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sa = smem, *sb = sa + S * kManyA, *out_stage = sb + S * C::b_bytes, *ss = out_stage + 8 * C::per_warp;
+    uint8_t *sa = smem, *sb = sa + S * kManyA, *out_stage = sb + S * C::b_bytes, *ss = out_stage + C::drain * C::per_warp;
     uint64_t *full = reinterpret_cast<uint64_t *>(ss + S * C::s_bytes);
     uint64_t *empty = full + S, *tfull = empty + S, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
@@ -241,7 +338,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         // an accumulator comes back from both CTAs' drain warps
-        for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 16);
+        for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 2 * C::drain);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -261,7 +358,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     griddep_enter();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeadRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::lead_regs));
         if (warp == 0) {
             // ------------------------------------------------------ producer
             if (lane == 0) {
@@ -356,36 +453,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::drain_regs));
         // ------------------------------------------------------ drain and epilogue
-        constexpr bool KEEP = MX || FULL;              // the tile's sums go to registers first
-        constexpr int UNITS = BN / 64;                 // of 32 channels, per warp
+        constexpr bool KEEP = C::keep;
+        constexpr int UNITS = C::units;
         const int q = warp & 3, h = (warp - 4) >> 2;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * (BN / 2));
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * UNITS * 32);
         const uint32_t tempty_even = mapa_shared(smem_u32(tempty), 0);
         uint8_t *stage = out_stage + (warp - 4) * C::per_warp;
         const int col_blocks = (int)((p.N + 127ll) / 128);
         int a = 0, piece = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
+        if (pair < tiles) other_to_l2<C::units>(p, tile_of(p, pair), BN, rank * 128 + q * 32 + lane, h);
         for (int t = pair; ok && t < tiles; t += pairs) {
             const Tile tile = tile_of(p, t);
-            const int m_warp = tile.m * kManyTokens + rank * 128 + q * 32, n_warp = tile.n * BN + h * (BN / 2);
+            const int m_warp = tile.m * kManyTokens + rank * 128 + q * 32, n_warp = tile.n * BN + h * UNITS * 32;
             const long long m = m_warp + lane;
-            float bias[UNITS];
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const int n = n_warp + u * 32 + lane;
-                bias[u] = p.bias && n < p.N ? __ldg(p.bias + n) : 0.f;
-            }
-            if (p.combine != BIGEMM_COMBINE_NONE && m < p.M && n_warp < p.N) {
-                // the tile's part of other comes to L2 while the MMAs run
-                const long long es = p.other_dt == BIGEMM_F32 ? 4 : 2;
-                const uint8_t *from = static_cast<const uint8_t *>(p.other) + (m * p.ldother + n_warp) * es;
-                const int bytes = (int)(min(BN / 2, p.N - n_warp) * es);
-                for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + bytes - 1));
-            }
+            // the next tile's part of other comes to L2 while this one is done
+            if (t + pairs < tiles) other_to_l2<C::units>(p, tile_of(p, t + pairs), BN, rank * 128 + q * 32 + lane, h);
+            Other32 ahead;
+            other_ahead(p, lane, m_warp, n_warp, ahead);
             uint32_t codes = 0;
             float keep[KEEP ? UNITS : 1][32];
             for (int k0 = 0; k0 < p.k_blocks; k0 += p.seg_blocks) {
@@ -423,14 +511,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                        float b = bias[0];
-#pragma unroll
-                        for (int j = 1; j < UNITS; ++j) b = u == j ? bias[j] : b;
                         if (p.by_rows && n + 32 <= p.N) {
-                            epilogue32(p, m, n, b, v);
-                            put_rows<C::per_warp>(p, &maps.out, stage, piece, lane, m_warp, n, v);
+                            epilogue32(p, stage, lane, m, n, ahead, v);
+                            put_rows<C::per_warp, MX, FULL>(p, &maps.out, stage, piece, lane, m_warp, n, v);
+                            // (not before: the fence in there waits for loads in flight)
+                            if (u + 1 < UNITS) other_ahead(p, lane, m_warp, n + 32, ahead);
                         } else if (n < p.N) {
-                            put_columns(p, stage, lane, m_warp, n, b, v);
+                            put_columns<MX, FULL>(p, stage, lane, m_warp, n, v);
                         }
                     }
                 }
@@ -445,13 +532,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                 for (int u = 0; u < UNITS; ++u) {
                     const int n = n_warp + u * 32;
                     if (p.by_rows && n + 32 <= p.N) {
-                        epilogue32(p, m, n, bias[u], keep[u]);
-                        codes |= put_rows<C::per_warp>(p, &maps.out, stage, piece, lane, m_warp, n, keep[u]) << (8 * u);
+                        epilogue32(p, stage, lane, m, n, ahead, keep[u]);
+                        codes |= put_rows<C::per_warp, MX, FULL>(p, &maps.out, stage, piece, lane, m_warp, n, keep[u]) << (8 * u);
+                        if (u + 1 < UNITS) other_ahead(p, lane, m_warp, n + 32, ahead);
                     } else if (n < p.N) {
-                        codes |= put_columns(p, stage, lane, m_warp, n, bias[u], keep[u]) << (8 * u);
+                        codes |= put_columns<MX, FULL>(p, stage, lane, m_warp, n, keep[u]) << (8 * u);
                     }
                 }
-                if (p.out_dt == BIGEMM_MXF8 && m < p.M && (n_warp >> 7) < col_blocks) {
+                if (MX && p.out_dt == BIGEMM_MXF8 && m < p.M && (n_warp >> 7) < col_blocks) {
                     uint8_t *at = p.outs + mx_scale_offset(m, n_warp / kMxGroup, col_blocks);
                     if (UNITS == 4) *reinterpret_cast<uint32_t *>(at) = codes;
                     else *reinterpret_cast<uint16_t *>(at) = (uint16_t)codes;
@@ -487,12 +575,12 @@ cudaError_t launch_one(const MatmulArgs &a, int grid, const ManyMaps &maps, cuda
         cudaFuncAttributes fa;
         const cudaError_t f = cudaFuncGetAttributes(&fa, kern);
         if (f != cudaSuccess) return f;
-        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        if (fa.numRegs != ManyCfg<BN, MX, FULL>::launch_regs) return cudaErrorInvalidConfiguration;
         if (dev < 64) attr_set |= 1ull << dev;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kManyThreads);
+    cfg.blockDim = dim3(ManyCfg<BN, MX, FULL>::threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
