@@ -376,53 +376,41 @@ def bcast(var, N, H, W, op=BC_EXP, eps=1e-5, out_dtype=None, out=None, stream=No
 # are a float8_e4m3fn tensor and its scales, a contiguous float8_e8m0fnu (or
 # uint8) tensor of mx_scale_shape(rows, cols).
 
-_LAYER_CODES: dict = {}
+_layer_module = None
 
 
-def _layer_code(dtype) -> int:
-    if not _LAYER_CODES:
+def _layer():
+    """The extension module that checks the tensors and makes the calls; raise if absent."""
+    global _layer_module
+    if _layer_module is None:
+        import importlib.machinery
+        import importlib.util
+
         import torch
-        _LAYER_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
-                             torch.float8_e4m3fn: MXF8})
-    code = _LAYER_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
+        path = os.path.join(_HERE, "_layer.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        lib = load_library()
+        loader = importlib.machinery.ExtensionFileLoader("_layer", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_layer", path, loader=loader))
+        loader.exec_module(module)
+        module.init((torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn),
+                    (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                    tuple(ctypes.cast(f, ctypes.c_void_p).value
+                          for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run)))
+        _layer_module = module
+    return _layer_module
 
 
-def _first(t, name):
-    """(rows, columns, row stride, device index) of the CUDA matrix that a call is about."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a 2-D CUDA tensor")
-    rows, cols = t.shape
-    return rows, cols, _rows_apart(t, name, rows, cols), t.get_device()
-
-
-def _rows_apart(t, name, rows, cols):
-    ld, one = t.stride()
-    if one != 1 and cols > 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    if ld < cols:
-        if rows > 1:
-            raise ValueError(f"{name}: rows overlap")
-        return cols    # a single row's stride may be anything
-    return ld
-
-
-def _matrix(t, name, rows, cols, dev):
-    """The row stride of another matrix of the call, rows x cols on device `dev`."""
-    if t.get_device() != dev or t.dim() != 2 or t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected shape ({rows}, {cols}) on cuda:{dev}, got {tuple(t.shape)} on {t.device}")
-    return _rows_apart(t, name, rows, cols)
-
-
-def _vector(t, name, n, dev):
-    """The address of a float32 vector, or None."""
-    if t is None:
-        return None
-    if _layer_code(t.dtype) != F32 or t.get_device() != dev or t.shape != (n,) or t.stride(0) != 1 and n > 1:
-        raise ValueError(f"{name}: expected a contiguous float32 vector of {n} elements on cuda:{dev}")
-    return t.data_ptr()
+def _status(status, where, again, x):
+    """Raise for a status that is not OK; if x's device was not the current one, call again with it current."""
+    if status == -1:
+        import torch
+        with torch.cuda.device(x.device):
+            status = again()
+    if status != 0:
+        raise BigemmError(status, where)
 
 
 def mx_scale_shape(rows: int, cols: int) -> tuple:
@@ -431,72 +419,23 @@ def mx_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
 
 
-def _scales(t, name, rows, cols, dev):
-    """The address of the scales of a rows x cols MXFP8 matrix."""
-    if (t.element_size() != 1 or t.numel() != -(-rows // 128) * -(-cols // 128) * 512 or not t.is_contiguous()
-            or t.get_device() != dev):
-        raise ValueError(f"{name}: expected contiguous scales of shape {mx_scale_shape(rows, cols)} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _new_scales(rows, cols, device):
+def _output(out, out_dtype, default, rows, cols, device):
     import torch
-    return torch.zeros(mx_scale_shape(rows, cols), dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
-
-
-def _call(fn, where, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current, on the given stream or torch's current one there."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
-    if status != 0:
-        raise BigemmError(status, where)
-
-
-def _product(x, xs, w, ws, bias, act, other, combine, out_dtype, out, out_scale, stream):
-    M, K, ldx, dev = _first(x, "x")
-    N = w.shape[0]
-    ldw = _matrix(w, "w", N, K, dev)
-    if w.dtype != x.dtype:
-        raise TypeError(f"x is {x.dtype} and w is {w.dtype}")
-    in_code = _layer_code(x.dtype)
-    if (xs is not None) != (in_code == MXF8):
-        raise TypeError("matmul_mx takes float8_e4m3fn matrices, matmul 16-bit ones")
-    if combine is None:
-        combine = COMBINE_NONE if other is None else COMBINE_ADD
-    ldother, other_code, other_ptr = 0, F32, None
-    if combine != COMBINE_NONE:
-        if other is None:
-            raise ValueError("combine needs other")
-        ldother, other_code, other_ptr = _matrix(other, "other", M, N, dev), _layer_code(other.dtype), other.data_ptr()
     if out is None:
-        import torch
-        odt = out_dtype if out_dtype is not None else (torch.bfloat16 if in_code == MXF8 else x.dtype)
-        out = torch.empty((M, N), dtype=odt, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
+        return torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else default, device=device)
+    if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    ldo, out_code = _matrix(out, "out", M, N, dev), _layer_code(out.dtype)
-    lib = _lib or load_library()
-    if in_code != MXF8:
-        _call(lib.matmul_run, "matmul_run", dev, stream, M, N, K, in_code, x.data_ptr(), ldx, w.data_ptr(), ldw,
-              _vector(bias, "bias", N, dev), act, combine, other_code, other_ptr, ldother, out_code, out.data_ptr(), ldo)
-        return out
-    scale_ptr = None
-    if out_code == MXF8:
-        if out_scale is None:
-            out_scale = _new_scales(M, N, x.device)
-        scale_ptr = _scales(out_scale, "out_scale", M, N, dev)
-    _call(lib.matmul_mx_run, "matmul_mx_run", dev, stream, M, N, K, x.data_ptr(), ldx, _scales(xs, "x_scale", M, K, dev),
-          w.data_ptr(), ldw, _scales(ws, "w_scale", N, K, dev), _vector(bias, "bias", N, dev), act, combine, other_code,
-          other_ptr, ldother, out_code, out.data_ptr(), ldo, scale_ptr)
-    return out if scale_ptr is None else (out, out_scale)
+    return out
+
+
+def _output_scales(out, scale):
+    """Scales for out if it is an MXFP8 matrix and has none."""
+    import torch
+    if out.dtype != torch.float8_e4m3fn:
+        return None
+    if scale is None:
+        scale = torch.zeros(mx_scale_shape(*out.shape), dtype=torch.uint8, device=out.device).view(torch.float8_e8m0fnu)
+    return scale
 
 
 def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=None, out=None, stream=None):
@@ -505,14 +444,32 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
     `combine` is COMBINE_ADD (a residual; the default when `other` is given) or COMBINE_MUL (a gate).
     Sums in fp32; out is x's type unless out_dtype (float32, float16, bfloat16) or out says otherwise.
     """
-    return _product(x, None, w, None, bias, act, other, combine, out_dtype, out, None, stream)
+    if combine is None:
+        combine = COMBINE_NONE if other is None else COMBINE_ADD
+    if out is None or out_dtype is not None:
+        out = _output(out, out_dtype, x.dtype, x.shape[0], w.shape[0], x.device)
+    args = (x, None, w, None, bias, act, other, combine, out, None, stream)
+    status = (_layer_module or _layer()).product(*args)
+    if status:
+        _status(status, "matmul", lambda: _layer().product(*args), x)
+    return out
 
 
 def matmul_mx(x, x_scale, w, w_scale, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=None, out=None,
               out_scale=None, stream=None):
     """matmul of MXFP8 matrices.  out is bfloat16 unless out_dtype or out says otherwise; for
     float8_e4m3fn the result is (elements, scales)."""
-    return _product(x, x_scale, w, w_scale, bias, act, other, combine, out_dtype, out, out_scale, stream)
+    import torch
+    if combine is None:
+        combine = COMBINE_NONE if other is None else COMBINE_ADD
+    if out is None or out_dtype is not None:
+        out = _output(out, out_dtype, torch.bfloat16, x.shape[0], w.shape[0], x.device)
+    out_scale = _output_scales(out, out_scale)
+    args = (x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream)
+    status = (_layer_module or _layer()).product(*args)
+    if status:
+        _status(status, "matmul_mx", lambda: _layer().product(*args), x)
+    return out if out_scale is None else (out, out_scale)
 
 
 def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, out_scale=None, sum_out=None,
@@ -521,54 +478,29 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, o
 
     Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.
     """
-    rows, cols, ldx, dev = _first(x, "x")
-    code = _layer_code(x.dtype)
-    if code == MXF8:
-        raise TypeError("rmsnorm takes float32, float16 or bfloat16")
-    ldr = lds = 0
-    res_ptr = sum_ptr = scale_ptr = None
-    if residual is not None:
-        ldr, res_ptr = _matrix(residual, "residual", rows, cols, dev), residual.data_ptr()
-        if residual.dtype != x.dtype:
-            raise TypeError(f"x is {x.dtype} and residual is {residual.dtype}")
-        if sum_out is None:
-            import torch
-            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    if sum_out is not None:
-        lds, sum_ptr = _matrix(sum_out, "sum_out", rows, cols, dev), sum_out.data_ptr()
-        if sum_out.dtype != x.dtype:
-            raise TypeError(f"x is {x.dtype} and sum_out is {sum_out.dtype}")
-    if out is None:
-        import torch
-        out = torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else x.dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    ldo, out_code = _matrix(out, "out", rows, cols, dev), _layer_code(out.dtype)
-    if out_code == MXF8:
-        if out_scale is None:
-            out_scale = _new_scales(rows, cols, x.device)
-        scale_ptr = _scales(out_scale, "out_scale", rows, cols, dev)
-    _call((_lib or load_library()).rmsnorm_run, "rmsnorm_run", dev, stream, rows, cols, code, x.data_ptr(), ldx, res_ptr,
-          ldr, _vector(weight, "weight", cols, dev), eps, sum_ptr, lds, out_code, out.data_ptr(), ldo, scale_ptr)
+    if residual is not None and sum_out is None:
+        sum_out = _output(None, None, x.dtype, *x.shape, x.device)
+    if out is None or out_dtype is not None:
+        out = _output(out, out_dtype, x.dtype, *x.shape, x.device)
+    out_scale = _output_scales(out, out_scale)
+    args = (x, weight, residual, eps, sum_out, out, out_scale, stream)
+    status = (_layer_module or _layer()).norm(*args)
+    if status:
+        _status(status, "rmsnorm", lambda: _layer().norm(*args), x)
     if residual is None:
-        return out if scale_ptr is None else (out, out_scale)
-    return (out, sum_out) if scale_ptr is None else (out, out_scale, sum_out)
+        return out if out_scale is None else (out, out_scale)
+    return (out, sum_out) if out_scale is None else (out, out_scale, sum_out)
 
 
 def mx_quantize(x, out=None, scale=None, stream=None):
     """(float8_e4m3fn elements, scales) of a float32, float16 or bfloat16 matrix."""
-    rows, cols, ldx, dev = _first(x, "x")
-    code = _layer_code(x.dtype)
-    if code == MXF8:
-        raise TypeError("mx_quantize takes float32, float16 or bfloat16")
+    import torch
     if out is None:
-        import torch
-        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
-    elif _layer_code(out.dtype) != MXF8:
-        raise TypeError(f"out is {out.dtype}")
-    ldo = _matrix(out, "out", rows, cols, dev)
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     if scale is None:
-        scale = _new_scales(rows, cols, x.device)
-    _call((_lib or load_library()).mx_quantize_run, "mx_quantize_run", dev, stream, rows, cols, code, x.data_ptr(), ldx,
-          out.data_ptr(), ldo, _scales(scale, "scale", rows, cols, dev))
+        scale = _output_scales(out, None)
+    args = (x, out, scale, stream)
+    status = (_layer_module or _layer()).quantize(*args)
+    if status:
+        _status(status, "mx_quantize", lambda: _layer().quantize(*args), x)
     return out, scale

@@ -1,8 +1,9 @@
 """Compile the CUDA library (csrc/*.cu) into libbigemm.so, in place, for sm_103a.
 
 Each translation unit is compiled by nvcc in parallel; the objects are linked
-into one shared library next to this file.  Rebuilds only when a source or a
-header is newer than the library.
+into one shared library next to this file, and layer_py.c is compiled into the
+extension module _layer.so beside it.  Rebuilds only when a source or a header
+is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbigemm.so")
+MODULE = os.path.join(HERE, "_layer.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -37,13 +40,14 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+            + glob.glob(os.path.join(CSRC, "*.c"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -60,6 +64,19 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_module() -> None:
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found: gcc is required to build _layer.so")
+    tmp = MODULE + f".tmp{os.getpid()}"
+    cmd = [cc, "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "layer_py.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on layer_py.c:\n{r.stderr}")
+    os.replace(tmp, MODULE)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     if not force and up_to_date():
         return LIB
@@ -67,7 +84,9 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     srcs = sources()
     jobs = jobs or min(len(srcs), max(2, os.cpu_count() or 2))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        module = ex.submit(_build_module)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -249,3 +249,49 @@ def test_mx_nan_scale_reaches_its_row_alone():
     got = bg.matmul_mx(x, xs, w, ws)
     keep = [m for m in range(M) if m != 130]
     assert torch.isnan(got[130]).all() and torch.equal(got[keep], clean[keep])
+
+
+# --------------------------------------------------------------------- refusals of the tensor calls
+
+def test_tensor_refusals():
+    x, w = torch.zeros(4, 32).half().cuda(), torch.zeros(8, 32).half().cuda()
+    q, s = bg.mx_quantize(x)
+    p, t = bg.mx_quantize(w)
+    b = torch.zeros(8, device="cuda")
+    for bad, call in (
+            (ValueError, lambda: bg.matmul(x[0], w)),
+            (ValueError, lambda: bg.matmul(x, w[:, :16])),
+            (ValueError, lambda: bg.matmul(x.t(), w)),
+            (ValueError, lambda: bg.matmul(x.expand(4, 32)[:, ::2], w[:, :16].contiguous())),
+            (ValueError, lambda: bg.matmul(x, w.cpu())),
+            (ValueError, lambda: bg.matmul(x, w, bias=b[:7])),
+            (ValueError, lambda: bg.matmul(x, w, bias=b.double())),
+            (ValueError, lambda: bg.matmul(x, w, bias=torch.zeros(16, device="cuda")[::2])),
+            (ValueError, lambda: bg.matmul(x, w, combine=bg.COMBINE_ADD)),
+            (ValueError, lambda: bg.matmul(x, w, other=torch.zeros(8, 4).half().cuda())),
+            (ValueError, lambda: bg.matmul(x, w, out=torch.zeros(4, 9).half().cuda())),
+            (TypeError, lambda: bg.matmul(x, w.bfloat16())),
+            (TypeError, lambda: bg.matmul(x, w, out=torch.zeros(4, 8).half().cuda(), out_dtype=torch.float32)),
+            (TypeError, lambda: bg.matmul(x, w, out=torch.zeros(4, 8, dtype=torch.int32, device="cuda"))),
+            (TypeError, lambda: bg.matmul(q, p)),
+            (TypeError, lambda: bg.matmul_mx(x, s, w, t)),
+            (ValueError, lambda: bg.matmul_mx(q, s.reshape(-1)[:256], p, t)),
+            (ValueError, lambda: bg.matmul_mx(q, s, p, None)),
+            (ValueError, lambda: bg.matmul_mx(q, s.view(torch.uint8).float(), p, t)),
+            (ValueError, lambda: bg.rmsnorm(x, weight=torch.ones(31, device="cuda"))),
+            (ValueError, lambda: bg.rmsnorm(x, residual=x[:3])),
+            (TypeError, lambda: bg.rmsnorm(x, residual=x.bfloat16())),
+            (ValueError, lambda: bg.mx_quantize(x, scale=s.view(torch.uint8).reshape(-1)[1:])),
+            (TypeError, lambda: bg.mx_quantize(x, out=torch.zeros(4, 32).half().cuda())),
+    ):
+        with pytest.raises(bad):
+            call()
+    with pytest.raises(bg.BigemmError):
+        bg.matmul(x.float(), w.float())
+    with pytest.raises(bg.BigemmError):
+        bg.rmsnorm(q)
+    with pytest.raises(bg.BigemmError):
+        bg.rmsnorm(x, out_dtype=torch.bfloat16)
+    assert bg.matmul(x[:0], w).shape == (0, 8)
+    assert bg.matmul_mx(q[:0], s[:0], p, t).shape == (0, 8)
+    assert bg.bigemm_last_device_error() == 0
