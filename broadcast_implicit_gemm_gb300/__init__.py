@@ -25,7 +25,8 @@ __all__ = [
     "bcast_nchw_run_flat", "bcast_run",
     "MXF8", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "ACT_NAMES",
     "COMBINE_NONE", "COMBINE_ADD", "COMBINE_MUL", "COMBINE_NAMES",
-    "matmul_run", "matmul_mx_run", "rmsnorm_run", "mx_quantize_run", "bigemm_mx_scale_bytes",
+    "matmul_run", "matmul_mx_run", "matmul_workspace_bytes", "rmsnorm_run", "mx_quantize_run",
+    "bigemm_mx_scale_bytes",
     "matmul", "matmul_mx", "rmsnorm", "mx_quantize", "mx_scale_shape",
     "bigemm_status_string", "bigemm_last_device_error", "bigemm_clear_device_error",
     "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout", "bigemm_profile_enable",
@@ -102,8 +103,10 @@ def _declare(lib):
     lib.bcast_nchw_run_flat.argtypes = [i, i, i, i, i, p, f, p, i, p]
     lib.bcast_run.argtypes = [i, i, i, i, p, f, p, i, p]
     i64 = ctypes.c_int64
-    lib.matmul_run.argtypes = [i, i, i, i, p, i64, p, i64, p, i, i, i, p, i64, i, p, i64, p]
-    lib.matmul_mx_run.argtypes = [i, i, i, p, i64, p, p, i64, p, p, i, i, i, p, i64, i, p, i64, p, p]
+    lib.matmul_run.argtypes = [i, i, i, i, p, i64, p, i64, p, i, i, i, p, i64, i, p, i64, p, u64, p]
+    lib.matmul_mx_run.argtypes = [i, i, i, p, i64, p, p, i64, p, p, i, i, i, p, i64, i, p, i64, p, p, u64, p]
+    lib.matmul_workspace_bytes.argtypes = [i, i, i, i, p, i64, p, i64]
+    lib.matmul_workspace_bytes.restype = u64
     lib.rmsnorm_run.argtypes = [i, i, i, p, i64, p, i64, p, f, p, i64, i, p, i64, p, p]
     lib.mx_quantize_run.argtypes = [i, i, i, p, i64, p, i64, p, p]
     lib.bigemm_mx_scale_bytes.argtypes = [i, i]
@@ -258,17 +261,22 @@ def bcast_run(B0, P, B1, op, var, eps, out, out_dtype, stream=None):
 
 
 def matmul_run(M, N, K, in_dtype, x, ldx, w, ldw, bias, act, combine, other_dtype, other, ldother,
-               out_dtype, out, ldo, stream=None):
+               out_dtype, out, ldo, workspace=None, workspace_bytes=0, stream=None):
     _check(load_library().matmul_run(M, N, K, in_dtype, _ptr(x), ldx, _ptr(w), ldw, _ptr(bias), act, combine,
                                      other_dtype, _ptr(other), ldother, out_dtype, _ptr(out), ldo,
-                                     _stream(stream)), "matmul_run")
+                                     _ptr(workspace), workspace_bytes, _stream(stream)), "matmul_run")
 
 
 def matmul_mx_run(M, N, K, x, ldx, x_scale, w, ldw, w_scale, bias, act, combine, other_dtype, other, ldother,
-                  out_dtype, out, ldo, out_scale, stream=None):
+                  out_dtype, out, ldo, out_scale, workspace=None, workspace_bytes=0, stream=None):
     _check(load_library().matmul_mx_run(M, N, K, _ptr(x), ldx, _ptr(x_scale), _ptr(w), ldw, _ptr(w_scale),
                                         _ptr(bias), act, combine, other_dtype, _ptr(other), ldother, out_dtype,
-                                        _ptr(out), ldo, _ptr(out_scale), _stream(stream)), "matmul_mx_run")
+                                        _ptr(out), ldo, _ptr(out_scale), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "matmul_mx_run")
+
+
+def matmul_workspace_bytes(M, N, K, in_dtype, x, ldx, w, ldw) -> int:
+    return load_library().matmul_workspace_bytes(M, N, K, in_dtype, _ptr(x), ldx, _ptr(w), ldw)
 
 
 def rmsnorm_run(rows, cols, in_dtype, x, ldx, residual, ldr, weight, eps, sum_out, lds, out_dtype, out, ldo,
@@ -398,17 +406,25 @@ def _layer():
         module.init((torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn),
                     (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
-                          for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run)))
+                          for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
+                                    lib.matmul_workspace_bytes)))
         _layer_module = module
     return _layer_module
 
 
-def _status(status, where, again, x):
-    """Raise for a status that is not OK; if x's device was not the current one, call again with it current."""
-    if status == -1:
-        import torch
-        with torch.cuda.device(x.device):
-            status = again()
+def _status(status, where, again, x, stream=None):
+    """Raise for a status that is not OK.  -1: x's device was not the current one, call again with it current;
+    -1 - n: call again with a workspace of n bytes."""
+    import torch
+    workspace = None
+    with torch.cuda.device(x.device):
+        while status < 0:
+            if status < -1:
+                workspace = torch.empty(-1 - status, dtype=torch.uint8, device=x.device)
+                if stream is not None:      # its memory is not given out again before that stream is done
+                    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+                    workspace.record_stream(s)
+            status = again(workspace)
     if status != 0:
         raise BigemmError(status, where)
 
@@ -449,9 +465,9 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
     if out is None or out_dtype is not None:
         out = _output(out, out_dtype, x.dtype, x.shape[0], w.shape[0], x.device)
     args = (x, None, w, None, bias, act, other, combine, out, None, stream)
-    status = (_layer_module or _layer()).product(*args)
+    status = (_layer_module or _layer()).product(*args, None)
     if status:
-        _status(status, "matmul", lambda: _layer().product(*args), x)
+        _status(status, "matmul", lambda workspace: _layer().product(*args, workspace), x, stream)
     return out
 
 
@@ -466,9 +482,9 @@ def matmul_mx(x, x_scale, w, w_scale, bias=None, act=ACT_NONE, other=None, combi
         out = _output(out, out_dtype, torch.bfloat16, x.shape[0], w.shape[0], x.device)
     out_scale = _output_scales(out, out_scale)
     args = (x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream)
-    status = (_layer_module or _layer()).product(*args)
+    status = (_layer_module or _layer()).product(*args, None)
     if status:
-        _status(status, "matmul_mx", lambda: _layer().product(*args), x)
+        _status(status, "matmul_mx", lambda workspace: _layer().product(*args, workspace), x, stream)
     return out if out_scale is None else (out, out_scale)
 
 
@@ -486,7 +502,7 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, o
     args = (x, weight, residual, eps, sum_out, out, out_scale, stream)
     status = (_layer_module or _layer()).norm(*args)
     if status:
-        _status(status, "rmsnorm", lambda: _layer().norm(*args), x)
+        _status(status, "rmsnorm", lambda workspace: _layer().norm(*args), x)
     if residual is None:
         return out if out_scale is None else (out, out_scale)
     return (out, sum_out) if out_scale is None else (out, out_scale, sum_out)
@@ -502,5 +518,5 @@ def mx_quantize(x, out=None, scale=None, stream=None):
     args = (x, out, scale, stream)
     status = (_layer_module or _layer()).quantize(*args)
     if status:
-        _status(status, "mx_quantize", lambda: _layer().quantize(*args), x)
+        _status(status, "mx_quantize", lambda workspace: _layer().quantize(*args), x)
     return out, scale

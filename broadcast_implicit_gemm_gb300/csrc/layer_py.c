@@ -19,10 +19,12 @@ static PyObject *g_current_stream, *g_current_device;
 static PyObject *s_shape, *s_stride, *s_device, *s_ptr, *s_dtype, *s_numel, *s_contiguous;
 
 static bigemm_status (*p_matmul)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *,
-                                 int, int, bigemm_dtype, const void *, int64_t, bigemm_dtype, void *, int64_t, void *);
+                                 int, int, bigemm_dtype, const void *, int64_t, bigemm_dtype, void *, int64_t, void *,
+                                 uint64_t, void *);
 static bigemm_status (*p_matmul_mx)(int, int, int, const void *, int64_t, const void *, const void *, int64_t,
                                     const void *, const float *, int, int, bigemm_dtype, const void *, int64_t,
-                                    bigemm_dtype, void *, int64_t, void *, void *);
+                                    bigemm_dtype, void *, int64_t, void *, void *, uint64_t, void *);
+static uint64_t (*p_workspace)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t);
 static bigemm_status (*p_norm)(int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *, float,
                                void *, int64_t, bigemm_dtype, void *, int64_t, void *, void *);
 static bigemm_status (*p_quantize)(int, int, bigemm_dtype, const void *, int64_t, void *, int64_t, void *, void *);
@@ -213,12 +215,14 @@ static int arity(const char *name, Py_ssize_t got, Py_ssize_t want)
     return -1;
 }
 
-/* product(x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream) -> status */
+/* product(x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream, workspace) -> status, or
+ * -1 - n where a workspace of n bytes is wanted and none is given */
 static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix x, w, o = {0}, y;
-    void *xs = NULL, *ws = NULL, *ys = NULL, *bias, *stream;
-    if (arity("product", n, 11) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 ||
+    void *xs = NULL, *ws = NULL, *ys = NULL, *bias, *stream, *space = NULL;
+    long long space_bytes = 0;
+    if (arity("product", n, 12) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 ||
         matrix(a[2], "w", &w, x.device, -1, x.cols) < 0)
         return NULL;
     if (w.dtype != x.dtype) return PyErr_Format(PyExc_TypeError, "w: of another dtype than x");
@@ -240,14 +244,21 @@ static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const int r = stream_on(a[10], x.device, &stream);
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    if (a[11] != Py_None) {
+        if (pointer_of(a[11], &space) < 0 || as_ll(PyObject_CallMethodNoArgs(a[11], s_numel), &space_bytes) < 0) return NULL;
+    } else if (x.rows > 0) {
+        const uint64_t want = p_workspace((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld);
+        if (want > 0) return PyLong_FromLongLong(-1 - (long long)want);
+    }
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (mx)
         st = p_matmul_mx((int)x.rows, (int)w.rows, (int)x.cols, x.ptr, x.ld, xs, w.ptr, w.ld, ws, bias, act, combine,
-                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, stream);
+                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, space, (uint64_t)space_bytes, stream);
     else
         st = p_matmul((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld, bias, act,
-                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, stream);
+                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, space, (uint64_t)space_bytes,
+                      stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
@@ -302,8 +313,9 @@ static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
 static PyObject *init(PyObject *self, PyObject *args)
 {
     PyObject *d, *st, *cs, *cd;
-    unsigned long long f[4];
-    if (!PyArg_ParseTuple(args, "O!O!OO(KKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &f[0], &f[1], &f[2], &f[3]))
+    unsigned long long f[5];
+    if (!PyArg_ParseTuple(args, "O!O!OO(KKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &f[0], &f[1], &f[2], &f[3],
+                          &f[4]))
         return NULL;
     if (PyTuple_GET_SIZE(d) != DT_COUNT || PyTuple_GET_SIZE(st) != 2)
         return PyErr_Format(PyExc_ValueError, "init: wrong number of dtypes");
@@ -315,6 +327,7 @@ static PyObject *init(PyObject *self, PyObject *args)
     p_matmul_mx = (void *)(uintptr_t)f[1];
     p_norm = (void *)(uintptr_t)f[2];
     p_quantize = (void *)(uintptr_t)f[3];
+    p_workspace = (void *)(uintptr_t)f[4];
     Py_RETURN_NONE;
 }
 

@@ -138,7 +138,44 @@ constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bi
 // (64; they have one accumulator, and each hand-over costs 1 us).
 int full_segment(bool mx) { return mx ? 16 : 8; }
 
-bigemm_status product(MatmulArgs &a, void *stream)
+constexpr long long kFar = 1ll << 40;           // TMA: strides below 2^40 bytes
+
+// Whether TMA can address an operand's rows.
+bool addressable(const void *p, long long ld, long long es) { return on_grid(p, ld, es, 16) && ld * es < kFar; }
+
+// More tokens than this, and operands off the 16-byte grid are better copied
+// onto it first than gathered by the product: @
+constexpr int kPackTokens = 128;
+
+long long packed_bytes(long long rows, long long cols, long long es) { return up(rows * up(cols * es, 16) * 16, 256) * 256; }
+
+uint64_t workspace_for(long long M, long long N, long long K, long long es, const void *x, long long ldx, const void *w,
+                       long long ldw)
+{
+    if (M <= kPackTokens) return 0;
+    return (uint64_t)((addressable(w, ldw, es) ? 0 : packed_bytes(N, K, es)) +
+                      (addressable(x, ldx, es) ? 0 : packed_bytes(M, K, es)));
+}
+
+// Copies what TMA cannot address to `workspace` and makes it the operand; w first.
+cudaError_t pack(MatmulArgs &a, long long es, uint8_t *workspace, cudaStream_t stream)
+{
+    PackArgs k = {};
+    if (!addressable(a.w, a.ldw, es)) {
+        const long long pitch = up(a.K * es, 16) * 16;
+        k.op[0] = {static_cast<const uint8_t *>(a.w), workspace, a.N, a.ldw * es, pitch, a.K * es, 0};
+        a.w = workspace, a.ldw = pitch / es;
+        workspace += packed_bytes(a.N, a.K, es);
+    }
+    if (!addressable(a.x, a.ldx, es)) {
+        const long long pitch = up(a.K * es, 16) * 16;
+        k.op[1] = {static_cast<const uint8_t *>(a.x), workspace, a.M, a.ldx * es, pitch, a.K * es, 0};
+        a.x = workspace, a.ldx = pitch / es;
+    }
+    return launch_matmul_pack(k, stream);
+}
+
+bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, void *stream)
 {
     if (a.M < 0 || a.N < 1 || a.K < 1) return BIGEMM_ERR_INVALID_ARG;
     const bool mx = a.in_dt == BIGEMM_MXF8;
@@ -168,10 +205,13 @@ bigemm_status product(MatmulArgs &a, void *stream)
     if (a.M == 1) a.ldx = (a.ldx + 15) / 16 * 16;   // the stride of a single row is free
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
-    // TMA: rows on the 16-byte grid, strides below 2^40 bytes
-    const long long far = 1ll << 40;
-    const bool gather = !on_grid(a.x, a.ldx, es, 16) || !on_grid(a.w, a.ldw, es, 16) || a.ldx * es >= far ||
-                        a.ldw * es >= far;
+    if (!on_grid(workspace, 0, 1, 16)) return BIGEMM_ERR_INVALID_ARG;
+    bool gather = !addressable(a.x, a.ldx, es) || !addressable(a.w, a.ldw, es);
+    const uint64_t pack_bytes = workspace_for(a.M, a.N, a.K, es, a.x, a.ldx, a.w, a.ldw);
+    if (workspace && pack_bytes > 0 && workspace_bytes >= pack_bytes) {
+        if (pack(a, es, static_cast<uint8_t *>(workspace), (cudaStream_t)stream) != cudaSuccess) return BIGEMM_ERR_CUDA;
+        gather = false;
+    }
     a.seg_blocks = a.out_dt == BIGEMM_F32 ? full_segment(mx) : a.k_blocks;
     const Choice pick = choose(a, ds->sm_count, gather);
     if (pick.many) {
@@ -179,7 +219,7 @@ bigemm_status product(MatmulArgs &a, void *stream)
         const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, nt = (a.N + bn - 1ll) / bn;
         if (mt * nt > 0x7fffffff) return BIGEMM_ERR_UNSUPPORTED;
         a.m_tiles = (int)mt, a.n_tiles = (int)nt;
-        a.by_rows = on_grid(a.out, a.ldo, os, 16) && a.ldo * os < far && (a.combine == BIGEMM_COMBINE_NONE || a.vec_other);
+        a.by_rows = on_grid(a.out, a.ldo, os, 16) && a.ldo * os < kFar && (a.combine == BIGEMM_COMBINE_NONE || a.vec_other);
         ManyMaps maps = {};
         if (!operand_map(&maps.x, a.x, a.in_dt, a.M, a.K, a.ldx, 128) ||
             !operand_map(&maps.w, a.w, a.in_dt, a.N, a.K, a.ldw, bn / 2) ||
@@ -204,10 +244,17 @@ bigemm_status product(MatmulArgs &a, void *stream)
 
 extern "C" {
 
+uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx, const void *w,
+                                int64_t ldw)
+{
+    if (M < 1 || N < 1 || K < 1 || in_dtype < BIGEMM_F16 || in_dtype > BIGEMM_MXF8) return 0;
+    return workspace_for(M, N, K, in_dtype == BIGEMM_MXF8 ? 1 : 2, x, ldx, w, ldw);
+}
+
 bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx, const void *w,
                          int64_t ldw, const float *bias, int act, int combine, bigemm_dtype other_dtype,
                          const void *other, int64_t ldother, bigemm_dtype out_dtype, void *out, int64_t ldo,
-                         void *stream)
+                         void *workspace, uint64_t workspace_bytes, void *stream)
 {
     if (in_dtype < BIGEMM_F32 || in_dtype > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
     if (out_dtype < BIGEMM_F32 || out_dtype > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
@@ -216,13 +263,14 @@ bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void 
     a.M = M, a.N = N, a.K = K, a.in_dt = in_dtype, a.out_dt = out_dtype, a.other_dt = other_dtype;
     a.act = act, a.combine = combine, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.ldo = ldo, a.ldother = ldother;
     a.bias = bias, a.other = other, a.out = out;
-    return product(a, stream);
+    return product(a, workspace, workspace_bytes, stream);
 }
 
 bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, const void *x_scale, const void *w,
                             int64_t ldw, const void *w_scale, const float *bias, int act, int combine,
                             bigemm_dtype other_dtype, const void *other, int64_t ldother, bigemm_dtype out_dtype,
-                            void *out, int64_t ldo, void *out_scale, void *stream)
+                            void *out, int64_t ldo, void *out_scale, void *workspace, uint64_t workspace_bytes,
+                            void *stream)
 {
     if (out_dtype < BIGEMM_F32 || out_dtype > BIGEMM_MXF8) return BIGEMM_ERR_INVALID_ARG;
     MatmulArgs a = {};
@@ -230,7 +278,7 @@ bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, con
     a.act = act, a.combine = combine, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.ldo = ldo, a.ldother = ldother;
     a.xs = static_cast<const uint8_t *>(x_scale), a.ws = static_cast<const uint8_t *>(w_scale);
     a.bias = bias, a.other = other, a.out = out, a.outs = static_cast<uint8_t *>(out_scale);
-    return product(a, stream);
+    return product(a, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -371,4 +371,16 @@ struct ManyMaps {
 };
 cudaError_t launch_matmul_many(const MatmulArgs &a, int bn, int sms, const ManyMaps &maps, cudaStream_t stream);
 
+// Operands copied to rows on the 16-byte grid (matmul_pack.cu); rows = 0: none.
+struct PackOperand {
+    const uint8_t *src;
+    uint8_t *dst;
+    long long rows, src_pitch, dst_pitch, bytes, runs;     // bytes: of a row
+};
+struct PackArgs {
+    PackOperand op[2];
+    long long items0;
+};
+cudaError_t launch_matmul_pack(PackArgs &a, cudaStream_t stream);
+
 }  // namespace bigemm

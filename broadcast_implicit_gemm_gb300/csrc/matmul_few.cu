@@ -14,7 +14,8 @@
 // 14.4 against 10.9.)
 //
 // GATHER: rows that TMA cannot address (a stride or base off the 16-byte grid)
-// are brought into the same swizzled stages by six more warps with plain loads.
+// are brought into the same swizzled stages by eight more warps, which load a
+// stage ahead of the one they write.
 //
 // MX: e4m3 operands; a stage's 128 bytes of a row are 128 elements, whose
 // scales are one block of 512 bytes per operand.  They land beside the stage
@@ -25,13 +26,14 @@
 // 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
 #include "matmul.cuh"
+#include "unaligned.cuh"
 
 namespace bigemm {
 
 namespace {
 
 constexpr int kFewThreads = 256;               // producer, MMA, two idle warps, four that drain
-constexpr int kGatherWarps = 6;
+constexpr int kGatherWarps = 8;
 constexpr int kFewA = 128 * kRow;              // bytes of weights per stage
 
 constexpr int kFewStages = 8;                  // at most
@@ -63,28 +65,13 @@ constexpr uint32_t few_cols()
     return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
-// One 16-byte piece of a row's 128-byte block, byte by byte where it has to
-// be: `size`-byte elements, `have` of them inside the row.
-__device__ __forceinline__ uint4 gather16(const uint8_t *p, int size, int have)
-{
-    uint32_t q[4] = {0, 0, 0, 0};
-    if (size == 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < have) q[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < have) q[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-    }
-    return make_uint4(q[0], q[1], q[2], q[3]);
-}
-
 template <bool GATHER>
 constexpr int few_threads() { return kFewThreads + (GATHER ? 32 * kGatherWarps : 0); }
 
+// (Gathering warps hold a stage's pieces in registers: two CTAs share an SM
+// where 64 of them are enough.)
 template <int BN, bool MX, bool GATHER, bool FULL>
-__global__ void __launch_bounds__(few_threads<GATHER>())
+__global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <= 32 ? 2 : 1)
     matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                       const MatmulArgs p)
 {
@@ -151,36 +138,53 @@ __global__ void __launch_bounds__(few_threads<GATHER>())
         uint32_t phase = 0, last_parity[kFewStages];
         bool issued[kFewStages];
         for (int i = 0; i < kFewStages; ++i) issued[i] = false, last_parity[i] = 0;
+        // GATHER: thread t brings piece t % 8 of rows t / 8, + 32, ...: four of the weights', then the tokens'
+        constexpr int kPieces = GATHER ? 4 + (BN + 31) / 32 : 1;
+        const int t = (int)threadIdx.x - kFewThreads, c16 = t & 7;
+        const long long k_bytes = (long long)p.K * esize;
+        const Span w_span = {static_cast<const uint8_t *>(p.w),
+                             static_cast<const uint8_t *>(p.w) + ((long long)(p.N - 1) * p.ldw + p.K) * esize};
+        const Span x_span = {static_cast<const uint8_t *>(p.x),
+                             static_cast<const uint8_t *>(p.x) + ((long long)(p.M - 1) * p.ldx + p.K) * esize};
+        Wide held[kPieces];
+        auto in_row = [&](int j, int kb) {          // bytes of piece j that are in its row
+            const int row = (t >> 3) + 32 * (j & 3);
+            const bool there = j < 4 ? n0 + (t >> 3) + 32 * j < p.N : row < BN && m0 + row < p.M;
+            const long long left = k_bytes - ((long long)kb * kRow + c16 * 16);
+            return there ? (int)max(0ll, min(16ll, left)) : 0;
+        };
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int row = (t >> 3) + 32 * (j & 3);
+                const uint8_t *from = j < 4 ? w_span.begin + (long long)(n0 + row) * p.ldw * esize
+                                            : x_span.begin + (long long)(m0 + row) * p.ldx * esize;
+                held[j] = wide_load(from + (long long)kb * kRow + c16 * 16, 0, in_row(j, kb), j < 4 ? w_span : x_span);
+            }
+        };
+        if (GATHER && kb0 < kb1) fetch(kb0);
         for (int kb = kb0; good && kb < kb1; ++kb) {
             uint8_t *a_dst = sa + stage * kFewA, *b_dst = sb + stage * BN * kRow;
             uint8_t *s_dst = ss + stage * 2 * kMxBlockBytes;
             good = mbar_wait_warp(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
             if (!good) break;
             if (GATHER) {
-                const int t = (int)threadIdx.x - kFewThreads;
-                const long long e0 = (long long)kb * per;
-                for (int i = t; i < (128 + BN) * 8; i += 32 * kGatherWarps) {
-                    const bool is_w = i < 128 * 8;
-                    const int j = is_w ? i : i - 128 * 8, row = j >> 3, c16 = j & 7;
-                    const long long r = is_w ? (long long)n0 + row : (long long)m0 + row;
-                    const int have = r < (is_w ? p.N : p.M)
-                                         ? (int)min((long long)(16 / esize), max(0ll, p.K - e0 - c16 * (16 / esize)))
-                                         : 0;
-                    const uint8_t *src = static_cast<const uint8_t *>(is_w ? p.w : p.x) +
-                                         (r * (is_w ? p.ldw : p.ldx) + e0 + c16 * (16 / esize)) * esize;
-                    uint8_t *dst = (is_w ? a_dst : b_dst) + row * kRow + ((c16 ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(dst) = gather16(src, esize, have);
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    const int row = (t >> 3) + 32 * (j & 3);
+                    if (j >= 4 && row >= BN) continue;
+                    *reinterpret_cast<uint4 *>((j < 4 ? a_dst : b_dst) + row * kRow + ((c16 ^ (row & 7)) << 4)) =
+                        wide_take(held[j], 0, in_row(j, kb));
                 }
-                if (MX) {
-                    for (int i = t; i < 64; i += 32 * kGatherWarps) {
-                        const bool is_w = i < 32;
-                        const long long blk = (is_w ? n0 >> 7 : m0 >> 7) * (long long)xblocks + kb;
-                        *reinterpret_cast<uint4 *>(s_dst + i * 16) = *reinterpret_cast<const uint4 *>(
-                            (is_w ? p.ws : p.xs) + blk * kMxBlockBytes + (i & 31) * 16);
-                    }
+                if (MX && t < 64) {
+                    const bool is_w = t < 32;
+                    const long long blk = (is_w ? n0 >> 7 : m0 >> 7) * (long long)xblocks + kb;
+                    *reinterpret_cast<uint4 *>(s_dst + t * 16) = *reinterpret_cast<const uint4 *>(
+                        (is_w ? p.ws : p.xs) + blk * kMxBlockBytes + (t & 31) * 16);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&full[stage]);
+                if (kb + 1 < kb1) fetch(kb + 1);
             } else if (lane == 0) {
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)(kFewA + BN * kRow + (MX ? 2 * kMxBlockBytes : 0)));
                 issued[stage] = true;

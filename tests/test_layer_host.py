@@ -17,12 +17,12 @@ def lib():
 
 def matmul(lib, M=4, N=8, K=16, dt=F16, x=256, ldx=16, w=256, ldw=16, bias=None, act=0, comb=0, odt=F16, o=None, ldo2=0,
            out_dt=F16, out=256, ldo=8):
-    return lib.matmul_run(M, N, K, dt, x, ldx, w, ldw, bias, act, comb, odt, o, ldo2, out_dt, out, ldo, None)
+    return lib.matmul_run(M, N, K, dt, x, ldx, w, ldw, bias, act, comb, odt, o, ldo2, out_dt, out, ldo, None, 0, None)
 
 
 def matmul_mx(lib, M=4, N=8, K=16, x=256, ldx=16, xs=256, w=256, ldw=16, ws=256, bias=None, act=0, comb=0, odt=F16, o=None,
               ldo2=0, out_dt=F16, out=256, ldo=8, outs=None):
-    return lib.matmul_mx_run(M, N, K, x, ldx, xs, w, ldw, ws, bias, act, comb, odt, o, ldo2, out_dt, out, ldo, outs, None)
+    return lib.matmul_mx_run(M, N, K, x, ldx, xs, w, ldw, ws, bias, act, comb, odt, o, ldo2, out_dt, out, ldo, outs, None, 0, None)
 
 
 def norm(lib, rows=2, cols=8, dt=F16, x=256, ldx=8, r=None, ldr=0, g=None, h=None, ldh=0, out_dt=F16, out=256, ldo=8, s=None):
@@ -86,3 +86,14 @@ def test_python_refusals():
     for call in (lambda: bg.matmul(x, x), lambda: bg.rmsnorm(x), lambda: bg.mx_quantize(x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_workspace_bytes(lib):
+    """Only for operands off the 16-byte grid, and for many tokens: a copy of each such operand, rows on the grid."""
+    q = bg.matmul_workspace_bytes
+    assert q(1000, 512, 256, F16, 256, 256, 256, 256) == 0
+    assert q(1000, 512, 257, F16, 256, 257, 256, 264) == -(-1000 * 528 // 256) * 256
+    assert q(1000, 512, 257, F16, 256, 264, 256, 257) == -(-512 * 528 // 256) * 256
+    assert q(1000, 512, 256, F16, 258, 256, 258, 256) == 1000 * 512 + 512 * 512
+    assert q(1000, 512, 250, MX, 256, 250, 256, 256) == 1000 * 256
+    assert q(1, 512, 257, F16, 256, 257, 256, 257) == 0 and q(0, 5, 5, F16, 256, 5, 256, 5) == 0
