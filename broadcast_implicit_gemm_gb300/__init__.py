@@ -404,7 +404,7 @@ def _layer():
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_layer", path, loader=loader))
         loader.exec_module(module)
         module.init((torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn),
-                    (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                    (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _workspace,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
                                     lib.matmul_workspace_bytes)))
@@ -412,19 +412,21 @@ def _layer():
     return _layer_module
 
 
-def _status(status, where, again, x, stream=None):
-    """Raise for a status that is not OK.  -1: x's device was not the current one, call again with it current;
-    -1 - n: call again with a workspace of n bytes."""
+def _workspace(n, x, stream):
+    """n bytes on x's device for a call on the given stream (None: the current one)."""
     import torch
-    workspace = None
-    with torch.cuda.device(x.device):
-        while status < 0:
-            if status < -1:
-                workspace = torch.empty(-1 - status, dtype=torch.uint8, device=x.device)
-                if stream is not None:      # its memory is not given out again before that stream is done
-                    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-                    workspace.record_stream(s)
-            status = again(workspace)
+    t = torch.empty(n, dtype=torch.uint8, device=x.device)
+    if stream is not None:      # the memory is not given out again before that stream is done with the call
+        t.record_stream(torch.cuda.ExternalStream(stream, device=x.device) if isinstance(stream, int) else stream)
+    return t
+
+
+def _status(status, where, again, x):
+    """Raise for a status that is not OK; if x's device was not the current one (-1), call again with it current."""
+    if status == -1:
+        import torch
+        with torch.cuda.device(x.device):
+            status = again()
     if status != 0:
         raise BigemmError(status, where)
 
@@ -465,9 +467,9 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
     if out is None or out_dtype is not None:
         out = _output(out, out_dtype, x.dtype, x.shape[0], w.shape[0], x.device)
     args = (x, None, w, None, bias, act, other, combine, out, None, stream)
-    status = (_layer_module or _layer()).product(*args, None)
+    status = (_layer_module or _layer()).product(*args)
     if status:
-        _status(status, "matmul", lambda workspace: _layer().product(*args, workspace), x, stream)
+        _status(status, "matmul", lambda: _layer().product(*args), x)
     return out
 
 
@@ -482,9 +484,9 @@ def matmul_mx(x, x_scale, w, w_scale, bias=None, act=ACT_NONE, other=None, combi
         out = _output(out, out_dtype, torch.bfloat16, x.shape[0], w.shape[0], x.device)
     out_scale = _output_scales(out, out_scale)
     args = (x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream)
-    status = (_layer_module or _layer()).product(*args, None)
+    status = (_layer_module or _layer()).product(*args)
     if status:
-        _status(status, "matmul_mx", lambda workspace: _layer().product(*args, workspace), x, stream)
+        _status(status, "matmul_mx", lambda: _layer().product(*args), x)
     return out if out_scale is None else (out, out_scale)
 
 
@@ -502,7 +504,7 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, o
     args = (x, weight, residual, eps, sum_out, out, out_scale, stream)
     status = (_layer_module or _layer()).norm(*args)
     if status:
-        _status(status, "rmsnorm", lambda workspace: _layer().norm(*args), x)
+        _status(status, "rmsnorm", lambda: _layer().norm(*args), x)
     if residual is None:
         return out if out_scale is None else (out, out_scale)
     return (out, sum_out) if out_scale is None else (out, out_scale, sum_out)
@@ -518,5 +520,5 @@ def mx_quantize(x, out=None, scale=None, stream=None):
     args = (x, out, scale, stream)
     status = (_layer_module or _layer()).quantize(*args)
     if status:
-        _status(status, "mx_quantize", lambda workspace: _layer().quantize(*args), x)
+        _status(status, "mx_quantize", lambda: _layer().quantize(*args), x)
     return out, scale

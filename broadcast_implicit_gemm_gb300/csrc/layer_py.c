@@ -15,7 +15,7 @@ enum { DT_COUNT = 4, OTHER_DEVICE = -1 };
 
 static PyObject *g_dtypes[DT_COUNT];                 /* torch dtypes of F32, F16, BF16, MXF8 */
 static PyObject *g_scale_types[2];                   /* uint8, float8_e8m0fnu */
-static PyObject *g_current_stream, *g_current_device;
+static PyObject *g_current_stream, *g_current_device, *g_workspace;
 static PyObject *s_shape, *s_stride, *s_device, *s_ptr, *s_dtype, *s_numel, *s_contiguous;
 
 static bigemm_status (*p_matmul)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *,
@@ -215,14 +215,12 @@ static int arity(const char *name, Py_ssize_t got, Py_ssize_t want)
     return -1;
 }
 
-/* product(x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream, workspace) -> status, or
- * -1 - n where a workspace of n bytes is wanted and none is given */
+/* product(x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream) -> status */
 static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix x, w, o = {0}, y;
     void *xs = NULL, *ws = NULL, *ys = NULL, *bias, *stream, *space = NULL;
-    long long space_bytes = 0;
-    if (arity("product", n, 12) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 ||
+    if (arity("product", n, 11) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 ||
         matrix(a[2], "w", &w, x.device, -1, x.cols) < 0)
         return NULL;
     if (w.dtype != x.dtype) return PyErr_Format(PyExc_TypeError, "w: of another dtype than x");
@@ -244,22 +242,34 @@ static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const int r = stream_on(a[10], x.device, &stream);
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
-    if (a[11] != Py_None) {
-        if (pointer_of(a[11], &space) < 0 || as_ll(PyObject_CallMethodNoArgs(a[11], s_numel), &space_bytes) < 0) return NULL;
-    } else if (x.rows > 0) {
-        const uint64_t want = p_workspace((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld);
-        if (want > 0) return PyLong_FromLongLong(-1 - (long long)want);
+    PyObject *workspace = NULL;
+    uint64_t bytes = 0;
+    if (x.rows > 0)
+        bytes = p_workspace((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld);
+    if (bytes > 0) {
+        /* torch's memory, the stream's until the call is done: it may be given out again after this returns */
+        PyObject *b = PyLong_FromUnsignedLongLong(bytes);
+        if (!b) return NULL;
+        PyObject *const args[3] = {b, a[0], a[10]};
+        workspace = PyObject_Vectorcall(g_workspace, args, 3, NULL);
+        Py_DECREF(b);
+        if (!workspace) return NULL;
+        if (pointer_of(workspace, &space) < 0) {
+            Py_DECREF(workspace);
+            return NULL;
+        }
     }
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (mx)
         st = p_matmul_mx((int)x.rows, (int)w.rows, (int)x.cols, x.ptr, x.ld, xs, w.ptr, w.ld, ws, bias, act, combine,
-                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, space, (uint64_t)space_bytes, stream);
+                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, space, bytes, stream);
     else
         st = p_matmul((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld, bias, act,
-                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, space, (uint64_t)space_bytes,
+                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, space, bytes,
                       stream);
     Py_END_ALLOW_THREADS
+    Py_XDECREF(workspace);
     return PyLong_FromLong(st);
 }
 
@@ -309,12 +319,12 @@ static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-/* init(dtypes, scale_types, current_stream, current_device, functions) */
+/* init(dtypes, scale_types, current_stream, current_device, workspace, functions) */
 static PyObject *init(PyObject *self, PyObject *args)
 {
-    PyObject *d, *st, *cs, *cd;
+    PyObject *d, *st, *cs, *cd, *ws;
     unsigned long long f[5];
-    if (!PyArg_ParseTuple(args, "O!O!OO(KKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &f[0], &f[1], &f[2], &f[3],
+    if (!PyArg_ParseTuple(args, "O!O!OOO(KKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &f[0], &f[1], &f[2], &f[3],
                           &f[4]))
         return NULL;
     if (PyTuple_GET_SIZE(d) != DT_COUNT || PyTuple_GET_SIZE(st) != 2)
@@ -323,6 +333,7 @@ static PyObject *init(PyObject *self, PyObject *args)
     for (int i = 0; i < 2; ++i) g_scale_types[i] = Py_NewRef(PyTuple_GET_ITEM(st, i));
     g_current_stream = Py_NewRef(cs);
     g_current_device = Py_NewRef(cd);
+    g_workspace = Py_NewRef(ws);
     p_matmul = (void *)(uintptr_t)f[0];
     p_matmul_mx = (void *)(uintptr_t)f[1];
     p_norm = (void *)(uintptr_t)f[2];

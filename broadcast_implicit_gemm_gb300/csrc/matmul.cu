@@ -110,7 +110,7 @@ long long many_cost(const MatmulArgs &a, int sms, int bn)
 // 256 x 4096 x 4096 17.7 us (64 tokens, K in 2) against 20.4 and 24.4 in pairs,
 // 512 x 4096 x 4096 25 against 20.9 and 24.7, 1024 x 1024 x 8192 25.5 against
 // 34.5 and 40.9.
-Choice choose(const MatmulArgs &a, int sms, bool gather)
+Choice choose(const MatmulArgs &a, int sms)
 {
     const bool full = a.out_dt == BIGEMM_F32;      // its running sums are in registers: at most 64 tokens
     Choice c = {};
@@ -122,9 +122,9 @@ Choice choose(const MatmulArgs &a, int sms, bool gather)
     long long least = few_cost(a, sms, c.few);
     if (!full) {
         const FewCut large = cut_few(a, sms, 128, true);
-        if (gather || few_cost(a, sms, large) < least) c.few = large, least = few_cost(a, sms, large);
+        if (few_cost(a, sms, large) < least) c.few = large, least = few_cost(a, sms, large);
     }
-    for (int bn = 128; bn <= 256 && !gather; bn += 128) {
+    for (int bn = 128; bn <= 256; bn += 128) {
         const long long cost = many_cost(a, sms, bn);
         if (cost < least) c.many = true, c.bn = bn, least = cost;
     }
@@ -143,21 +143,19 @@ constexpr long long kFar = 1ll << 40;           // TMA: strides below 2^40 bytes
 // Whether TMA can address an operand's rows.
 bool addressable(const void *p, long long ld, long long es) { return on_grid(p, ld, es, 16) && ld * es < kFar; }
 
-// More tokens than this, and operands off the 16-byte grid are better copied
-// onto it first than gathered by the product: @
-constexpr int kPackTokens = 128;
-
 long long packed_bytes(long long rows, long long cols, long long es) { return up(rows * up(cols * es, 16) * 16, 256) * 256; }
 
 uint64_t workspace_for(long long M, long long N, long long K, long long es, const void *x, long long ldx, const void *w,
                        long long ldw)
 {
-    if (M <= kPackTokens) return 0;
     return (uint64_t)((addressable(w, ldw, es) ? 0 : packed_bytes(N, K, es)) +
                       (addressable(x, ldx, es) ? 0 : packed_bytes(M, K, es)));
 }
 
-// Copies what TMA cannot address to `workspace` and makes it the operand; w first.
+// Copies what TMA cannot address to `workspace` and makes it the operand; w
+// first.  (Warps that brought such rows into the product's stages themselves, by
+// aligned loads and shifts, took 26.5 us for 1 x 4097 x 4097 bf16 against 20.7,
+// 6.5 for 8 x 64 x 65 against 5.0, 360 for 1000 x 4096 x 4097 against 45.)
 cudaError_t pack(MatmulArgs &a, long long es, uint8_t *workspace, cudaStream_t stream)
 {
     PackArgs k = {};
@@ -197,23 +195,20 @@ bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, 
         if (!a.other || a.ldother < a.N || !on_grid(a.other, 0, 1, ts)) return BIGEMM_ERR_INVALID_ARG;
         a.vec_other = on_grid(a.other, a.ldother, ts, 16);
     }
+    const uint64_t space = workspace_for(a.M, a.N, a.K, es, a.x, a.ldx, a.w, a.ldw);
+    if (!on_grid(workspace, 0, 1, 16) || (space > 0 && (!workspace || workspace_bytes < space)))
+        return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();
     if (!ds) return BIGEMM_ERR_CUDA;
     a.vec_out = on_grid(a.out, a.ldo, os, a.out_dt == BIGEMM_MXF8 ? 8 : 16);
     a.vec_bias = on_grid(a.bias, 0, 1, 16);
     a.k_blocks = (int)((a.K * es + kRow - 1) / kRow);
-    if (a.M == 1) a.ldx = (a.ldx + 15) / 16 * 16;   // the stride of a single row is free
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
-    if (!on_grid(workspace, 0, 1, 16)) return BIGEMM_ERR_INVALID_ARG;
-    bool gather = !addressable(a.x, a.ldx, es) || !addressable(a.w, a.ldw, es);
-    const uint64_t pack_bytes = workspace_for(a.M, a.N, a.K, es, a.x, a.ldx, a.w, a.ldw);
-    if (workspace && pack_bytes > 0 && workspace_bytes >= pack_bytes) {
-        if (pack(a, es, static_cast<uint8_t *>(workspace), (cudaStream_t)stream) != cudaSuccess) return BIGEMM_ERR_CUDA;
-        gather = false;
-    }
+    if (space > 0 && pack(a, es, static_cast<uint8_t *>(workspace), (cudaStream_t)stream) != cudaSuccess)
+        return BIGEMM_ERR_CUDA;
     a.seg_blocks = a.out_dt == BIGEMM_F32 ? full_segment(mx) : a.k_blocks;
-    const Choice pick = choose(a, ds->sm_count, gather);
+    const Choice pick = choose(a, ds->sm_count);
     if (pick.many) {
         const int bn = pick.bn;
         const long long mt = (a.M + kManyTokens - 1ll) / kManyTokens, nt = (a.N + bn - 1ll) / bn;
@@ -233,10 +228,10 @@ bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, 
     if ((a.M + (long long)cut.bn - 1) / cut.bn > 65535) return BIGEMM_ERR_UNSUPPORTED;
     a.split = cut.split;
     CUtensorMap mw = {}, mxm = {};
-    if (!gather && (!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
+    if ((!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
                     !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn)))
         return BIGEMM_ERR_CUDA;
-    const cudaError_t e = launch_matmul_few(a, cut, gather, mw, mxm, (cudaStream_t)stream);
+    const cudaError_t e = launch_matmul_few(a, cut, mw, mxm, (cudaStream_t)stream);
     return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
 }
 

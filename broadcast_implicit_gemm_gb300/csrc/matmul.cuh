@@ -360,8 +360,8 @@ struct FewCut {
     int bn, split;
     bool alone;
 };
-cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
-                              const CUtensorMap &map_x, cudaStream_t stream);
+cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, const CUtensorMap &map_w, const CUtensorMap &map_x,
+                              cudaStream_t stream);
 
 // The kernel for many tokens (matmul_many.cu): tiles of 256 tokens by bn (128 or
 // 256) channels.  maps: x, w, scales of x, scales of w, out.

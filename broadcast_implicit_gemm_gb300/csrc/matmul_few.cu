@@ -13,10 +13,6 @@
 // second barrier: one token through 4096 x 4096 bf16 8.1 us against 7.8, 64 tokens
 // 14.4 against 10.9.)
 //
-// GATHER: rows that TMA cannot address (a stride or base off the 16-byte grid)
-// are brought into the same swizzled stages by eight more warps, which load a
-// stage ahead of the one they write.
-//
 // MX: e4m3 operands; a stage's 128 bytes of a row are 128 elements, whose
 // scales are one block of 512 bytes per operand.  They land beside the stage
 // and go to tensor memory columns of that stage before its MMAs.
@@ -26,14 +22,12 @@
 // 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
 #include "matmul.cuh"
-#include "unaligned.cuh"
 
 namespace bigemm {
 
 namespace {
 
 constexpr int kFewThreads = 256;               // producer, MMA, two idle warps, four that drain
-constexpr int kGatherWarps = 8;
 constexpr int kFewA = 128 * kRow;              // bytes of weights per stage
 
 constexpr int kFewStages = 8;                  // at most
@@ -65,13 +59,8 @@ constexpr uint32_t few_cols()
     return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
-template <bool GATHER>
-constexpr int few_threads() { return kFewThreads + (GATHER ? 32 * kGatherWarps : 0); }
-
-// (Gathering warps hold a stage's pieces in registers: two CTAs share an SM
-// where 64 of them are enough.)
-template <int BN, bool MX, bool GATHER, bool FULL>
-__global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <= 32 ? 2 : 1)
+template <int BN, bool MX, bool FULL>
+__global__ void __launch_bounds__(kFewThreads)
     matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                       const MatmulArgs p)
 {
@@ -96,21 +85,18 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
     const int ct = (int)blockIdx.x / split, n0 = ct * 128;
     const int m0 = (int)blockIdx.y * BN;
     const int kb0 = (int)((long long)rank * p.k_blocks / split), kb1 = (int)((long long)(rank + 1) * p.k_blocks / split);
-    const int xblocks = p.k_blocks;                  // MX: blocks of scales per block row
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], GATHER ? 32 * kGatherWarps : 1);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if (!GATHER) {
-            tma_prefetch_desc(&map_w);
-            tma_prefetch_desc(&map_x);
-        }
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_x);
     }
     if (warp == 1) {
         __syncwarp();
@@ -131,83 +117,38 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
         for (int i = 0; i < (FULL ? BN : 1); ++i) acc[i] = 0.f;
     }
 
-    if (GATHER ? warp >= 8 : warp == 0) {
-        // ------------------------------------------------------ producers
-        const int esize = MX ? 1 : 2, per = kRow / esize;      // elements per stage row
-        int stage = 0;
-        uint32_t phase = 0, last_parity[kFewStages];
-        bool issued[kFewStages];
-        for (int i = 0; i < kFewStages; ++i) issued[i] = false, last_parity[i] = 0;
-        // GATHER: thread t brings piece t % 8 of rows t / 8, + 32, ...: four of the weights', then the tokens'
-        constexpr int kPieces = GATHER ? 4 + (BN + 31) / 32 : 1;
-        const int t = (int)threadIdx.x - kFewThreads, c16 = t & 7;
-        const long long k_bytes = (long long)p.K * esize;
-        const Span w_span = {static_cast<const uint8_t *>(p.w),
-                             static_cast<const uint8_t *>(p.w) + ((long long)(p.N - 1) * p.ldw + p.K) * esize};
-        const Span x_span = {static_cast<const uint8_t *>(p.x),
-                             static_cast<const uint8_t *>(p.x) + ((long long)(p.M - 1) * p.ldx + p.K) * esize};
-        Wide held[kPieces];
-        auto in_row = [&](int j, int kb) {          // bytes of piece j that are in its row
-            const int row = (t >> 3) + 32 * (j & 3);
-            const bool there = j < 4 ? n0 + (t >> 3) + 32 * j < p.N : row < BN && m0 + row < p.M;
-            const long long left = k_bytes - ((long long)kb * kRow + c16 * 16);
-            return there ? (int)max(0ll, min(16ll, left)) : 0;
-        };
-        auto fetch = [&](int kb) {
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                const int row = (t >> 3) + 32 * (j & 3);
-                const uint8_t *from = j < 4 ? w_span.begin + (long long)(n0 + row) * p.ldw * esize
-                                            : x_span.begin + (long long)(m0 + row) * p.ldx * esize;
-                held[j] = wide_load(from + (long long)kb * kRow + c16 * 16, 0, in_row(j, kb), j < 4 ? w_span : x_span);
-            }
-        };
-        if (GATHER && kb0 < kb1) fetch(kb0);
-        for (int kb = kb0; good && kb < kb1; ++kb) {
-            uint8_t *a_dst = sa + stage * kFewA, *b_dst = sb + stage * BN * kRow;
-            uint8_t *s_dst = ss + stage * 2 * kMxBlockBytes;
-            good = mbar_wait_warp(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
-            if (!good) break;
-            if (GATHER) {
-#pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    const int row = (t >> 3) + 32 * (j & 3);
-                    if (j >= 4 && row >= BN) continue;
-                    *reinterpret_cast<uint4 *>((j < 4 ? a_dst : b_dst) + row * kRow + ((c16 ^ (row & 7)) << 4)) =
-                        wide_take(held[j], 0, in_row(j, kb));
-                }
-                if (MX && t < 64) {
-                    const bool is_w = t < 32;
-                    const long long blk = (is_w ? n0 >> 7 : m0 >> 7) * (long long)xblocks + kb;
-                    *reinterpret_cast<uint4 *>(s_dst + t * 16) = *reinterpret_cast<const uint4 *>(
-                        (is_w ? p.ws : p.xs) + blk * kMxBlockBytes + (t & 31) * 16);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&full[stage]);
-                if (kb + 1 < kb1) fetch(kb + 1);
-            } else if (lane == 0) {
+    if (warp == 0) {
+        // ------------------------------------------------------ producer
+        if (lane == 0) {
+            constexpr int per = MX ? kRow : kRow / 2;         // elements of K per stage
+            int stage = 0;
+            uint32_t phase = 0, last_parity[kFewStages];
+            bool issued[kFewStages];
+            for (int i = 0; i < kFewStages; ++i) issued[i] = false, last_parity[i] = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                good = mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
+                if (!good) break;
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)(kFewA + BN * kRow + (MX ? 2 * kMxBlockBytes : 0)));
-                issued[stage] = true;
-                last_parity[stage] = phase;
-                tma_load_2d(a_dst, &map_w, &full[stage], kb * per, n0);
-                tma_load_2d(b_dst, &map_x, &full[stage], kb * per, m0);
+                issued[stage] = true, last_parity[stage] = phase;
+                tma_load_2d(sa + stage * kFewA, &map_w, &full[stage], kb * per, n0);
+                tma_load_2d(sb + stage * BN * kRow, &map_x, &full[stage], kb * per, m0);
                 if (MX) {
-                    bulk_load(s_dst, p.ws + ((long long)(n0 >> 7) * xblocks + kb) * kMxBlockBytes, kMxBlockBytes,
+                    uint8_t *s = ss + stage * 2 * kMxBlockBytes;
+                    bulk_load(s, p.ws + ((long long)(n0 >> 7) * p.k_blocks + kb) * kMxBlockBytes, kMxBlockBytes,
                               &full[stage]);
-                    bulk_load(s_dst + kMxBlockBytes, p.xs + ((long long)(m0 >> 7) * xblocks + kb) * kMxBlockBytes,
+                    bulk_load(s + kMxBlockBytes, p.xs + ((long long)(m0 >> 7) * p.k_blocks + kb) * kMxBlockBytes,
                               kMxBlockBytes, &full[stage]);
                 }
+                if (++stage == S) stage = 0, phase ^= 1u;
             }
-            if (++stage == S) stage = 0, phase ^= 1u;
-        }
-        if (!GATHER && !good && lane == 0) {
-            int local_abort = 0;
-            for (int i = 0; i < S; ++i)
-                if (issued[i]) mbar_wait(&full[i], last_parity[i], p.timeout_ns, &local_abort, p.err);
+            if (!good) {
+                int local_abort = 0;
+                for (int i = 0; i < S; ++i)
+                    if (issued[i]) mbar_wait(&full[i], last_parity[i], p.timeout_ns, &local_abort, p.err);
+            }
         }
         __syncwarp();
-    }
-    if (warp == 1) {
+    } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
         if (lane == 0) {
             const uint32_t idesc = MX ? make_idesc_mx(128, BN)
@@ -259,7 +200,7 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
             }
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4) {
         // ------------------------------------------------------ drain: lane = channel, column = token
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
         int a = 0;
@@ -293,7 +234,7 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
         if (!C::beside) cluster_arrive();
         cluster_wait();
     }
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 4) {
         tc_fence_after();
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
         // slot of this rank in the owner's memory
@@ -334,7 +275,7 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
     // ---------------------------------------------------------- sum over the ranks and epilogue
     // pieces of 8 channels, 16 to a token
     const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
-    for (int i0 = 0; i0 < mine * 16; i0 += few_threads<GATHER>()) {
+    for (int i0 = 0; i0 < mine * 16; i0 += kFewThreads) {
         const int i = i0 + (int)threadIdx.x;
         const bool live = i < mine * 16;
         const int t = t0 + (live ? i >> 4 : 0), c = (i & 15) * 8;
@@ -376,12 +317,12 @@ __global__ void __launch_bounds__(few_threads<GATHER>(), GATHER && !FULL && BN <
     }
 }
 
-template <int BN, bool MX, bool GATHER, bool FULL>
+template <int BN, bool MX, bool FULL>
 cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
                        cudaStream_t stream)
 {
     a.stages = alone ? FewCfg<BN>::whole : FewCfg<BN>::half;
-    auto kern = matmul_few_kernel<BN, MX, GATHER, FULL>;
+    auto kern = matmul_few_kernel<BN, MX, FULL>;
     static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
@@ -393,7 +334,7 @@ cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &m
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.N + 127ll) / 128 * split), (unsigned)((a.M + (long long)BN - 1) / BN));
-    cfg.blockDim = dim3(few_threads<GATHER>());
+    cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = FewCfg<BN>::smem(a.stages);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -409,37 +350,30 @@ cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &m
 }
 
 template <int BN>
-cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, bool gather, const CUtensorMap &mw, const CUtensorMap &mx,
+cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
                       cudaStream_t s)
 {
     if (a.out_dt == BIGEMM_F32) {
-        if constexpr (BN <= 64) {
-            if (a.in_dt == BIGEMM_MXF8)
-                return gather ? launch_one<BN, true, true, true>(a, split, alone, mw, mx, s)
-                              : launch_one<BN, true, false, true>(a, split, alone, mw, mx, s);
-            return gather ? launch_one<BN, false, true, true>(a, split, alone, mw, mx, s)
-                          : launch_one<BN, false, false, true>(a, split, alone, mw, mx, s);
-        }
+        if constexpr (BN <= 64)
+            return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, true>(a, split, alone, mw, mx, s)
+                                          : launch_one<BN, false, true>(a, split, alone, mw, mx, s);
         return cudaErrorInvalidValue;   // 128 running sums per thread would spill
     }
-    if (a.in_dt == BIGEMM_MXF8)
-        return gather ? launch_one<BN, true, true, false>(a, split, alone, mw, mx, s)
-                      : launch_one<BN, true, false, false>(a, split, alone, mw, mx, s);
-    return gather ? launch_one<BN, false, true, false>(a, split, alone, mw, mx, s)
-                  : launch_one<BN, false, false, false>(a, split, alone, mw, mx, s);
+    return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, false>(a, split, alone, mw, mx, s)
+                                  : launch_one<BN, false, false>(a, split, alone, mw, mx, s);
 }
 
 }  // namespace
 
-cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, bool gather, const CUtensorMap &map_w,
+cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, const CUtensorMap &map_w,
                               const CUtensorMap &map_x, cudaStream_t stream)
 {
     ProfScope prof("matmul_few", stream);
     switch (cut.bn) {
-    case 16: return launch_bn<16>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
-    case 32: return launch_bn<32>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
-    case 64: return launch_bn<64>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
-    case 128: return launch_bn<128>(a, cut.split, cut.alone, gather, map_w, map_x, stream);
+    case 16: return launch_bn<16>(a, cut.split, cut.alone, map_w, map_x, stream);
+    case 32: return launch_bn<32>(a, cut.split, cut.alone, map_w, map_x, stream);
+    case 64: return launch_bn<64>(a, cut.split, cut.alone, map_w, map_x, stream);
+    case 128: return launch_bn<128>(a, cut.split, cut.alone, map_w, map_x, stream);
     default: return cudaErrorInvalidValue;
     }
 }

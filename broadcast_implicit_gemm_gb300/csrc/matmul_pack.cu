@@ -19,19 +19,19 @@ __global__ void __launch_bounds__(256) matmul_pack_kernel(const PackArgs a)
     const long long i = second ? item - a.items0 : item;
     const long long row = i / o.runs;
     if (row >= o.rows) return;
-    const int p0 = (int)(i - row * o.runs) * 32 * U + lane;
+    const long long p0 = (i - row * o.runs) * 32 * U + lane;
     const Span span = {o.src, o.src + (o.rows - 1) * o.src_pitch + o.bytes};
     const uint8_t *from = o.src + row * o.src_pitch;
     uint8_t *to = o.dst + row * o.dst_pitch;
     Wide w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int at = (p0 + 32 * u) * 16;
+        const long long at = (p0 + 32ll * u) * 16;
         w[u] = wide_load(from + at, 0, (int)max(0ll, min(16ll, o.bytes - at)), span);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int at = (p0 + 32 * u) * 16;
+        const long long at = (p0 + 32ll * u) * 16;
         if (at < o.bytes)
             *reinterpret_cast<uint4 *>(to + at) = wide_take(w[u], 0, (int)min(16ll, o.bytes - at));
     }

@@ -287,8 +287,7 @@ bigemm_status conv2d_nchw_run_noalloc(int N, int H, int W, int CO, int CI, int K
  * Matrices are row-major in device memory, rows `ld` elements apart (ld at
  * least the row's length), each base on a boundary of its element size.  Rows
  * on 16-byte boundaries take the fast paths; any other alignment is served too.
- * The calls keep no state, need no workspace (matmul_run says where one helps)
- * and allocate nothing; they are asynchronous on `stream`, and calls may overlap on different streams.  rows
+ * The calls keep no state and allocate nothing; they are asynchronous on `stream`, and calls may overlap on different streams.  rows
  * or M = 0 is a call that does nothing.
  *
  * MXF8 matrices: e4m3 elements, and a buffer of scales (16-byte aligned,
@@ -324,11 +323,10 @@ typedef enum {
  *   out [M,N] of out_dtype (F32, F16, BF16), rounded once.  For F32 at most 512
  *   products at a time (2048 of MXF8) are summed in the tensor core, the rest in
  *   fp32 adds.
- *   workspace: NULL, or device memory on a 16-byte boundary that is the call's
- *   until it is done.  With matmul_workspace_bytes of it, a product of operands
- *   off the 16-byte grid is many times faster; without, it is served all the same.
- * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum),
- * UNSUPPORTED (in_dtype F32; N or K above 2^30, more than 4 million tokens), CUDA.
+ *   workspace: matmul_workspace_bytes of device memory on a 16-byte boundary,
+ *   the call's until it is done; NULL where that is 0.
+ * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum, a
+ * workspace that is too small), UNSUPPORTED (in_dtype F32; N or K above 2^30, more than 4 million tokens), CUDA.
  */
 bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx,
                          const void *w, int64_t ldw, const float *bias, int act, int combine,
@@ -348,9 +346,9 @@ bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, con
                             void *out_scale, void *workspace, uint64_t workspace_bytes,
                             void *stream);
 
-/* Bytes of workspace with which a product of these operands (in_dtype F16, BF16
- * or MXF8) first copies those whose rows are off the 16-byte grid onto it; 0
- * where that is not needed or not worth it. */
+/* Bytes of workspace that a product of these operands (in_dtype F16, BF16 or
+ * MXF8) needs: for a copy of each whose rows are off the 16-byte grid, rows on
+ * it; 0 where none is. */
 uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, const void *x,
                                 int64_t ldx, const void *w, int64_t ldw);
 
