@@ -116,13 +116,6 @@ __device__ __forceinline__ float mm_value(uint32_t bits, int dt)
                               : __uint_as_float(bits << 16);
 }
 
-__device__ __forceinline__ float mm_load1(const void *p, long long i, int dt)
-{
-    if (dt == BIGEMM_F32) return static_cast<const float *>(p)[i];
-    if (dt == BIGEMM_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-
 // 8 16-bit values.
 __device__ __forceinline__ void mm_unpack8(const uint4 &u, int dt, float (&v)[8])
 {
@@ -160,37 +153,63 @@ __device__ __forceinline__ uint32_t mm_pack2(float a, float b, int dt)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void mm_store1(void *p, long long i, int dt, float v)
+// 8 consecutive channels of other as they lie in memory: whole words where rows
+// are on the 16-byte grid, else an element each.
+struct Raw8 {
+    uint32_t e[8];
+};
+
+__device__ __forceinline__ void mm_other8(const MatmulArgs &a, int m, int n, Raw8 &r)
 {
-    if (dt == BIGEMM_F32) static_cast<float *>(p)[i] = v;
-    else if (dt == BIGEMM_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    if (a.combine == BIGEMM_COMBINE_NONE) return;
+    const long long at = (long long)m * a.ldother + n;
+    const bool wide = a.other_dt == BIGEMM_F32;
+    if (a.vec_other && n + 8 <= a.N) {
+        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.other) + at * (wide ? 4 : 2));
+        const uint4 u = from[0];
+        r.e[0] = u.x, r.e[1] = u.y, r.e[2] = u.z, r.e[3] = u.w;
+        if (wide) {
+            const uint4 w = from[1];
+            r.e[4] = w.x, r.e[5] = w.y, r.e[6] = w.z, r.e[7] = w.w;
+        }
+    } else if (wide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.e[j] = n + j < a.N ? static_cast<const uint32_t *>(a.other)[at + j] : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.e[j] = n + j < a.N ? static_cast<const uint16_t *>(a.other)[at + j] : 0u;
+    }
 }
 
-// bias, act and combine of 8 consecutive channels from n on of token m, in
-// place; channels past N become 0.
-__device__ __forceinline__ void mm_epilogue8(const MatmulArgs &a, int m, int n, float (&v)[8])
+// act(v + b), combined with other, in place; channels past N become 0.
+__device__ __forceinline__ void mm_epilogue8(const MatmulArgs &a, int n, const float (&b)[8], const Raw8 &o, float (&v)[8])
 {
-    float b[8], o[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = a.bias && n + j < a.N ? __ldg(a.bias + n + j) : 0.f;
-    if (a.combine != BIGEMM_COMBINE_NONE) {
-        const long long at = (long long)m * a.ldother + n;
-        if (a.vec_other && n + 8 <= a.N) {
-            mm_load8(a.other, at, a.other_dt, o);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = n + j < a.N ? mm_load1(a.other, at + j, a.other_dt) : 0.f;
-        }
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += b[j];
     mm_act_all(a.act, v);
+    if (a.combine != BIGEMM_COMBINE_NONE) {
+        float f[8];
+        if (a.other_dt != BIGEMM_F32 && a.vec_other && n + 8 <= a.N) {
+            mm_unpack8(make_uint4(o.e[0], o.e[1], o.e[2], o.e[3]), a.other_dt, f);
+        } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (a.combine != BIGEMM_COMBINE_NONE) v[j] = mm_combine(a.combine, v[j], o[j]);
-        if (n + j >= a.N) v[j] = 0.f;
+            for (int j = 0; j < 8; ++j) f[j] = mm_value(o.e[j], a.other_dt);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = mm_combine(a.combine, v[j], f[j]);
     }
+    if (n + 8 > a.N) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = n + j < a.N ? v[j] : 0.f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void mm_store_each(const MatmulArgs &a, long long at, int n, const float (&v)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (n + j < a.N) static_cast<T *>(a.out)[at + j] = T(v[j]);
 }
 
 // 8 channels of a 32- or 16-bit output.
@@ -207,10 +226,12 @@ __device__ __forceinline__ void mm_store8(const MatmulArgs &a, int m, int n, con
                 make_uint4(mm_pack2(v[0], v[1], a.out_dt), mm_pack2(v[2], v[3], a.out_dt),
                            mm_pack2(v[4], v[5], a.out_dt), mm_pack2(v[6], v[7], a.out_dt));
         }
+    } else if (a.out_dt == BIGEMM_F32) {
+        mm_store_each<float>(a, at, n, v);
+    } else if (a.out_dt == BIGEMM_F16) {
+        mm_store_each<__half>(a, at, n, v);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (n + j < a.N) mm_store1(a.out, at + j, a.out_dt, v[j]);
+        mm_store_each<__nv_bfloat16>(a, at, n, v);
     }
 }
 

@@ -200,6 +200,17 @@ __global__ void __launch_bounds__(kFewThreads)
             }
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------ other comes to L2 meanwhile
+        if (p.combine != BIGEMM_COMBINE_NONE) {
+            const int es = p.other_dt == BIGEMM_F32 ? 4 : 2, bytes = min(128, p.N - n0) * es;
+            for (int t = lane; t < min(BN, p.M - m0); t += 32) {
+                const uint8_t *from = static_cast<const uint8_t *>(p.other) + ((long long)(m0 + t) * p.ldother + n0) * es;
+                for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + bytes - 1));
+            }
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------ drain: lane = channel, column = token
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
@@ -228,6 +239,15 @@ __global__ void __launch_bounds__(kFewThreads)
     // ---------------------------------------------------------- each token's sums to the rank that finishes it
     const int tokens = min(BN, p.M - m0);
     const int per_rank = split > 1 ? (tokens + split - 1) / split : tokens;
+    const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
+    // a thread finishes 8 channels, always the same ones, of every 16th token of the rank's; its bias
+    // and its first other are asked for now
+    const int c = ((int)threadIdx.x & 15) * 8;
+    float bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bias[j] = p.bias && n0 + c + j < p.N ? __ldg(p.bias + n0 + c + j) : 0.f;
+    Raw8 other;
+    if ((int)threadIdx.x < mine * 16) mm_other8(p, m0 + t0 + ((int)threadIdx.x >> 4), n0 + c, other);
     if (split > 1) {
         // the sums' memory is free: beside the stages since each peer began, over them since its
         // drain warps saw the last MMA done
@@ -274,11 +294,12 @@ __global__ void __launch_bounds__(kFewThreads)
 
     // ---------------------------------------------------------- sum over the ranks and epilogue
     // pieces of 8 channels, 16 to a token
-    const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
     for (int i0 = 0; i0 < mine * 16; i0 += kFewThreads) {
         const int i = i0 + (int)threadIdx.x;
         const bool live = i < mine * 16;
-        const int t = t0 + (live ? i >> 4 : 0), c = (i & 15) * 8;
+        const int t = t0 + (live ? i >> 4 : 0);
+        const Raw8 now = other;
+        if (i + kFewThreads < mine * 16) mm_other8(p, m0 + t0 + ((i + kFewThreads) >> 4), n0 + c, other);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -291,7 +312,7 @@ __global__ void __launch_bounds__(kFewThreads)
                 v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
                 v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
             }
-            mm_epilogue8(p, m0 + t, n0 + c, v);
+            mm_epilogue8(p, n0 + c, bias, now, v);
         }
         if (p.out_dt == BIGEMM_MXF8) {
             float m = 0.f;
@@ -369,6 +390,9 @@ cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, const CUtensorMap
                               const CUtensorMap &map_x, cudaStream_t stream)
 {
     ProfScope prof("matmul_few", stream);
+    // the scales of a 32-token tile inside a block of 128 would start at an odd column of tensor
+    // memory, which the MMA does not take
+    if (a.in_dt == BIGEMM_MXF8 && cut.bn < 64 && a.M > cut.bn) return cudaErrorInvalidValue;
     switch (cut.bn) {
     case 16: return launch_bn<16>(a, cut.split, cut.alone, map_w, map_x, stream);
     case 32: return launch_bn<32>(a, cut.split, cut.alone, map_w, map_x, stream);
