@@ -56,9 +56,8 @@ bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows, long l
     return encode_tiled(map, t, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Which kernel, and how it is cut.  The estimates are in hundredths of a
-// microsecond, from sizes measured with 16-bit operands; a block (128 bytes) of
-// K takes 1.3 to 1.4 times as long with MXFP8 ones, in every form alike.
+// Which kernel, and how it is cut: the least of estimates in nanoseconds whose
+// terms were fitted to measurements (each term says to which).
 struct Choice {
     bool many;
     int bn;          // many tokens: channels per tile
@@ -67,67 +66,72 @@ struct Choice {
 
 long long up(long long a, long long b) { return (a + b - 1) / b; }
 
-// Few tokens: tiles of the fewest tokens that hold them all (each tile reads the
-// weights again), K shared by as many CTAs as fit beside each other, two per SM
-// for small tiles, one for large ones, up to the cluster's eight, as long as
-// each keeps four blocks.
-//   64 x 4096 x 4096: 23.3 us with K whole, 15.2 in 2, 11.5 in 4 (128 CTAs), 14.5 in 8
-//   1 x 4096 x 4096: 19.2, 12.1, 8.5 and 8.1 us
-FewCut cut_few(const MatmulArgs &a, int sms, int bn, bool alone)
-{
-    const long long tiles = up(a.N, 128) * up(a.M, bn), room = (alone ? 1 : 2) * (long long)sms;
-    const long long most = std::min<long long>(a.k_blocks / 4, room / tiles);
-    FewCut c;
-    c.bn = bn;
-    // clusters of 5 to 7 leave SMs of their processor cluster idle (300 x 1000 x 2048: 13.6 us in 7, 8.9 in 4)
-    c.split = most >= 8 ? 8 : most >= 4 ? 4 : most >= 1 ? (int)most : 1;
-    c.alone = alone && tiles * c.split <= sms;
-    return c;
-}
-
-// A wave of it: a start and an end of 5.7 us, and per block of K 0.33 us for a
-// CTA alone on its SM with 128 tokens, 0.37 for two with 64 each, 0.52 for two
-// with 128.
+// Few tokens: bn tokens per tile, `split` CTAs on a tile's K.  A start and an end
+// of 3.6 us; a block of K (128 bytes of each row) in 0.165 us, or as long as it
+// takes to reach an SM that `beside` CTAs share, (128 + bn) rows at 1 ns each;
+// 23 ns per token that a CTA finishes and 22 per token of the tile.  N = K = 1024
+// bf16: 12.0, 9.4 and 7.8 us for 128 tokens in one tile with K whole, in 2 and
+// in 4; 9.1, 7.2 and 6.1 in tiles of 64; 7.0 and 5.5 in tiles of 16 with K whole
+// and in 2; 100 x 300 x 304: 13.0 us with 128-token tiles, 5.2 with 16.  2 ns per
+// token and further rank for the sums that cross between SMs (100 x 4096 x 4096:
+// 12.9 us for 128-token tiles in 4, 16.5 in 8).
+// Weights that fill the machine come at 6.8 TB/s: 1 x 4096 x 4096 in 8: 8.1 us.
+// Rows of the output or of other off the 16-byte grid go element by element, 60
+// ns a token (777 x 5001 x 1000: 34 us, 128 tokens to a tile).
 long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 {
-    const long long grid = up(a.N, 128) * up(a.M, c.bn) * c.split, per = up(a.k_blocks, c.split);
-    // rows off the 16-byte grid leave element by element: 0.15 us a token (777 x 5001 x 1000: 34 us against 22 in pairs)
-    const int ragged = a.vec_out && (a.combine == BIGEMM_COMBINE_NONE || a.vec_other) ? 0 : 15 * c.bn;
-    return ragged + (c.alone ? 600 + 33 * per : up(grid, 2ll * sms) * (570 + (c.bn == 128 ? 52 : 37) * per));
+    const long long grid = up(a.N, 128) * up(a.M, c.bn) * c.split;
+    const long long beside = c.alone ? 1 : std::min<long long>(2, up(grid, sms)), waves = up(grid, beside * sms);
+    const long long mine = up(std::min(a.M, c.bn), c.split);
+    const bool ragged = !a.vec_out || (a.combine != BIGEMM_COMBINE_NONE && !a.vec_other);
+    const long long one = up(a.k_blocks, c.split) * std::max<long long>(165, beside * (128 + c.bn)) + 23 * mine + 22 * c.bn +
+                          2 * (c.split - 1) * beside * c.bn + (ragged ? 60 * mine * beside : 0);
+    const long long memory = (long long)a.k_blocks * kRow * a.N / 6800;
+    return 3600 + std::max(memory, waves * one);
 }
 
-// The pair kernel: 3.5 us, and per wave of tiles over the SM pairs and block of
-// K 0.33 us at 256 channels, 0.26 at 128 (where shared memory, not the tensor
-// core, sets the pace).
+// Many tokens, in pairs of CTAs: 3.5 us, and per wave of tiles over the pairs
+// and block of K 0.33 us at 256 channels and 0.26 at 128 (where shared memory,
+// not the tensor core, sets the pace), with MXFP8 operands 0.44 and 0.36.
+// 4096 x 4096 x 4096 bf16: 79.6 us in 4 waves of 256, 110 in 7 of 128; 512 x 4096
+// x 4096 24.7 in one wave of 256, 20.9 in one of 128.
 long long many_cost(const MatmulArgs &a, int sms, int bn)
 {
     const long long waves = up(up(a.M, kManyTokens) * up(a.N, bn), sms / 2);
-    return 350 + waves * a.k_blocks * (bn == 256 ? 33 : 26);
+    const bool mx = a.in_dt == BIGEMM_MXF8;
+    return 3500 + waves * a.k_blocks * (bn == 256 ? (mx ? 440 : 330) : (mx ? 360 : 260));
 }
 
-// Up to 128 tokens one tile of tokens is enough, and the few-token kernel has
-// no rival: 128 x 4096 x 4096 13 us against 20.  Above, the least estimate:
-// 256 x 4096 x 4096 17.7 us (64 tokens, K in 2) against 20.4 and 24.4 in pairs,
-// 512 x 4096 x 4096 25 against 20.9 and 24.7, 1024 x 1024 x 8192 25.5 against
-// 34.5 and 40.9.
+// 256 x 4096 x 4096 bf16: 17.9 us for few (64 tokens, K in 2) against 20.4 and
+// 24.4 in pairs; 512 x 4096 x 4096: 25 against 20.9 and 24.7; 1024 x 1024 x 8192:
+// 25.5 against 34.5 and 40.9.
 Choice choose(const MatmulArgs &a, int sms)
 {
-    const bool full = a.out_dt == BIGEMM_F32;      // its running sums are in registers: at most 64 tokens
+    const bool mx = a.in_dt == BIGEMM_MXF8;
     Choice c = {};
-    if (a.M <= 128) {
-        c.few = cut_few(a, sms, a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || full ? 64 : 128, a.M > 32);
-        return c;
+    long long least = -1;
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        // a 32-bit output's running sums are in registers, of at most 64 tokens; smaller MXFP8 tiles
+        // would start inside a block of scales
+        if ((bn == 128 && a.out_dt == BIGEMM_F32) || (mx && bn < 64 && a.M > bn)) continue;
+        const long long tiles = up(a.N, 128) * up(a.M, bn);
+        // clusters of 5 to 7 CTAs leave SMs of their neighbourhood idle (300 x 1000 x 2048: 13.6 us in
+        // 7, 8.9 in 4)
+        for (int split : {1, 2, 3, 4, 8}) {
+            if (split > 1 && (split * 4 > a.k_blocks || tiles * split > 2ll * sms)) break;
+            for (int alone = 0; alone <= (bn >= 64 && tiles * split <= sms ? 1 : 0); ++alone) {
+                const FewCut cut = {bn, split, alone != 0};
+                const long long cost = few_cost(a, sms, cut);
+                if (least < 0 || cost <= least) c.few = cut, least = cost;
+            }
+        }
+        if (bn >= a.M) break;                  // larger tiles hold no more
     }
-    c.few = cut_few(a, sms, 64, false);
-    long long least = few_cost(a, sms, c.few);
-    if (!full) {
-        const FewCut large = cut_few(a, sms, 128, true);
-        if (few_cost(a, sms, large) < least) c.few = large, least = few_cost(a, sms, large);
-    }
-    for (int bn = 128; bn <= 256; bn += 128) {
-        const long long cost = many_cost(a, sms, bn);
-        if (cost < least) c.many = true, c.bn = bn, least = cost;
-    }
+    if (a.M > 128)
+        for (int bn = 128; bn <= 256; bn += 128) {
+            const long long cost = many_cost(a, sms, bn);
+            if (cost < least) c.many = true, c.bn = bn, least = cost;
+        }
     return c;
 }
 

@@ -42,9 +42,11 @@ struct FewCfg {
     static constexpr int stage = kFewA + BN * kRow + 2 * kMxBlockBytes;
     static constexpr int half = BN == 128 ? 3 : BN == 64 ? 4 : BN == 32 ? 4 : 5;   // stages in half an SM
     static constexpr int whole = BN == 128 ? 6 : BN == 64 ? 8 : half;              // stages of a CTA alone
-    // the sums that a rank gets: at most 7 tokens more than a tile has, since the ranks' shares are
-    // rounded up.  Beside the stages for small tiles, over them for large ones.
-    static constexpr int sums = (BN + 7) * 512;
+    // the ranks' shares of the tokens are whole groups; a rank's sums, of all ranks, are then of at
+    // most BN tokens, and of a group more where three ranks share a tile.  Beside the stages for
+    // small tiles, over them for large ones.
+    static constexpr int group = BN / 8;
+    static constexpr int sums = (BN + 2 * group) * 512;
     static constexpr bool beside = BN <= 32;
     static constexpr int bytes(int stages) { return stages * stage + (beside ? sums : 0) + 256 + 1024; }
     static constexpr int smem(int stages) { return bytes(stages) > kFewShared ? bytes(stages) : kFewShared; }
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kFewThreads)
 
     // ---------------------------------------------------------- each token's sums to the rank that finishes it
     const int tokens = min(BN, p.M - m0);
-    const int per_rank = split > 1 ? (tokens + split - 1) / split : tokens;
+    const int per_rank = ((tokens + split - 1) / split + C::group - 1) / C::group * C::group;
     const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
     // a thread finishes 8 channels, always the same ones, of every 16th token of the rank's; its bias
     // and its first other are asked for now
@@ -269,16 +271,22 @@ __global__ void __launch_bounds__(kFewThreads)
                 tmem_ld_32x32b_x16(lane_base + (uint32_t)c, r);
                 tmem_wait_ld16(r);
             }
+            // a group of tokens has one owner (what a last group holds past the tokens is zeros)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (c + i < tokens) {
-                    const float v = FULL ? acc[FULL ? c + i : 0] : __uint_as_float(r[i]);
-                    if (split > 1) st_cluster_f32(to + (uint32_t)t * 512u, v);
-                    else part[(c + i) * 128 + (warp & 3) * 32 + lane] = v;
-                    if (split > 1 && ++t == per_rank) {
-                        t = 0;
-                        to = mapa_shared(at, (uint32_t)min(++owner, split - 1));
+            for (int g = 0; g < 16; g += C::group) {
+                const uint32_t slot = to + (uint32_t)t * 512u;
+                if (c + g < tokens) {
+#pragma unroll
+                    for (int i = g; i < g + C::group; ++i) {
+                        const float v = FULL ? acc[FULL ? c + i : 0] : __uint_as_float(r[i]);
+                        if (split > 1) st_cluster_f32(slot + (uint32_t)(i - g) * 512u, v);
+                        else st_shared_f32(slot + (uint32_t)(i - g) * 512u, v);
                     }
+                }
+                t += C::group;
+                if (t == per_rank && split > 1) {
+                    t = 0;
+                    to = mapa_shared(at, (uint32_t)min(++owner, split - 1));
                 }
             }
         }
