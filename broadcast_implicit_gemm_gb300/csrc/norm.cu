@@ -31,18 +31,23 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const NormArgs a, int 
     if (r >= a.rows) return;
     const T *row = static_cast<const T *>(a.x) + r * a.ldx;
     const int p0 = (int)run * 32 * U + lane;
-    Raw<T> x[U];
+    const Span span = span_of(a.x, a.rows, a.ldx, a.cols, sizeof(T));
+    Held<T, VEC> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (p0 + u * 32 < a.pieces) x[u] = load_raw<T, VEC>(row, (p0 + u * 32) * kPiece, a.cols);
+        if (p0 + u * 32 < a.pieces) hold<T, VEC>(row, (p0 + u * 32) * kPiece, a.cols, span, x[u]);
     uint8_t *out = static_cast<uint8_t *>(a.out) + r * a.ldo, *scale = a.scale + mx_scale_row(r, a.col_blocks);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int p = p0 + u * 32;
         if (p - lane >= a.pieces) return;     // the whole warp is past the row
         float v[kPiece];
-        if (p >= a.pieces) x[u] = Raw<T>{};
-        unpack<T>(x[u], v);
+        if (p < a.pieces) {
+            take<T, VEC>(x[u], p * kPiece, a.cols, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) v[i] = 0.f;
+        }
         store_mx_piece<VEC>(out, scale, p * kPiece, a.cols, p < a.pieces, v);
     }
 }

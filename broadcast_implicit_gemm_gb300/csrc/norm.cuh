@@ -10,9 +10,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "mx.cuh"
 #include "ptx.cuh"
+#include "unaligned.cuh"
 
 namespace bigemm {
 
@@ -87,44 +90,56 @@ __device__ __forceinline__ void unpack(const Raw<T> &p, float (&v)[kPiece])
     for (int i = 0; i < kPiece; ++i) v[i] = to_f32<T>(e[i]);
 }
 
-// 8 elements from column c on; zeros past the row's end.  VEC: the piece starts
-// on a 16-byte boundary.  Otherwise a 16-bit piece is cut out of the two
-// aligned 16-byte words around it where both lie inside the row, which takes 2
-// loads for 8; pieces at the row's ends go element by element.
-// (c may be up to 7 below 0 where pieces are shifted.)
+// A piece on its way: 8 elements from column c on (up to 7 below 0 where pieces
+// are shifted), zeros outside the row.  VEC: it starts on a 16-byte boundary;
+// else a 16-bit piece is two aligned loads and a shift that waits until it is
+// used, so that a thread's pieces are all in flight together.
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw<T> load_raw(const T *row, int c, int cols)
+struct Held {
+    static constexpr bool wide = !VEC && sizeof(T) == 2;
+    std::conditional_t<wide, Wide, Raw<T>> d;
+};
+
+template <typename T>
+__device__ __forceinline__ int first_byte(int c) { return c < 0 ? -c * (int)sizeof(T) : 0; }
+template <typename T>
+__device__ __forceinline__ int last_byte(int c, int cols)
 {
-    Raw<T> p;
-    if (VEC && c + kPiece <= cols) {
+    return c >= cols ? 0 : min(kPiece, cols - c) * (int)sizeof(T);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void hold(const T *row, int c, int cols, const Span &span, Held<T, VEC> &h)
+{
+    if constexpr (Held<T, VEC>::wide) {
+        h.d = wide_load(reinterpret_cast<const uint8_t *>(row) + (long long)c * (int)sizeof(T), first_byte<T>(c),
+                        last_byte<T>(c, cols), span);
+    } else if (VEC && c + kPiece <= cols) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) p.q[i] = reinterpret_cast<const uint4 *>(row + c)[i];
-        return p;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) h.d.q[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+    } else {
+        T *e = reinterpret_cast<T *>(&h.d);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) e[i] = (VEC || c + i >= 0) && c + i < cols ? row[c + i] : from_f32<T>(0.f);
     }
-    if (!VEC && sizeof(T) == 2 && c < cols) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c), lo = at & ~(uintptr_t)15;
-        if (lo >= reinterpret_cast<uintptr_t>(row) && lo + 32 <= reinterpret_cast<uintptr_t>(row + cols)) {
-            const uint4 a = reinterpret_cast<const uint4 *>(lo)[0], b = reinterpret_cast<const uint4 *>(lo)[1];
-            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const uint32_t by = (uint32_t)(at - lo);
-            if (by & 8) {
-#pragma unroll
-                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (by & 4) {
-#pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-            }
-            const uint32_t sh = (by & 2) * 8;
-            p.q[0] = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                                __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-            return p;
-        }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void take(const Held<T, VEC> &h, int c, int cols, float (&v)[kPiece])
+{
+    if constexpr (Held<T, VEC>::wide) {
+        Raw<T> r;
+        r.q[0] = wide_take(h.d, first_byte<T>(c), last_byte<T>(c, cols));
+        unpack<T>(r, v);
+    } else {
+        unpack<T>(h.d, v);
     }
-    T *e = reinterpret_cast<T *>(&p);
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) e[i] = (VEC || c + i >= 0) && c + i < cols ? row[c + i] : from_f32<T>(0.f);
-    return p;
+}
+
+__device__ __forceinline__ Span span_of(const void *p, long long rows, long long ld, int cols, size_t es)
+{
+    const uint8_t *b = static_cast<const uint8_t *>(p);
+    return {b, b + ((rows - 1) * ld + cols) * (long long)es};
 }
 
 // 8 elements to column c on, those inside the row.  Off the 16-byte grid a
@@ -226,64 +241,77 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int c, float (&g)
     for (int i = 0; i < kPiece; ++i) g[i] = a.weight && c + i >= 0 && c + i < a.cols ? __ldg(a.weight + c + i) : 1.f;
 }
 
-// Threads of a block with so many per row, and blocks per SM that its registers
-// leave room for: 1024 threads (64 registers), half as many for 32-bit rows,
-// which hold twice the bytes.
+// Threads of a block with so many per row at most, and threads per SM that its
+// registers leave room for: 1024 (64 registers), half as many for 32-bit rows
+// and for rows off the 16-byte grid, which hold twice the bytes.
 constexpr int norm_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
-constexpr int norm_blocks(int tpr, size_t es)
+constexpr int norm_room(size_t es, bool vec) { return es == 4 || !vec ? 512 : 1024; }
+constexpr int norm_blocks(int tpr, size_t es, bool vec)
 {
-    const int n = (es == 4 ? 512 : 1024) / norm_threads(tpr);
-    return n < 1 ? 1 : n;
+    return norm_room(es, vec) < norm_threads(tpr) ? 1 : norm_room(es, vec) / norm_threads(tpr);
 }
 
-// TPR threads per row, PPT pieces per thread in registers; a block of
-// max(TPR, 128) threads walks over its rows and loads the next one before it
+// TPR threads per row at most (a warp, or the block), PPT pieces per thread in
+// registers; a block walks over its rows and loads the next one before it
 // sums the present one, so that memory works through the sums and the barrier.
 // RES: there is a residual, and the weights come from L1 again for each row,
 // because the rows in flight need the registers (16384 x 4096 f16: 6.2 TB/s).
 // Without one they stay in registers: L1 delivered more of them than of rows
 // (the same rows to MXFP8 took 54 us with them from L1, 37 us so).
-template <typename T, int FORM, bool RES, int TPR, int PPT, bool VEC>
-__global__ void __launch_bounds__(norm_threads(TPR), norm_blocks(TPR, sizeof(T))) rmsnorm_kernel(const NormArgs a)
+// EXACT: the block has all of TPR (on the 16-byte grid, where reading the size of
+// the block at run time costs: 8192 x 8192 f16 to MXFP8 38.8 us, 41.7 so).
+// Otherwise it has the warps that the row needs (4096 x 2049 f16 with a residual:
+// 36.6 us with TPR threads, 22.9 so).
+template <typename T, int FORM, bool RES, int TPR, int PPT, bool VEC, bool EXACT>
+__global__ void __launch_bounds__(norm_threads(TPR), norm_blocks(TPR, sizeof(T), VEC)) rmsnorm_kernel(const NormArgs a)
 {
     griddep_enter();
     constexpr int THREADS = norm_threads(TPR), ROWS = THREADS / TPR;
     static_assert(TPR == 32 || ROWS == 1, "a row has a warp or the block");
     __shared__ float4 part[2][THREADS / 128];
-    const int t = (int)threadIdx.x % TPR;
+    const int tpr = TPR == 32 || EXACT ? TPR : (int)blockDim.x, t = TPR == 32 ? (int)threadIdx.x & 31 : (int)threadIdx.x;
+    if (TPR > 32 && !EXACT) {
+        // a block may have fewer warps than the sums have places
+        for (int i = threadIdx.x; i < 2 * THREADS / 32; i += blockDim.x) reinterpret_cast<float *>(part)[i] = 0.f;
+        __syncthreads();
+    }
     const long long step = (long long)gridDim.x * ROWS;
-    long long r = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
-    Raw<T> x[PPT], res[RES ? PPT : 1];
+    long long r = (long long)blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x / 32 : 0);
+    Held<T, VEC> x[PPT], res[RES ? PPT : 1];
+    const Span x_span = span_of(a.x, a.rows, a.ldx, a.cols, sizeof(T));
+    const Span res_span = RES ? span_of(a.residual, a.rows, a.ldr, a.cols, sizeof(T)) : x_span;
     auto load = [&](long long row) {
         if (row >= a.rows) return;
         const int c0 = t * kPiece - row_shift<FORM, T, VEC>(a, row);
 #pragma unroll
         for (int s = 0; s < PPT; ++s)
-            x[s] = load_raw<T, VEC>(static_cast<const T *>(a.x) + row * a.ldx, c0 + s * TPR * kPiece, a.cols);
+            hold<T, VEC>(static_cast<const T *>(a.x) + row * a.ldx, c0 + s * tpr * kPiece, a.cols, x_span, x[s]);
         if (RES) {
 #pragma unroll
             for (int s = 0; s < PPT; ++s)
-                res[RES ? s : 0] = load_raw<T, VEC>(static_cast<const T *>(a.residual) + row * a.ldr, c0 + s * TPR * kPiece, a.cols);
+                hold<T, VEC>(static_cast<const T *>(a.residual) + row * a.ldr, c0 + s * tpr * kPiece, a.cols, res_span,
+                             res[RES ? s : 0]);
         }
     };
     float kept[RES ? 1 : PPT][kPiece];
     constexpr bool SHIFTED = !VEC && FORM != OUT_MX;      // a row's pieces start where its output lies
     if (!RES && !SHIFTED) {
 #pragma unroll
-        for (int s = 0; s < PPT; ++s) load_weight(a, (s * TPR + t) * kPiece, kept[RES ? 0 : s]);
+        for (int s = 0; s < PPT; ++s) load_weight(a, (s * tpr + t) * kPiece, kept[RES ? 0 : s]);
     }
     load(r);
     // the loop's condition is the block's first row, so that no warp leaves another at the barrier or in a shuffle
-    for (int turn = 0; r - (ROWS > 1 ? threadIdx.x / TPR : 0) < a.rows; ++turn, r += step) {
+    for (int turn = 0; r - (ROWS > 1 ? threadIdx.x / 32 : 0) < a.rows; ++turn, r += step) {
         float h[PPT][kPiece];
         float sum = 0.f;
         const bool live = r < a.rows;
+        const int c0 = t * kPiece - (live ? row_shift<FORM, T, VEC>(a, r) : 0);
 #pragma unroll
         for (int s = 0; s < PPT; ++s) {
-            unpack<T>(x[s], h[s]);
+            take<T, VEC>(x[s], c0 + s * tpr * kPiece, a.cols, h[s]);
             if (RES) {
                 float w[kPiece];
-                unpack<T>(res[RES ? s : 0], w);
+                take<T, VEC>(res[RES ? s : 0], c0 + s * tpr * kPiece, a.cols, w);
 #pragma unroll
                 for (int i = 0; i < kPiece; ++i) h[s][i] += w[i];
             }
@@ -307,16 +335,15 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks(TPR, sizeof(T))
         }
         const float inv = rsqrtf(sum * a.inv_cols + a.eps);
         if (!live) continue;
-        const int c0 = t * kPiece - row_shift<FORM, T, VEC>(a, r);
 #pragma unroll
         for (int s = 0; s < PPT; ++s) {
-            const int c = c0 + s * TPR * kPiece;
+            const int c = c0 + s * tpr * kPiece;
             if constexpr (RES || SHIFTED) {
                 float g[kPiece];
                 load_weight(a, c, g);
-                norm_out<FORM, T, VEC>(a, r, s * TPR + t, c, inv, h[s], g);
+                norm_out<FORM, T, VEC>(a, r, s * tpr + t, c, inv, h[s], g);
             } else {
-                norm_out<FORM, T, VEC>(a, r, s * TPR + t, c, inv, h[s], kept[s]);
+                norm_out<FORM, T, VEC>(a, r, s * tpr + t, c, inv, h[s], kept[s]);
             }
         }
     }
@@ -333,11 +360,16 @@ __global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
     const T *x = static_cast<const T *>(a.x) + r * a.ldx;
     const T *res = a.residual ? static_cast<const T *>(a.residual) + r * a.ldr : nullptr;
     const int steps = (a.pieces + 511) / 512, shift = row_shift<FORM, T, VEC>(a, r);
-    auto take = [&](int c, float (&h)[kPiece]) {
-        unpack<T>(load_raw<T, VEC>(x, c, a.cols), h);
+    const Span x_span = span_of(a.x, a.rows, a.ldx, a.cols, sizeof(T));
+    const Span res_span = res ? span_of(a.residual, a.rows, a.ldr, a.cols, sizeof(T)) : x_span;
+    auto sum_at = [&](int c, float (&h)[kPiece]) {
+        Held<T, VEC> p, q;
+        hold<T, VEC>(x, c, a.cols, x_span, p);
+        if (res) hold<T, VEC>(res, c, a.cols, res_span, q);
+        take<T, VEC>(p, c, a.cols, h);
         if (res) {
             float w[kPiece];
-            unpack<T>(load_raw<T, VEC>(res, c, a.cols), w);
+            take<T, VEC>(q, c, a.cols, w);
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) h[i] += w[i];
         }
@@ -345,7 +377,7 @@ __global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
     float sum = 0.f;
     for (int s = 0; s < steps; ++s) {
         float h[kPiece];
-        take((s * 512 + (int)threadIdx.x) * kPiece - shift, h);
+        sum_at((s * 512 + (int)threadIdx.x) * kPiece - shift, h);
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) sum += h[i] * h[i];
     }
@@ -359,7 +391,7 @@ __global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
     for (int s = 0; s < steps; ++s) {
         const int p = s * 512 + (int)threadIdx.x, c = p * kPiece - shift;
         float h[kPiece], g[kPiece];
-        take(c, h);
+        sum_at(c, h);
         load_weight(a, c, g);
         norm_out<FORM, T, VEC>(a, r, p, c, inv, h, g);
     }
@@ -368,10 +400,16 @@ __global__ void __launch_bounds__(512) rmsnorm_long_kernel(const NormArgs a)
 template <typename T, int FORM, bool RES, int TPR, int PPT, bool VEC>
 cudaError_t launch_norm_rows(const NormArgs &a, int sms, cudaStream_t s)
 {
-    constexpr int THREADS = norm_threads(TPR), ROWS = THREADS / TPR;
-    const long long most = (long long)sms * norm_blocks(TPR, sizeof(T)), need = (a.rows + ROWS - 1) / ROWS;
-    return launch_pdl(rmsnorm_kernel<T, FORM, RES, TPR, PPT, VEC>, dim3((unsigned)(need < most ? need : most)),
-                      dim3(THREADS), 0, s, a);
+    // as many warps as hold the row's pieces, and one wave of such blocks
+    const int threads = TPR == 32 ? norm_threads(TPR) : ((a.pieces + PPT - 1) / PPT + 31) / 32 * 32;
+    const int rows = TPR == 32 ? threads / 32 : 1, beside = norm_room(sizeof(T), VEC) / threads;
+    const long long most = (long long)sms * (beside < 1 ? 1 : beside), need = (a.rows + rows - 1) / rows;
+    const dim3 grid((unsigned)(need < most ? need : most));
+    if constexpr (VEC && TPR > 32) {
+        if (threads == TPR)
+            return launch_pdl(rmsnorm_kernel<T, FORM, RES, TPR, PPT, VEC, true>, grid, dim3(threads), 0, s, a);
+    }
+    return launch_pdl(rmsnorm_kernel<T, FORM, RES, TPR, PPT, VEC, false>, grid, dim3(threads), 0, s, a);
 }
 
 // The fewest threads whose pieces hold a row.
