@@ -114,6 +114,7 @@ Choice choose(const MatmulArgs &a, int sms)
         // a 32-bit output's running sums are in registers, of at most 64 tokens; smaller MXFP8 tiles
         // would start inside a block of scales
         if ((bn == 128 && a.out_dt == BIGEMM_F32) || (mx && bn < 64 && a.M > bn)) continue;
+        if (up(a.M, bn) > 65535) continue;     // the grid's second axis
         const long long tiles = up(a.N, 128) * up(a.M, bn);
         // clusters of 5 to 7 CTAs leave SMs of their neighbourhood idle (300 x 1000 x 2048: 13.6 us in
         // 7, 8.9 in 4)
@@ -130,7 +131,7 @@ Choice choose(const MatmulArgs &a, int sms)
     if (a.M > 128)
         for (int bn = 128; bn <= 256; bn += 128) {
             const long long cost = many_cost(a, sms, bn);
-            if (cost < least) c.many = true, c.bn = bn, least = cost;
+            if (least < 0 || cost < least) c.many = true, c.bn = bn, least = cost;
         }
     return c;
 }
@@ -229,11 +230,10 @@ bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, 
         return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
     }
     const FewCut cut = pick.few;
-    if ((a.M + (long long)cut.bn - 1) / cut.bn > 65535) return BIGEMM_ERR_UNSUPPORTED;
     a.split = cut.split;
     CUtensorMap mw = {}, mxm = {};
-    if ((!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
-                    !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn)))
+    if (!operand_map(&mw, a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
+        !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, cut.bn))
         return BIGEMM_ERR_CUDA;
     const cudaError_t e = launch_matmul_few(a, cut, mw, mxm, (cudaStream_t)stream);
     return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const int c = ((int)threadIdx.x & 15) * 8;
     float bias[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = p.bias && n0 + c + j < p.N ? __ldg(p.bias + n0 + c + j) : 0.f;
+    for (int j = 0; j < 8; ++j) bias[j] = p.bias && n0 + c + j < p.N ? p.bias[n0 + c + j] : 0.f;
     Raw8 other;
     if ((int)threadIdx.x < mine * 16) mm_other8(p, m0 + t0 + ((int)threadIdx.x >> 4), n0 + c, other);
     if (split > 1) {

@@ -132,12 +132,12 @@ __device__ __forceinline__ void epilogue32(const MatmulArgs &p, uint8_t *stage, 
             const float4 *b = reinterpret_cast<const float4 *>(p.bias + n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 f = __ldg(b + i);
+                const float4 f = b[i];
                 v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += __ldg(p.bias + n + i);
+            for (int i = 0; i < 32; ++i) v[i] += p.bias[n + i];
         }
     }
     mm_act_all(p.act, v);
@@ -263,7 +263,7 @@ __device__ __forceinline__ uint32_t put_columns(const MatmulArgs &p, uint8_t *st
 {
     float *turn = reinterpret_cast<float *>(stage);
     const bool in = n + lane < p.N;
-    const float bias = p.bias && in ? __ldg(p.bias + n + lane) : 0.f;
+    const float bias = p.bias && in ? p.bias[n + lane] : 0.f;
     uint32_t code = 0;
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();

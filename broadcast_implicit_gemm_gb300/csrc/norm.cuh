@@ -232,13 +232,13 @@ __device__ __forceinline__ int row_shift(const NormArgs &a, long long r)
 __device__ __forceinline__ void load_weight(const NormArgs &a, int c, float (&g)[kPiece])
 {
     if (a.vec_weight && c % 4 == 0 && c >= 0 && c + kPiece <= a.cols) {
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(a.weight + c));
-        const float4 w = __ldg(reinterpret_cast<const float4 *>(a.weight + c + 4));
+        const float4 u = *reinterpret_cast<const float4 *>(a.weight + c);
+        const float4 w = *reinterpret_cast<const float4 *>(a.weight + c + 4);
         g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w, g[4] = w.x, g[5] = w.y, g[6] = w.z, g[7] = w.w;
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) g[i] = a.weight && c + i >= 0 && c + i < a.cols ? __ldg(a.weight + c + i) : 1.f;
+    for (int i = 0; i < kPiece; ++i) g[i] = a.weight && c + i >= 0 && c + i < a.cols ? a.weight[c + i] : 1.f;
 }
 
 // Threads of a block with so many per row at most, and threads per SM that its

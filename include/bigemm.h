@@ -326,7 +326,7 @@ typedef enum {
  *   workspace: matmul_workspace_bytes of device memory on a 16-byte boundary,
  *   the call's until it is done; NULL where that is 0.
  * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum, a
- * workspace that is too small), UNSUPPORTED (in_dtype F32; N or K above 2^30, more than 4 million tokens), CUDA.
+ * workspace that is too small), UNSUPPORTED (in_dtype F32; a size above 2^30 or 2^31 tiles), CUDA.
  */
 bigemm_status matmul_run(int M, int N, int K, bigemm_dtype in_dtype, const void *x, int64_t ldx,
                          const void *w, int64_t ldw, const float *bias, int act, int combine,

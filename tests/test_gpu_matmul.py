@@ -105,6 +105,12 @@ def test_many_channels_few_tokens_and_many_tokens_few_channels():
     run_case(5000, 40, 96, "f16", "f16", "silu", "none", True)
 
 
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_a_million_tokens(out):
+    """More tiles of few tokens than a grid's second axis has places."""
+    run_case(1_100_003, 8, 16, "f16", out, "relu", "add", True)
+
+
 @pytest.mark.parametrize("M,N,K", [(300, 700, 520), (513, 1030, 264), (1024, 512, 1024), (777, 260, 4096)])
 @pytest.mark.parametrize("kind,out", [("bf16", "bf16"), ("f16", "f32")])
 def test_prompts(M, N, K, kind, out):
@@ -295,3 +301,25 @@ def test_tensor_refusals():
     assert bg.matmul(x[:0], w).shape == (0, 8)
     assert bg.matmul_mx(q[:0], s[:0], p, t).shape == (0, 8)
     assert bg.bigemm_last_device_error() == 0
+
+
+# --------------------------------------------------------------------- far offsets
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that element offsets pass 2^32: first, middle and last rows land where they should."""
+    rows, cols, apart = 5, 64, (1 << 30) + 8
+    base = torch.empty(4 * apart + cols, dtype=torch.float16, device="cuda")
+    x = base.as_strided((rows, cols), (apart, 1))
+    x.copy_(rand((rows, cols), 1).half())
+    w = rand((72, cols), 2, 0.125).half().cuda()
+    ref, d = lr.product64(f64(x), f64(w), None, "none", None, "none", torch.float16, False)
+    lr.check_float(bg.matmul(x, w), ref, d, "far x")
+    q, s = bg.mx_quantize(x)
+    p, t = bg.mx_quantize(x.contiguous())
+    assert torch.equal(q.view(torch.uint8), p.view(torch.uint8)) and torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+    assert torch.equal(bg.rmsnorm(x), bg.rmsnorm(x.contiguous()))
+    y = base.as_strided((rows, 72), (apart - 8, 1))
+    want = bg.matmul(x, w)
+    x = x.contiguous()
+    bg.matmul(x, w, out=y)
+    assert torch.equal(y, want)
