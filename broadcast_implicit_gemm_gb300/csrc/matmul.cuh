@@ -36,12 +36,6 @@ struct MatmulArgs {
     int *err;
 };
 
-// Whether K is summed in pieces, added up in registers (matmul_few.cu says why):
-// for 32-bit outputs, and for MXFP8 ones, where the error of one long sum would
-// show as elements and scales rounded the other way.  16-bit outputs round off
-// a hundred times that error.
-inline bool matmul_in_pieces(const MatmulArgs &a) { return a.out_dt == BIGEMM_F32 || a.out_dt == BIGEMM_MXF8; }
-
 namespace {
 
 constexpr int kRow = 128;            // bytes of one row in a stage: a 128-byte swizzle row
