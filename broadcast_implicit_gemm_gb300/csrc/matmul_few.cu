@@ -17,7 +17,7 @@
 // scales are one block of 512 bytes per operand.  They land beside the stage
 // and go to tensor memory columns of that stage before its MMAs.
 //
-// FULL: a 32-bit output.  The tensor core cuts each addition into its fp32
+// FULL: K summed in pieces.  The tensor core cuts each addition into its fp32
 // accumulator short, so the error of one long sum grows with K (measured
 // 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
@@ -382,7 +382,7 @@ template <int BN>
 cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
                       cudaStream_t s)
 {
-    if (a.out_dt == BIGEMM_F32) {
+    if (matmul_in_pieces(a)) {
         if constexpr (BN <= 64)
             return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, true>(a, split, alone, mw, mx, s)
                                           : launch_one<BN, false, true>(a, split, alone, mw, mx, s);

@@ -13,7 +13,8 @@
 // 16-bit operands: two accumulators fill tensor memory, and a tile's epilogue
 // runs beside the next one's MMAs.  MX: the scales take columns too (12 per
 // stage), so there is one accumulator; the drain warps take all of it to
-// registers, hand it back, and go on from there.
+// registers, hand it back, and go on from there.  For an MXFP8 output they add up
+// pieces of 2048 elements there.
 //
 // FULL: a 32-bit output, sums of at most 512 or 2048 elements added up in registers
 // (matmul_few.cu says why).
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(ManyCfg<BN, MX, FULL>::threads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = lane_base + (uint32_t)(a * BN);
-                if constexpr (KEEP && !FULL) {
+                if (KEEP && !FULL && k0 == 0) {
                     uint32_t r[UNITS][32];
 #pragma unroll
                     for (int u = 0; u < UNITS; ++u) tmem_ld_32x32b_x32(base + u * 32, r[u]);
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(ManyCfg<BN, MX, FULL>::threads, 1)
                     for (int u = 0; u < UNITS; ++u) {
                         tmem_wait_ld32(r[u]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) keep[u][i] = __uint_as_float(r[u][i]);
+                        for (int i = 0; i < 32; ++i) keep[KEEP ? u : 0][i] = __uint_as_float(r[u][i]);
                     }
                 } else if constexpr (KEEP) {
 #pragma unroll

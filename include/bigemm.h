@@ -320,9 +320,9 @@ typedef enum {
  *   x [M,K], w [N,K] of in_dtype (F16 or BF16), fp32 sums; bias [N] fp32 or NULL
  *   other [M,N] of other_dtype (F32, F16, BF16), read unless combine is NONE; it
  *   may be out itself (same type and rows)
- *   out [M,N] of out_dtype (F32, F16, BF16), rounded once.  For F32 at most 512
- *   products at a time (2048 of MXF8) are summed in the tensor core, the rest in
- *   fp32 adds.
+ *   out [M,N] of out_dtype (F32, F16, BF16), rounded once.  For F32, and for an MXF8
+ *   output, at most 512 products at a time (2048 of MXF8 operands) are summed in
+ *   the tensor core, the rest in fp32 adds.
  *   workspace: matmul_workspace_bytes of device memory on a 16-byte boundary,
  *   the call's until it is done; NULL where that is 0.
  * Errors: INVALID_ARG (a size, null or misaligned pointer, short ld, bad enum, a
