@@ -383,6 +383,10 @@ def bcast(var, N, H, W, op=BC_EXP, eps=1e-5, out_dtype=None, out=None, stream=No
 # Matrices are 2-D CUDA tensors whose last axis is contiguous.  MXFP8 matrices
 # are a float8_e4m3fn tensor and its scales, a contiguous float8_e8m0fnu (or
 # uint8) tensor of mx_scale_shape(rows, cols).
+#
+# A call runs on `stream` (a torch.cuda.Stream or a cudaStream_t value; None: the
+# current one), and so does the making of what it allocates.  What the caller
+# passes in has to be ready on that stream.
 
 _layer_module = None
 
@@ -412,13 +416,34 @@ def _layer():
     return _layer_module
 
 
-def _workspace(n, x, stream):
-    """n bytes on x's device for a call on the given stream (None: the current one)."""
+def _on(stream, device):
+    """A context in which tensors are made on the given stream: memory comes from the stream's own pool, so that
+    neither work pending elsewhere nor the fill of a new tensor runs beside the call."""
     import torch
-    t = torch.empty(n, dtype=torch.uint8, device=x.device)
-    if stream is not None:      # the memory is not given out again before that stream is done with the call
-        t.record_stream(torch.cuda.ExternalStream(stream, device=x.device) if isinstance(stream, int) else stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)    # 0 and 1 stand for the device's default stream, others are addresses
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _new(make, shape, dtype, device, stream):
+    """make(shape) for a call on the given stream (None: the current one) to return."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))      # which is where the caller goes on to use it
     return t
+
+
+def _workspace(n, x, stream):
+    """n bytes on x's device for a call on the given stream (None: the current one), where they are freed too."""
+    import torch
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
+    with _on(stream, x.device):
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
 def _status(status, where, again, x):
@@ -437,22 +462,22 @@ def mx_scale_shape(rows: int, cols: int) -> tuple:
     return (-(-rows // 128), -(-cols // 128), 32, 4, 4)
 
 
-def _output(out, out_dtype, default, rows, cols, device):
+def _output(out, out_dtype, default, rows, cols, device, stream):
     import torch
     if out is None:
-        return torch.empty((rows, cols), dtype=out_dtype if out_dtype is not None else default, device=device)
+        return _new(torch.empty, (rows, cols), out_dtype if out_dtype is not None else default, device, stream)
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     return out
 
 
-def _output_scales(out, scale):
+def _output_scales(out, scale, stream):
     """Scales for out if it is an MXFP8 matrix and has none."""
     import torch
     if out.dtype != torch.float8_e4m3fn:
         return None
     if scale is None:
-        scale = torch.zeros(mx_scale_shape(*out.shape), dtype=torch.uint8, device=out.device).view(torch.float8_e8m0fnu)
+        scale = _new(torch.zeros, mx_scale_shape(*out.shape), torch.uint8, out.device, stream).view(torch.float8_e8m0fnu)
     return scale
 
 
@@ -465,7 +490,7 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
     if combine is None:
         combine = COMBINE_NONE if other is None else COMBINE_ADD
     if out is None or out_dtype is not None:
-        out = _output(out, out_dtype, x.dtype, x.shape[0], w.shape[0], x.device)
+        out = _output(out, out_dtype, x.dtype, x.shape[0], w.shape[0], x.device, stream)
     args = (x, None, w, None, bias, act, other, combine, out, None, stream)
     status = (_layer_module or _layer()).product(*args)
     if status:
@@ -481,8 +506,8 @@ def matmul_mx(x, x_scale, w, w_scale, bias=None, act=ACT_NONE, other=None, combi
     if combine is None:
         combine = COMBINE_NONE if other is None else COMBINE_ADD
     if out is None or out_dtype is not None:
-        out = _output(out, out_dtype, torch.bfloat16, x.shape[0], w.shape[0], x.device)
-    out_scale = _output_scales(out, out_scale)
+        out = _output(out, out_dtype, torch.bfloat16, x.shape[0], w.shape[0], x.device, stream)
+    out_scale = _output_scales(out, out_scale, stream)
     args = (x, x_scale, w, w_scale, bias, act, other, combine, out, out_scale, stream)
     status = (_layer_module or _layer()).product(*args)
     if status:
@@ -497,10 +522,10 @@ def rmsnorm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, o
     Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.
     """
     if residual is not None and sum_out is None:
-        sum_out = _output(None, None, x.dtype, *x.shape, x.device)
+        sum_out = _output(None, None, x.dtype, *x.shape, x.device, stream)
     if out is None or out_dtype is not None:
-        out = _output(out, out_dtype, x.dtype, *x.shape, x.device)
-    out_scale = _output_scales(out, out_scale)
+        out = _output(out, out_dtype, x.dtype, *x.shape, x.device, stream)
+    out_scale = _output_scales(out, out_scale, stream)
     args = (x, weight, residual, eps, sum_out, out, out_scale, stream)
     status = (_layer_module or _layer()).norm(*args)
     if status:
@@ -514,9 +539,9 @@ def mx_quantize(x, out=None, scale=None, stream=None):
     """(float8_e4m3fn elements, scales) of a float32, float16 or bfloat16 matrix."""
     import torch
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = _new(torch.empty, x.shape, torch.float8_e4m3fn, x.device, stream)
     if scale is None:
-        scale = _output_scales(out, None)
+        scale = _output_scales(out, None, stream)
     args = (x, out, scale, stream)
     status = (_layer_module or _layer()).quantize(*args)
     if status:
