@@ -136,7 +136,7 @@ Choice choose(const MatmulArgs &a, int sms)
     return c;
 }
 
-constexpr int kMaxSize = 1 << 30;   // index arithmetic within a row is in 32 bits
+constexpr int kMaxSize = 1 << 30;   // indices within a row are in 32 bits, byte offsets in 64
 
 // 128-byte pieces of a row that one tensor-memory accumulator sums where K is
 // summed in pieces: 512 products of 16-bit operands (32 additions), 2048 of MXFP8 ones

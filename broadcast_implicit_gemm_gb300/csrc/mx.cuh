@@ -5,33 +5,13 @@
 // is e4m3's largest value), so no element saturates; it is stored as the byte
 // code with s = 2^(code - 127) (E8M0).  A group that holds a NaN or an infinity
 // gets code 255, E8M0's NaN, and NaN elements.
-//
-// Scales are kept in blocks of 128 rows by 128 columns, 512 bytes each, the
-// blocks of one block row next to each other.  Within a block, the byte of row
-// r and group g is (r % 32) * 16 + (r / 32) * 4 + g: the order in which tensor
-// memory takes a block's scales from shared memory in one copy.
 #pragma once
 #include <cstdint>
 #include <cuda_fp8.h>
 
+#include "mx_layout.h"
+
 namespace bigemm {
-
-constexpr int kMxGroup = 32;        // elements per scale
-constexpr int kMxBlock = 128;       // rows, and columns, per block of scales
-constexpr int kMxBlockBytes = 512;
-
-// Byte offset of a row's first scale in a matrix with col_blocks blocks per
-// block row; the row's further blocks follow kMxBlockBytes apart.
-__device__ __forceinline__ long long mx_scale_row(long long row, int col_blocks)
-{
-    const int r = (int)row;
-    return (row >> 7) * col_blocks * kMxBlockBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-}
-
-__device__ __forceinline__ long long mx_scale_offset(long long row, int group, int col_blocks)
-{
-    return mx_scale_row(row, col_blocks) + (long long)(group >> 2) * kMxBlockBytes + (group & 3);
-}
 
 // The scale's code from a group's largest magnitude: its exponent less 8, one
 // more where the fraction exceeds 448's (1.75, fraction bits 0x600000: adding

@@ -35,7 +35,7 @@ enum OutForm { OUT_SAME = 0, OUT_F32 = 1, OUT_MX = 2 };
 namespace {
 
 constexpr int kPiece = 8;            // elements per thread and step
-constexpr int kMaxCols = 1 << 30;    // index arithmetic within a row is in 32 bits
+constexpr int kMaxCols = 1 << 30;    // column indices are in 32 bits, byte offsets in 64
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -173,7 +173,7 @@ __device__ __forceinline__ void store_mx_piece(uint8_t *row, uint8_t *scale, int
     top = mx_amax(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t code = mx_scale_code(top);
     if (!live) return;
-    if ((threadIdx.x & 3) == 0) scale[(c >> 7) * kMxBlockBytes + ((c >> 5) & 3)] = (uint8_t)code;
+    if ((threadIdx.x & 3) == 0) scale[mx_scale_group(c / kMxGroup)] = (uint8_t)code;
     const float inv = mx_inv_scale(code);
     float w[kPiece];
     scale8(v, inv, w);
