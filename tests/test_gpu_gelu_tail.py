@@ -34,3 +34,24 @@ def test_relative_to_the_value(out, many):
     bound = bound + lr.U[out] * (np.abs(ref) + bound) + lr.TINY[out]
     err = np.abs(y - ref)
     assert (err <= bound).all(), f"worst {np.max(err / bound):.2f} of the bound, at z = {z[np.argmax(err / bound)]}"
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("many", [False, True])
+def test_quotients_relative_to_the_value(act, out, many):
+    """z / (1 + exp(-v)), v = z or 2 sqrt(2/pi) (z + 0.044715 z^3): v's value and its product with log2(e) are off by at most
+    5 times 2^-24 of v, so the power by 5 |v| 2^-24; the power, sum, reciprocal and product by 8 times 2^-24 together.  Where
+    1 + exp(-v) passes 2^126 its reciprocal is flushed to zero: 16 * 2^-126."""
+    z = zs()
+    x, w = z[:, None].cuda(), torch.ones(1, 1).half().cuda()
+    if not many:
+        x, w = w, x
+    y = bg.matmul(x, w, act=bg.ACT_NAMES[act], out_dtype=out).reshape(-1).cpu().double().numpy()
+    z = z.double().numpy()
+    v = z if act == "silu" else 2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)
+    ref = z / (1 + np.exp(-v))
+    bound = np.abs(ref) * (5 * np.abs(v) + 8) * 2.0 ** -24 + 2.0 ** -122
+    bound = bound + lr.U[out] * (np.abs(ref) + bound) + lr.TINY[out]
+    err = np.abs(y - ref)
+    assert (err <= bound).all(), f"worst {np.max(err / bound):.2f} of the bound, at z = {z[np.argmax(err / bound)]}"
