@@ -386,7 +386,7 @@ def bcast(var, N, H, W, op=BC_EXP, eps=1e-5, out_dtype=None, out=None, stream=No
 #
 # A call runs on `stream` (a torch.cuda.Stream or a cudaStream_t value; None: the
 # current one), and so does the making of what it allocates.  What the caller
-# passes in has to be ready on that stream.
+# passes in has to be ready on that stream.  Results carry no gradient.
 
 _layer_module = None
 
@@ -486,6 +486,7 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
 
     `combine` is COMBINE_ADD (a residual; the default when `other` is given) or COMBINE_MUL (a gate).
     Sums in fp32; out is x's type unless out_dtype (float32, float16, bfloat16) or out says otherwise.
+    Forward only, like the calls below: the result carries no gradient.
     """
     if combine is None:
         combine = COMBINE_NONE if other is None else COMBINE_ADD
