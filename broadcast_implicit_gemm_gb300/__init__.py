@@ -26,8 +26,10 @@ __all__ = [
     "MXF8", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "ACT_NAMES",
     "COMBINE_NONE", "COMBINE_ADD", "COMBINE_MUL", "COMBINE_NAMES",
     "matmul_run", "matmul_mx_run", "matmul_workspace_bytes", "rmsnorm_run", "mx_quantize_run",
-    "bigemm_mx_scale_bytes",
-    "matmul", "matmul_mx", "rmsnorm", "mx_quantize", "mx_scale_shape",
+    "bigemm_mx_scale_bytes", "layernorm_run", "layernorm_backward_run", "rmsnorm_backward_run",
+    "norm_backward_workspace_bytes",
+    "matmul", "matmul_mx", "rmsnorm", "mx_quantize", "mx_scale_shape", "layernorm", "layernorm_backward",
+    "rmsnorm_backward",
     "bigemm_status_string", "bigemm_last_device_error", "bigemm_clear_device_error",
     "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout", "bigemm_profile_enable",
     "bigemm_profile_read", "bigemm_version", "conv2d", "bcast", "out_size",
@@ -111,6 +113,11 @@ def _declare(lib):
     lib.mx_quantize_run.argtypes = [i, i, i, p, i64, p, i64, p, p]
     lib.bigemm_mx_scale_bytes.argtypes = [i, i]
     lib.bigemm_mx_scale_bytes.restype = u64
+    lib.layernorm_run.argtypes = [i, i, i, p, i64, p, i64, p, p, f, p, i64, i, p, i64, p, p, p, p]
+    lib.layernorm_backward_run.argtypes = [i, i, i, p, i64, p, i64, p, p, p, p, i64, p, i64, p, p, p, u64, p]
+    lib.rmsnorm_backward_run.argtypes = [i, i, i, p, i64, p, i64, p, f, p, i64, p, i64, p, p, u64, p]
+    lib.norm_backward_workspace_bytes.argtypes = [i, i]
+    lib.norm_backward_workspace_bytes.restype = u64
     lib.bigemm_status_string.argtypes = [i]
     lib.bigemm_status_string.restype = ctypes.c_char_p
     lib.bigemm_last_device_error.argtypes = []
@@ -125,7 +132,8 @@ def _declare(lib):
                  "conv2d_nchw_run_noalloc",
                  "conv2d_nchw_plan_destroy", "conv2d_nchw_plan_describe", "bcast_nchw_run",
                  "bcast_nchw_run_flat", "bcast_run", "matmul_run", "matmul_mx_run", "rmsnorm_run",
-                 "mx_quantize_run", "bigemm_last_device_error",
+                 "mx_quantize_run", "layernorm_run", "layernorm_backward_run", "rmsnorm_backward_run",
+                 "bigemm_last_device_error",
                  "bigemm_clear_device_error",
                  "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout",
                  "bigemm_profile_enable", "bigemm_profile_read"):
@@ -291,6 +299,32 @@ def mx_quantize_run(rows, cols, in_dtype, x, ldx, out, ldo, scale, stream=None):
                                           _stream(stream)), "mx_quantize_run")
 
 
+def layernorm_run(rows, cols, in_dtype, x, ldx, residual, ldr, weight, bias, eps, sum_out, lds, out_dtype, out, ldo,
+                  out_scale, mean, rstd, stream=None):
+    _check(load_library().layernorm_run(rows, cols, in_dtype, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(bias),
+                                        float(eps), _ptr(sum_out), lds, out_dtype, _ptr(out), ldo, _ptr(out_scale),
+                                        _ptr(mean), _ptr(rstd), _stream(stream)), "layernorm_run")
+
+
+def layernorm_backward_run(rows, cols, dtype, dout, lddout, x, ldx, mean, rstd, weight, dsum, lddsum, dx, lddx, dweight,
+                           dbias, workspace=None, workspace_bytes=0, stream=None):
+    _check(load_library().layernorm_backward_run(rows, cols, dtype, _ptr(dout), lddout, _ptr(x), ldx, _ptr(mean),
+                                                 _ptr(rstd), _ptr(weight), _ptr(dsum), lddsum, _ptr(dx), lddx,
+                                                 _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace_bytes,
+                                                 _stream(stream)), "layernorm_backward_run")
+
+
+def rmsnorm_backward_run(rows, cols, dtype, dout, lddout, x, ldx, weight, eps, dsum, lddsum, dx, lddx, dweight,
+                         workspace=None, workspace_bytes=0, stream=None):
+    _check(load_library().rmsnorm_backward_run(rows, cols, dtype, _ptr(dout), lddout, _ptr(x), ldx, _ptr(weight),
+                                               float(eps), _ptr(dsum), lddsum, _ptr(dx), lddx, _ptr(dweight),
+                                               _ptr(workspace), workspace_bytes, _stream(stream)), "rmsnorm_backward_run")
+
+
+def norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return load_library().norm_backward_workspace_bytes(rows, cols)
+
+
 def bigemm_mx_scale_bytes(rows: int, cols: int) -> int:
     return load_library().bigemm_mx_scale_bytes(rows, cols)
 
@@ -411,7 +445,8 @@ def _layer():
                     (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _workspace,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
-                                    lib.matmul_workspace_bytes)))
+                                    lib.matmul_workspace_bytes, lib.layernorm_run, lib.layernorm_backward_run,
+                                    lib.rmsnorm_backward_run, lib.norm_backward_workspace_bytes)))
         _layer_module = module
     return _layer_module
 
@@ -548,3 +583,60 @@ def mx_quantize(x, out=None, scale=None, stream=None):
     if status:
         _status(status, "mx_quantize", lambda: _layer().quantize(*args), x)
     return out, scale
+
+
+def layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None, out=None, out_scale=None, sum_out=None,
+              mean_out=None, rstd_out=None, stream=None):
+    """h = x + residual; y = (h - mean(h)) * rsqrt(var(h) + eps) * weight + bias over the last axis of a matrix.
+
+    Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.  mean_out and
+    rstd_out, float32 vectors of a value per row, receive what layernorm_backward takes.
+    """
+    if residual is not None and sum_out is None:
+        sum_out = _output(None, None, x.dtype, *x.shape, x.device, stream)
+    if out is None or out_dtype is not None:
+        out = _output(out, out_dtype, x.dtype, *x.shape, x.device, stream)
+    out_scale = _output_scales(out, out_scale, stream)
+    args = (x, weight, bias, residual, eps, sum_out, mean_out, rstd_out, out, out_scale, stream)
+    status = (_layer_module or _layer()).layernorm(*args)
+    if status:
+        _status(status, "layernorm", lambda: _layer().layernorm(*args), x)
+    if residual is None:
+        return out if out_scale is None else (out, out_scale)
+    return (out, sum_out) if out_scale is None else (out, out_scale, sum_out)
+
+
+# Gradients.  They take what the forward call took and the gradient of what it gave, and return the gradients of its
+# inputs; outputs that are not given are made.  No autograd: a torch.autograd.Function is a call of each kind.
+
+def _gradient(out, like, stream):
+    import torch
+    return _new(torch.empty, like.shape, like.dtype, like.device, stream) if out is None else out
+
+
+def _sums(out, n, device, stream):
+    import torch
+    return _new(torch.empty, (n,), torch.float32, device, stream) if out is None else out
+
+
+def layernorm_backward(dout, x, mean, rstd, weight=None, dsum=None, dx=None, dweight=None, dbias=None, stream=None):
+    """(dx, dweight, dbias) of layernorm, x the rows that were normed (h where there was a residual), mean and rstd
+    from its call.  dsum, the gradient that reaches h along the residual stream, is added to dx, which may be dout or
+    dsum itself.  dout, dsum and dx are of x's dtype, dweight and dbias float32."""
+    dx = _gradient(dx, x, stream)
+    dweight, dbias = _sums(dweight, x.shape[-1], x.device, stream), _sums(dbias, x.shape[-1], x.device, stream)
+    args = (dout, x, mean, rstd, weight, 0.0, dsum, dx, dweight, dbias, stream)
+    status = (_layer_module or _layer()).norm_backward(*args)
+    if status:
+        _status(status, "layernorm_backward", lambda: _layer().norm_backward(*args), x)
+    return dx, dweight, dbias
+
+
+def rmsnorm_backward(dout, x, weight=None, eps=1e-6, dsum=None, dx=None, dweight=None, stream=None):
+    """(dx, dweight) of rmsnorm with this weight and eps, otherwise as layernorm_backward."""
+    dx, dweight = _gradient(dx, x, stream), _sums(dweight, x.shape[-1], x.device, stream)
+    args = (dout, x, None, None, weight, eps, dsum, dx, dweight, None, stream)
+    status = (_layer_module or _layer()).norm_backward(*args)
+    if status:
+        _status(status, "rmsnorm_backward", lambda: _layer().norm_backward(*args), x)
+    return dx, dweight

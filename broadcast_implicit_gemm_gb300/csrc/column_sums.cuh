@@ -1,0 +1,17 @@
+// column_sums.cuh -- the last step of sums over all rows (gradients of weights and
+// biases): rows of partial sums, added in their order.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace bigemm {
+
+// out[i][c] = sum over p < parts of from[i][p * cols + c], i < count; zeros where parts = 0.
+struct ColumnSums {
+    const float *from[2];
+    float *out[2];
+    int count, parts;
+    long long cols;
+};
+cudaError_t launch_column_sums(const ColumnSums &a, cudaStream_t stream);
+
+}  // namespace bigemm

@@ -29,6 +29,17 @@ static bigemm_status (*p_norm)(int, int, bigemm_dtype, const void *, int64_t, co
                                void *, int64_t, bigemm_dtype, void *, int64_t, void *, void *);
 static bigemm_status (*p_quantize)(int, int, bigemm_dtype, const void *, int64_t, void *, int64_t, void *, void *);
 
+static bigemm_status (*p_layernorm)(int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *,
+                                    const float *, float, void *, int64_t, bigemm_dtype, void *, int64_t, void *, float *,
+                                    float *, void *);
+static bigemm_status (*p_layernorm_backward)(int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t,
+                                             const float *, const float *, const float *, const void *, int64_t, void *,
+                                             int64_t, float *, float *, void *, uint64_t, void *);
+static bigemm_status (*p_rmsnorm_backward)(int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t,
+                                           const float *, float, const void *, int64_t, void *, int64_t, float *, void *,
+                                           uint64_t, void *);
+static uint64_t (*p_norm_workspace)(int, int);
+
 typedef struct {
     long long rows, cols, ld;
     void *ptr;
@@ -208,6 +219,25 @@ static int stream_on(PyObject *s, long device, void **stream)
     return !*stream && PyErr_Occurred() ? -1 : 0;
 }
 
+/* `bytes` of torch's memory (none for 0) beside t, the stream's until the call is done: it may be given out again
+ * after this returns. */
+static int space_for(uint64_t bytes, PyObject *t, PyObject *stream, PyObject **workspace, void **space)
+{
+    *workspace = NULL, *space = NULL;
+    if (bytes == 0) return 0;
+    PyObject *b = PyLong_FromUnsignedLongLong(bytes);
+    if (!b) return -1;
+    PyObject *const args[3] = {b, t, stream};
+    *workspace = PyObject_Vectorcall(g_workspace, args, 3, NULL);
+    Py_DECREF(b);
+    if (!*workspace) return -1;
+    if (pointer_of(*workspace, space) < 0) {
+        Py_CLEAR(*workspace);
+        return -1;
+    }
+    return 0;
+}
+
 static int arity(const char *name, Py_ssize_t got, Py_ssize_t want)
 {
     if (got == want) return 0;
@@ -242,23 +272,11 @@ static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const int r = stream_on(a[10], x.device, &stream);
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
-    PyObject *workspace = NULL;
     uint64_t bytes = 0;
     if (x.rows > 0)
         bytes = p_workspace((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld);
-    if (bytes > 0) {
-        /* torch's memory, the stream's until the call is done: it may be given out again after this returns */
-        PyObject *b = PyLong_FromUnsignedLongLong(bytes);
-        if (!b) return NULL;
-        PyObject *const args[3] = {b, a[0], a[10]};
-        workspace = PyObject_Vectorcall(g_workspace, args, 3, NULL);
-        Py_DECREF(b);
-        if (!workspace) return NULL;
-        if (pointer_of(workspace, &space) < 0) {
-            Py_DECREF(workspace);
-            return NULL;
-        }
-    }
+    PyObject *workspace;
+    if (space_for(bytes, a[0], a[10], &workspace, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (mx)
@@ -319,13 +337,83 @@ static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
+/* layernorm(x, weight, bias, residual, eps, sum_out, mean, rstd, out, out_scale, stream) -> status */
+static PyObject *layernorm(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Matrix x, res = {0}, sum = {0}, y;
+    void *weight, *bias, *mean, *rstd, *ys = NULL, *stream;
+    if (arity("layernorm", n, 11) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0) return NULL;
+    if (vector(a[1], "weight", x.cols, x.device, &weight) < 0 || vector(a[2], "bias", x.cols, x.device, &bias) < 0) return NULL;
+    if (a[3] != Py_None && matrix(a[3], "residual", &res, x.device, x.rows, x.cols) < 0) return NULL;
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (PyErr_Occurred()) return NULL;
+    if (a[5] != Py_None && matrix(a[5], "sum_out", &sum, x.device, x.rows, x.cols) < 0) return NULL;
+    if ((a[3] != Py_None && res.dtype != x.dtype) || (a[5] != Py_None && sum.dtype != x.dtype))
+        return PyErr_Format(PyExc_TypeError, "residual and sum_out are of x's dtype");
+    if (vector(a[6], "mean_out", x.rows, x.device, &mean) < 0 || vector(a[7], "rstd_out", x.rows, x.device, &rstd) < 0)
+        return NULL;
+    if (matrix(a[8], "out", &y, x.device, x.rows, x.cols) < 0) return NULL;
+    if (y.dtype == BIGEMM_MXF8 && scales(a[9], "out_scale", y.rows, y.cols, x.device, &ys) < 0) return NULL;
+    const int r = stream_on(a[10], x.device, &stream);
+    if (r < 0) return NULL;
+    if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    bigemm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = p_layernorm((int)x.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, res.ptr, res.ld, weight, bias, (float)eps,
+                     sum.ptr, sum.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, mean, rstd, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* norm_backward(dout, x, mean, rstd, weight, eps, dsum, dx, dweight, dbias, stream) -> status; the root-mean-square
+ * norm's where mean is None */
+static PyObject *norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Matrix d, x, sum = {0}, dx;
+    void *mean = NULL, *rstd = NULL, *weight, *dweight, *dbias = NULL, *stream, *space;
+    if (arity("norm_backward", n, 11) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
+        matrix(a[0], "dout", &d, x.device, x.rows, x.cols) < 0)
+        return NULL;
+    const int layer = a[9] != Py_None;
+    if (layer) {
+        if (a[2] == Py_None || a[3] == Py_None) return PyErr_Format(PyExc_ValueError, "mean and rstd: missing");
+        if (vector(a[2], "mean", x.rows, x.device, &mean) < 0 || vector(a[3], "rstd", x.rows, x.device, &rstd) < 0) return NULL;
+        if (vector(a[9], "dbias", x.cols, x.device, &dbias) < 0) return NULL;
+    }
+    if (vector(a[4], "weight", x.cols, x.device, &weight) < 0) return NULL;
+    const double eps = PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    if (a[6] != Py_None && matrix(a[6], "dsum", &sum, x.device, x.rows, x.cols) < 0) return NULL;
+    if (matrix(a[7], "dx", &dx, x.device, x.rows, x.cols) < 0) return NULL;
+    if (d.dtype != x.dtype || dx.dtype != x.dtype || (a[6] != Py_None && sum.dtype != x.dtype))
+        return PyErr_Format(PyExc_TypeError, "dout, dsum and dx are of x's dtype");
+    if (vector(a[8], "dweight", x.cols, x.device, &dweight) < 0) return NULL;
+    const int r = stream_on(a[10], x.device, &stream);
+    if (r < 0) return NULL;
+    if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    const uint64_t bytes = p_norm_workspace((int)x.rows, (int)x.cols);
+    PyObject *workspace;
+    if (space_for(bytes, a[1], a[10], &workspace, &space) < 0) return NULL;
+    bigemm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    if (layer)
+        st = p_layernorm_backward((int)x.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, mean, rstd, weight,
+                                  sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, dbias, space, bytes, stream);
+    else
+        st = p_rmsnorm_backward((int)x.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, weight, (float)eps,
+                                sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, space, bytes, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(workspace);
+    return PyLong_FromLong(st);
+}
+
 /* init(dtypes, scale_types, current_stream, current_device, workspace, functions) */
 static PyObject *init(PyObject *self, PyObject *args)
 {
     PyObject *d, *st, *cs, *cd, *ws;
-    unsigned long long f[5];
-    if (!PyArg_ParseTuple(args, "O!O!OOO(KKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &f[0], &f[1], &f[2], &f[3],
-                          &f[4]))
+    unsigned long long f[9];
+    if (!PyArg_ParseTuple(args, "O!O!OOO(KKKKKKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &f[0], &f[1], &f[2],
+                          &f[3], &f[4], &f[5], &f[6], &f[7], &f[8]))
         return NULL;
     if (PyTuple_GET_SIZE(d) != DT_COUNT || PyTuple_GET_SIZE(st) != 2)
         return PyErr_Format(PyExc_ValueError, "init: wrong number of dtypes");
@@ -339,6 +427,10 @@ static PyObject *init(PyObject *self, PyObject *args)
     p_norm = (void *)(uintptr_t)f[2];
     p_quantize = (void *)(uintptr_t)f[3];
     p_workspace = (void *)(uintptr_t)f[4];
+    p_layernorm = (void *)(uintptr_t)f[5];
+    p_layernorm_backward = (void *)(uintptr_t)f[6];
+    p_rmsnorm_backward = (void *)(uintptr_t)f[7];
+    p_norm_workspace = (void *)(uintptr_t)f[8];
     Py_RETURN_NONE;
 }
 
@@ -347,6 +439,8 @@ static PyMethodDef methods[] = {
     {"product", (PyCFunction)(void (*)(void))product, METH_FASTCALL, NULL},
     {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, NULL},
     {"quantize", (PyCFunction)(void (*)(void))quantize, METH_FASTCALL, NULL},
+    {"layernorm", (PyCFunction)(void (*)(void))layernorm, METH_FASTCALL, NULL},
+    {"norm_backward", (PyCFunction)(void (*)(void))norm_backward, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -366,6 +366,60 @@ bigemm_status rmsnorm_run(int rows, int cols, bigemm_dtype in_dtype, const void 
                           void *sum_out, int64_t lds, bigemm_dtype out_dtype, void *out, int64_t ldo,
                           void *out_scale, void *stream);
 
+/*
+ * layernorm_run -- h = x + residual; out = (h - mean(h)) * rsqrt(var(h) + eps) *
+ * weight + bias, row by row over `cols` columns, var the mean square of h - mean(h);
+ * in fp32 from the inputs to one rounding of each output.
+ *   x, residual (NULL: none), sum_out (NULL: not wanted; receives h; it may be x or
+ *   residual itself) of in_dtype (F32, F16, BF16); weight, bias [cols] fp32, each or
+ *   NULL (ones, zeros); out of in_dtype, F32, or MXF8 (then out_scale, else NULL)
+ *   mean, rstd [rows] fp32, each or NULL (not wanted): of h before it is rounded,
+ *   what layernorm_backward_run takes
+ * Errors: INVALID_ARG, UNSUPPORTED (another out_dtype; cols above 2^30), CUDA.
+ */
+bigemm_status layernorm_run(int rows, int cols, bigemm_dtype in_dtype, const void *x, int64_t ldx,
+                            const void *residual, int64_t ldr, const float *weight,
+                            const float *bias, float eps, void *sum_out, int64_t lds,
+                            bigemm_dtype out_dtype, void *out, int64_t ldo, void *out_scale,
+                            float *mean, float *rstd, void *stream);
+
+/*
+ * layernorm_backward_run -- gradients of out = (x - mean) * rstd * weight + bias, of
+ * dout, that of out.  With xh = (x - mean) rstd and g = dout * weight, mean over k:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + dsum
+ *   dweight[k] = sum over rows of dout xh,  dbias[k] = sum over rows of dout
+ * in fp32, dx rounded once; the sums' order does not depend on timing.
+ *   dout, x (the normed rows: h where there was a residual), dsum (NULL: none; the
+ *   gradient that reaches h along the residual stream) and dx of dtype (F32, F16,
+ *   BF16); dx may be dout or dsum itself
+ *   mean, rstd [rows] of the forward pass; weight [cols] or NULL (ones); dweight,
+ *   dbias [cols], all fp32.  rows = 0 writes zeros to dweight and dbias.
+ *   workspace: norm_backward_workspace_bytes of device memory on a 16-byte boundary,
+ *   the call's until it is done.
+ * Errors: INVALID_ARG, UNSUPPORTED (cols above 2^30), CUDA.
+ */
+bigemm_status layernorm_backward_run(int rows, int cols, bigemm_dtype dtype, const void *dout,
+                                     int64_t lddout, const void *x, int64_t ldx, const float *mean,
+                                     const float *rstd, const float *weight, const void *dsum,
+                                     int64_t lddsum, void *dx, int64_t lddx, float *dweight,
+                                     float *dbias, void *workspace, uint64_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * rmsnorm_backward_run -- gradients of out = x * rstd * weight, rstd = rsqrt(mean(x^2)
+ * + eps), found again from x.  With xh = x rstd and g = dout * weight:
+ *   dx = rstd (g - xh mean(g xh)) + dsum,  dweight[k] = sum over rows of dout xh
+ * Otherwise as layernorm_backward_run.
+ */
+bigemm_status rmsnorm_backward_run(int rows, int cols, bigemm_dtype dtype, const void *dout,
+                                   int64_t lddout, const void *x, int64_t ldx, const float *weight,
+                                   float eps, const void *dsum, int64_t lddsum, void *dx,
+                                   int64_t lddx, float *dweight, void *workspace,
+                                   uint64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that either norm's gradients need. */
+uint64_t norm_backward_workspace_bytes(int rows, int cols);
+
 /* mx_quantize_run -- a matrix of in_dtype (F32, F16, BF16) as MXF8. */
 bigemm_status mx_quantize_run(int rows, int cols, bigemm_dtype in_dtype, const void *x, int64_t ldx,
                               void *out, int64_t ldo, void *scale, void *stream);
