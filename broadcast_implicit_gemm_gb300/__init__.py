@@ -27,9 +27,10 @@ __all__ = [
     "COMBINE_NONE", "COMBINE_ADD", "COMBINE_MUL", "COMBINE_NAMES",
     "matmul_run", "matmul_mx_run", "matmul_workspace_bytes", "rmsnorm_run", "mx_quantize_run",
     "bigemm_mx_scale_bytes", "layernorm_run", "layernorm_backward_run", "rmsnorm_backward_run",
-    "norm_backward_workspace_bytes",
+    "norm_backward_workspace_bytes", "matmul_gated_run", "matmul_gated_workspace_bytes", "matmul_backward_run",
+    "matmul_backward_workspace_bytes", "matmul_gated_backward_run", "matmul_gated_backward_workspace_bytes",
     "matmul", "matmul_mx", "rmsnorm", "mx_quantize", "mx_scale_shape", "layernorm", "layernorm_backward",
-    "rmsnorm_backward",
+    "rmsnorm_backward", "matmul_gated", "matmul_backward", "matmul_gated_backward",
     "bigemm_status_string", "bigemm_last_device_error", "bigemm_clear_device_error",
     "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout", "bigemm_profile_enable",
     "bigemm_profile_read", "bigemm_version", "conv2d", "bcast", "out_size",
@@ -118,6 +119,15 @@ def _declare(lib):
     lib.rmsnorm_backward_run.argtypes = [i, i, i, p, i64, p, i64, p, f, p, i64, p, i64, p, p, u64, p]
     lib.norm_backward_workspace_bytes.argtypes = [i, i]
     lib.norm_backward_workspace_bytes.restype = u64
+    at = [p, i64]      # a matrix
+    lib.matmul_gated_run.argtypes = [i] * 4 + at * 3 + [p, p, i] + at * 3 + [p, u64, p]
+    lib.matmul_gated_workspace_bytes.argtypes = [i] * 3 + at * 3
+    lib.matmul_backward_run.argtypes = [i] * 4 + at * 5 + [p, p, u64, p]
+    lib.matmul_backward_workspace_bytes.argtypes = [i] * 3 + at * 3
+    lib.matmul_gated_backward_run.argtypes = [i] * 4 + at * 6 + [i] + at * 3 + [p, p, p, u64, p]
+    lib.matmul_gated_backward_workspace_bytes.argtypes = [i] * 3 + at * 3
+    for name in ("matmul_gated", "matmul_backward", "matmul_gated_backward"):
+        getattr(lib, name + "_workspace_bytes").restype = u64
     lib.bigemm_status_string.argtypes = [i]
     lib.bigemm_status_string.restype = ctypes.c_char_p
     lib.bigemm_last_device_error.argtypes = []
@@ -133,6 +143,7 @@ def _declare(lib):
                  "conv2d_nchw_plan_destroy", "conv2d_nchw_plan_describe", "bcast_nchw_run",
                  "bcast_nchw_run_flat", "bcast_run", "matmul_run", "matmul_mx_run", "rmsnorm_run",
                  "mx_quantize_run", "layernorm_run", "layernorm_backward_run", "rmsnorm_backward_run",
+                 "matmul_gated_run", "matmul_backward_run", "matmul_gated_backward_run",
                  "bigemm_last_device_error",
                  "bigemm_clear_device_error",
                  "bigemm_set_wait_timeout_ns", "bigemm_debug_wait_timeout",
@@ -325,6 +336,43 @@ def norm_backward_workspace_bytes(rows: int, cols: int) -> int:
     return load_library().norm_backward_workspace_bytes(rows, cols)
 
 
+def matmul_gated_run(M, N, K, dtype, x, ldx, w_gate, ldw_gate, w_up, ldw_up, bias_gate, bias_up, act, out, ldo, gate=None,
+                     ldgate=0, up=None, ldup=0, workspace=None, workspace_bytes=0, stream=None):
+    _check(load_library().matmul_gated_run(M, N, K, dtype, _ptr(x), ldx, _ptr(w_gate), ldw_gate, _ptr(w_up), ldw_up,
+                                           _ptr(bias_gate), _ptr(bias_up), act, _ptr(out), ldo, _ptr(gate), ldgate, _ptr(up),
+                                           ldup, _ptr(workspace), workspace_bytes, _stream(stream)), "matmul_gated_run")
+
+
+def matmul_gated_workspace_bytes(M, N, K, x, ldx, w_gate, ldw_gate, w_up, ldw_up) -> int:
+    return load_library().matmul_gated_workspace_bytes(M, N, K, _ptr(x), ldx, _ptr(w_gate), ldw_gate, _ptr(w_up), ldw_up)
+
+
+def matmul_backward_run(M, N, K, dtype, dout, lddout, x, ldx, w, ldw, dx, lddx, dw, lddw, dbias=None, workspace=None,
+                        workspace_bytes=0, stream=None):
+    _check(load_library().matmul_backward_run(M, N, K, dtype, _ptr(dout), lddout, _ptr(x), ldx, _ptr(w), ldw, _ptr(dx), lddx,
+                                              _ptr(dw), lddw, _ptr(dbias), _ptr(workspace), workspace_bytes,
+                                              _stream(stream)), "matmul_backward_run")
+
+
+def matmul_backward_workspace_bytes(M, N, K, dout, lddout, x, ldx, w, ldw) -> int:
+    return load_library().matmul_backward_workspace_bytes(M, N, K, _ptr(dout), lddout, _ptr(x), ldx, _ptr(w), ldw)
+
+
+def matmul_gated_backward_run(M, N, K, dtype, dout, lddout, x, ldx, w_gate, ldw_gate, w_up, ldw_up, gate, ldgate, up, ldup,
+                              act, dx, lddx, dw_gate, lddw_gate, dw_up, lddw_up, dbias_gate=None, dbias_up=None,
+                              workspace=None, workspace_bytes=0, stream=None):
+    _check(load_library().matmul_gated_backward_run(M, N, K, dtype, _ptr(dout), lddout, _ptr(x), ldx, _ptr(w_gate), ldw_gate,
+                                                    _ptr(w_up), ldw_up, _ptr(gate), ldgate, _ptr(up), ldup, act, _ptr(dx),
+                                                    lddx, _ptr(dw_gate), lddw_gate, _ptr(dw_up), lddw_up,
+                                                    _ptr(dbias_gate), _ptr(dbias_up), _ptr(workspace), workspace_bytes,
+                                                    _stream(stream)), "matmul_gated_backward_run")
+
+
+def matmul_gated_backward_workspace_bytes(M, N, K, x, ldx, w_gate, ldw_gate, w_up, ldw_up) -> int:
+    return load_library().matmul_gated_backward_workspace_bytes(M, N, K, _ptr(x), ldx, _ptr(w_gate), ldw_gate, _ptr(w_up),
+                                                                ldw_up)
+
+
 def bigemm_mx_scale_bytes(rows: int, cols: int) -> int:
     return load_library().bigemm_mx_scale_bytes(rows, cols)
 
@@ -446,7 +494,10 @@ def _layer():
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
                                     lib.matmul_workspace_bytes, lib.layernorm_run, lib.layernorm_backward_run,
-                                    lib.rmsnorm_backward_run, lib.norm_backward_workspace_bytes)))
+                                    lib.rmsnorm_backward_run, lib.norm_backward_workspace_bytes, lib.matmul_gated_run,
+                                    lib.matmul_gated_workspace_bytes, lib.matmul_backward_run,
+                                    lib.matmul_backward_workspace_bytes, lib.matmul_gated_backward_run,
+                                    lib.matmul_gated_backward_workspace_bytes)))
         _layer_module = module
     return _layer_module
 
@@ -585,6 +636,23 @@ def mx_quantize(x, out=None, scale=None, stream=None):
     return out, scale
 
 
+def matmul_gated(x, w_gate, w_up, bias_gate=None, bias_up=None, act=ACT_SILU, out=None, gate_out=None, up_out=None,
+                 stream=None):
+    """act(x @ w_gate.T + bias_gate) * (x @ w_up.T + bias_up) in one kernel: x [M, K], w_gate and w_up [N, K] float16 or
+    bfloat16, biases [N] float32.
+
+    Sums in fp32; the result is of x's type.  gate_out and up_out, [M, N] of it too, receive the two sums before the
+    activation and the multiplication, which matmul_gated_backward takes.
+    """
+    if out is None:
+        out = _output(None, None, x.dtype, x.shape[0], w_gate.shape[0], x.device, stream)
+    args = (x, w_gate, w_up, bias_gate, bias_up, act, out, gate_out, up_out, stream)
+    status = (_layer_module or _layer()).gated(*args)
+    if status:
+        _status(status, "matmul_gated", lambda: _layer().gated(*args), x)
+    return out
+
+
 def layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None, out=None, out_scale=None, sum_out=None,
               mean_out=None, rstd_out=None, stream=None):
     """h = x + residual; y = (h - mean(h)) * rsqrt(var(h) + eps) * weight + bias over the last axis of a matrix.
@@ -640,3 +708,28 @@ def rmsnorm_backward(dout, x, weight=None, eps=1e-6, dsum=None, dx=None, dweight
     if status:
         _status(status, "rmsnorm_backward", lambda: _layer().norm_backward(*args), x)
     return dx, dweight
+
+
+def matmul_backward(dout, x, w, dx=None, dw=None, dbias=None, stream=None):
+    """(dx, dw) of x @ w.T: dout @ w and dout.T @ x, of the operands' type (float16 or bfloat16), sums in fp32.  dbias, a
+    float32 vector, receives the sum of dout over the tokens."""
+    dx, dw = _gradient(dx, x, stream), _gradient(dw, w, stream)
+    args = (dout, x, w, dx, dw, dbias, stream)
+    status = (_layer_module or _layer()).product_backward(*args)
+    if status:
+        _status(status, "matmul_backward", lambda: _layer().product_backward(*args), x)
+    return dx, dw
+
+
+def matmul_gated_backward(dout, x, w_gate, w_up, gate, up, act=ACT_SILU, dx=None, dw_gate=None, dw_up=None,
+                          dbias_gate=None, dbias_up=None, stream=None):
+    """(dx, dw_gate, dw_up) of matmul_gated with this act, gate and up as its call gave them to gate_out and up_out.  The
+    gradients of the two sums are rounded to the operands' type before their products.  dbias_gate and dbias_up, float32
+    vectors, receive their sums over the tokens."""
+    dx = _gradient(dx, x, stream)
+    dw_gate, dw_up = _gradient(dw_gate, w_gate, stream), _gradient(dw_up, w_up, stream)
+    args = (dout, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, dbias_gate, dbias_up, stream)
+    status = (_layer_module or _layer()).gated_backward(*args)
+    if status:
+        _status(status, "matmul_gated_backward", lambda: _layer().gated_backward(*args), x)
+    return dx, dw_gate, dw_up

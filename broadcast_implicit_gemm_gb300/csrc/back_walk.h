@@ -1,0 +1,53 @@
+// back_walk.h -- which unit of the gradients' products (matmul_back.cu) a pair of CTAs
+// takes at each turn.
+//
+// Units 0 to dx - 1 are dx's, long ones, and dx to dx + dw - 1 are dw's.  The pairs take
+// the dx units in turn; the `late` ones that get one fewer take `ahead` dw units each
+// meanwhile, and then all walk the rest in turn.
+//
+// No CUDA dependency on the host side, so that a plain C++ test can check it.
+#pragma once
+
+#if defined(__CUDACC__)
+#define BIGEMM_BW_HD __host__ __device__ __forceinline__
+#else
+#define BIGEMM_BW_HD inline
+#endif
+
+namespace bigemm {
+
+struct BackWalk {
+    int dx, dw;                      // units
+    int late, ahead;
+};
+
+// dx_time, dw_time: a unit's, in the same measure.
+BIGEMM_BW_HD BackWalk make_back_walk(int dx, int dw, int pairs, long long dx_time, long long dw_time)
+{
+    BackWalk w = {dx, dw, 0, 0};
+    if (dx % pairs) {
+        w.late = pairs - dx % pairs;
+        const long long fit = dx_time / dw_time, most = dw / w.late;
+        w.ahead = (int)(fit < most ? fit : most);
+    }
+    return w;
+}
+
+// The pair's unit of a turn; -1: none left.
+BIGEMM_BW_HD int back_unit(const BackWalk &w, int turn, int pair, int pairs)
+{
+    const int i = turn * pairs + pair;
+    if (i < w.dx) return i;
+    const int first = pairs - w.late, behind = w.dx / pairs + (pair < w.dx % pairs ? 1 : 0);
+    int j = turn - behind;           // turns since this pair's last dx unit
+    int k;
+    if (pair >= first && j < w.ahead) {
+        k = j * w.late + (pair - first);
+    } else {
+        if (pair >= first) j -= w.ahead;
+        k = w.ahead * w.late + j * pairs + pair;
+    }
+    return k < w.dw ? w.dx + k : -1;
+}
+
+}  // namespace bigemm

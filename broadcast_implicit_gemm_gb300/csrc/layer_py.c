@@ -39,6 +39,18 @@ static bigemm_status (*p_rmsnorm_backward)(int, int, bigemm_dtype, const void *,
                                            const float *, float, const void *, int64_t, void *, int64_t, float *, void *,
                                            uint64_t, void *);
 static uint64_t (*p_norm_workspace)(int, int);
+static bigemm_status (*p_gated)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const void *, int64_t,
+                                const float *, const float *, int, void *, int64_t, void *, int64_t, void *, int64_t, void *,
+                                uint64_t, void *);
+static uint64_t (*p_gated_workspace)(int, int, int, const void *, int64_t, const void *, int64_t, const void *, int64_t);
+static bigemm_status (*p_backward)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const void *,
+                                   int64_t, void *, int64_t, void *, int64_t, float *, void *, uint64_t, void *);
+static uint64_t (*p_backward_workspace)(int, int, int, const void *, int64_t, const void *, int64_t, const void *, int64_t);
+static bigemm_status (*p_gated_backward)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const void *,
+                                         int64_t, const void *, int64_t, const void *, int64_t, const void *, int64_t, int,
+                                         void *, int64_t, void *, int64_t, void *, int64_t, float *, float *, void *, uint64_t,
+                                         void *);
+static uint64_t (*p_gated_backward_workspace)(int, int, int, const void *, int64_t, const void *, int64_t, const void *, int64_t);
 
 typedef struct {
     long long rows, cols, ld;
@@ -407,14 +419,117 @@ static PyObject *norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
+/* A matrix of x's type, or nothing for None where `optional`. */
+static int beside(PyObject *t, const char *name, Matrix *m, const Matrix *x, long long rows, long long cols, int optional)
+{
+    if (optional && t == Py_None) return 0;
+    if (matrix(t, name, m, x->device, rows, cols) < 0) return -1;
+    if (m->dtype == x->dtype) return 0;
+    PyErr_Format(PyExc_TypeError, "%s: of another dtype than x", name);
+    return -1;
+}
+
+/* gated(x, w_gate, w_up, bias_gate, bias_up, act, out, gate, up, stream) -> status */
+static PyObject *gated(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Matrix x, wg, wu, y, g = {0}, u = {0};
+    void *bg, *bu, *stream, *space;
+    if (arity("gated", n, 10) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 || beside(a[1], "w_gate", &wg, &x, -1, x.cols, 0) < 0 ||
+        beside(a[2], "w_up", &wu, &x, wg.rows, x.cols, 0) < 0 || vector(a[3], "bias_gate", wg.rows, x.device, &bg) < 0 ||
+        vector(a[4], "bias_up", wg.rows, x.device, &bu) < 0)
+        return NULL;
+    const int act = (int)PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    if (beside(a[6], "out", &y, &x, x.rows, wg.rows, 0) < 0 || beside(a[7], "gate_out", &g, &x, x.rows, wg.rows, 1) < 0 ||
+        beside(a[8], "up_out", &u, &x, x.rows, wg.rows, 1) < 0)
+        return NULL;
+    const int r = stream_on(a[9], x.device, &stream);
+    if (r < 0) return NULL;
+    if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    const uint64_t bytes = p_gated_workspace((int)x.rows, (int)wg.rows, (int)x.cols, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr, wu.ld);
+    PyObject *workspace;
+    if (space_for(bytes, a[0], a[9], &workspace, &space) < 0) return NULL;
+    bigemm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = p_gated((int)x.rows, (int)wg.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr, wu.ld, bg, bu,
+                 act, y.ptr, y.ld, g.ptr, g.ld, u.ptr, u.ld, space, bytes, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(workspace);
+    return PyLong_FromLong(st);
+}
+
+/* product_backward(dout, x, w, dx, dw, dbias, stream) -> status */
+static PyObject *product_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Matrix d, x, w, dx, dw;
+    void *dbias, *stream, *space;
+    if (arity("product_backward", n, 7) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
+        beside(a[2], "w", &w, &x, -1, x.cols, 0) < 0 || beside(a[0], "dout", &d, &x, x.rows, w.rows, 0) < 0 ||
+        beside(a[3], "dx", &dx, &x, x.rows, x.cols, 0) < 0 || beside(a[4], "dw", &dw, &x, w.rows, x.cols, 0) < 0 ||
+        vector(a[5], "dbias", w.rows, x.device, &dbias) < 0)
+        return NULL;
+    const int r = stream_on(a[6], x.device, &stream);
+    if (r < 0) return NULL;
+    if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    const uint64_t bytes = p_backward_workspace((int)x.rows, (int)w.rows, (int)x.cols, d.ptr, d.ld, x.ptr, x.ld, w.ptr, w.ld);
+    PyObject *workspace;
+    if (space_for(bytes, a[1], a[6], &workspace, &space) < 0) return NULL;
+    bigemm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = p_backward((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, w.ptr, w.ld, dx.ptr,
+                    dx.ld, dw.ptr, dw.ld, dbias, space, bytes, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(workspace);
+    return PyLong_FromLong(st);
+}
+
+/* gated_backward(dout, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, dbias_gate, dbias_up, stream) -> status */
+static PyObject *gated_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    Matrix d, x, wg, wu, g, u, dx, dwg, dwu;
+    void *dbg, *dbu, *stream, *space;
+    if (arity("gated_backward", n, 13) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
+        beside(a[2], "w_gate", &wg, &x, -1, x.cols, 0) < 0 || beside(a[3], "w_up", &wu, &x, wg.rows, x.cols, 0) < 0 ||
+        beside(a[0], "dout", &d, &x, x.rows, wg.rows, 0) < 0 || beside(a[4], "gate", &g, &x, x.rows, wg.rows, 0) < 0 ||
+        beside(a[5], "up", &u, &x, x.rows, wg.rows, 0) < 0)
+        return NULL;
+    const int act = (int)PyLong_AsLong(a[6]);
+    if (PyErr_Occurred()) return NULL;
+    if (beside(a[7], "dx", &dx, &x, x.rows, x.cols, 0) < 0 || beside(a[8], "dw_gate", &dwg, &x, wg.rows, x.cols, 0) < 0 ||
+        beside(a[9], "dw_up", &dwu, &x, wg.rows, x.cols, 0) < 0 || vector(a[10], "dbias_gate", wg.rows, x.device, &dbg) < 0 ||
+        vector(a[11], "dbias_up", wg.rows, x.device, &dbu) < 0)
+        return NULL;
+    const int r = stream_on(a[12], x.device, &stream);
+    if (r < 0) return NULL;
+    if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
+    const uint64_t bytes = p_gated_backward_workspace((int)x.rows, (int)wg.rows, (int)x.cols, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr,
+                                                      wu.ld);
+    PyObject *workspace;
+    if (space_for(bytes, a[1], a[12], &workspace, &space) < 0) return NULL;
+    bigemm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = p_gated_backward((int)x.rows, (int)wg.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, wg.ptr, wg.ld,
+                          wu.ptr, wu.ld, g.ptr, g.ld, u.ptr, u.ld, act, dx.ptr, dx.ld, dwg.ptr, dwg.ld, dwu.ptr, dwu.ld, dbg,
+                          dbu, space, bytes, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(workspace);
+    return PyLong_FromLong(st);
+}
+
 /* init(dtypes, scale_types, current_stream, current_device, workspace, functions) */
 static PyObject *init(PyObject *self, PyObject *args)
 {
     PyObject *d, *st, *cs, *cd, *ws;
-    unsigned long long f[9];
-    if (!PyArg_ParseTuple(args, "O!O!OOO(KKKKKKKKK)", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &f[0], &f[1], &f[2],
-                          &f[3], &f[4], &f[5], &f[6], &f[7], &f[8]))
+    PyObject *functions;
+    enum { COUNT = 15 };
+    unsigned long long f[COUNT];
+    if (!PyArg_ParseTuple(args, "O!O!OOOO!", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &PyTuple_Type, &functions))
         return NULL;
+    if (PyTuple_GET_SIZE(functions) != COUNT) return PyErr_Format(PyExc_ValueError, "init: wrong number of functions");
+    for (int i = 0; i < COUNT; ++i) {
+        f[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(functions, i));
+        if (PyErr_Occurred()) return NULL;
+    }
     if (PyTuple_GET_SIZE(d) != DT_COUNT || PyTuple_GET_SIZE(st) != 2)
         return PyErr_Format(PyExc_ValueError, "init: wrong number of dtypes");
     for (int i = 0; i < DT_COUNT; ++i) g_dtypes[i] = Py_NewRef(PyTuple_GET_ITEM(d, i));
@@ -431,6 +546,12 @@ static PyObject *init(PyObject *self, PyObject *args)
     p_layernorm_backward = (void *)(uintptr_t)f[6];
     p_rmsnorm_backward = (void *)(uintptr_t)f[7];
     p_norm_workspace = (void *)(uintptr_t)f[8];
+    p_gated = (void *)(uintptr_t)f[9];
+    p_gated_workspace = (void *)(uintptr_t)f[10];
+    p_backward = (void *)(uintptr_t)f[11];
+    p_backward_workspace = (void *)(uintptr_t)f[12];
+    p_gated_backward = (void *)(uintptr_t)f[13];
+    p_gated_backward_workspace = (void *)(uintptr_t)f[14];
     Py_RETURN_NONE;
 }
 
@@ -440,6 +561,9 @@ static PyMethodDef methods[] = {
     {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, NULL},
     {"quantize", (PyCFunction)(void (*)(void))quantize, METH_FASTCALL, NULL},
     {"layernorm", (PyCFunction)(void (*)(void))layernorm, METH_FASTCALL, NULL},
+    {"gated", (PyCFunction)(void (*)(void))gated, METH_FASTCALL, NULL},
+    {"product_backward", (PyCFunction)(void (*)(void))product_backward, METH_FASTCALL, NULL},
+    {"gated_backward", (PyCFunction)(void (*)(void))gated_backward, METH_FASTCALL, NULL},
     {"norm_backward", (PyCFunction)(void (*)(void))norm_backward, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 

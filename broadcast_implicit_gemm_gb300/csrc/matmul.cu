@@ -3,15 +3,12 @@
 #include <algorithm>
 
 #include "matmul.cuh"
+#include "matmul_gated.cuh"
+#include "matmul_host.cuh"
 
 using namespace bigemm;
 
 namespace {
-
-bool on_grid(const void *p, long long ld, long long size, long long to)
-{
-    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0 && (ld * size) % to == 0;
-}
 
 // The scales of a rows x cols MXFP8 matrix as boxes of `blocks` blocks, one below the other.
 bool scale_map(CUtensorMap *map, const void *p, long long rows, long long cols, int blocks)
@@ -42,20 +39,6 @@ bool out_map(CUtensorMap *map, const MatmulArgs &a)
                                   : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
-// A row-major operand as boxes of box_rows rows by 128 bytes, 128-byte swizzle.
-bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows, long long cols, long long ld, int box_rows)
-{
-    const size_t es = dt == BIGEMM_MXF8 ? 1 : 2;
-    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
-    const uint64_t strides[1] = {(uint64_t)ld * es};
-    const uint32_t box[2] = {(uint32_t)(kRow / es), (uint32_t)box_rows};
-    const uint32_t ones[2] = {1, 1};
-    const CUtensorMapDataType t = dt == BIGEMM_MXF8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                  : dt == BIGEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return encode_tiled(map, t, 2, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 // Which kernel, and how it is cut: the least of estimates in nanoseconds whose
 // terms were fitted to measurements (each term says to which).
 struct Choice {
@@ -63,8 +46,6 @@ struct Choice {
     int bn;          // many tokens: channels per tile
     FewCut few;
 };
-
-long long up(long long a, long long b) { return (a + b - 1) / b; }
 
 // Few tokens: bn tokens per tile, `split` CTAs on a tile's K.  A start and an end
 // of 3.6 us; a block of K (128 bytes of each row) in 0.165 us, or as long as it
@@ -78,15 +59,17 @@ long long up(long long a, long long b) { return (a + b - 1) / b; }
 // Weights that fill the machine come at 6.8 TB/s: 1 x 4096 x 4096 in 8: 8.1 us.
 // Rows of the output or of other off the 16-byte grid go element by element, 60
 // ns a token (777 x 5001 x 1000: 34 us, 128 tokens to a tile).
+// GATED: tiles of 64 channels, and twice the weights.
+template <bool GATED>
 long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 {
-    const long long grid = up(a.N, 128) * up(a.M, c.bn) * c.split;
+    const long long grid = up(a.N, GATED ? 64 : 128) * up(a.M, c.bn) * c.split;
     const long long beside = c.alone ? 1 : std::min<long long>(2, up(grid, sms)), waves = up(grid, beside * sms);
     const long long mine = up(std::min(a.M, c.bn), c.split);
     const bool ragged = !a.vec_out || (a.combine != BIGEMM_COMBINE_NONE && !a.vec_other);
     const long long one = up(a.k_blocks, c.split) * std::max<long long>(165, beside * (128 + c.bn)) + 23 * mine + 22 * c.bn +
                           2 * (c.split - 1) * beside * c.bn + (ragged ? 60 * mine * beside : 0);
-    const long long memory = (long long)a.k_blocks * kRow * a.N / 6800;
+    const long long memory = (long long)a.k_blocks * kRow * a.N * (GATED ? 2 : 1) / 6800;
     return 3600 + std::max(memory, waves * one);
 }
 
@@ -95,9 +78,9 @@ long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 // not the tensor core, sets the pace), with MXFP8 operands 0.44 and 0.36.
 // 4096 x 4096 x 4096 bf16: 79.6 us in 4 waves of 256, 110 in 7 of 128; 512 x 4096
 // x 4096 24.7 in one wave of 256, 20.9 in one of 128.
-long long many_cost(const MatmulArgs &a, int sms, int bn)
+long long many_cost(const MatmulArgs &a, int sms, int bn, int channels)
 {
-    const long long waves = up(up(a.M, kManyTokens) * up(a.N, bn), sms / 2);
+    const long long waves = up(up(a.M, kManyTokens) * up(a.N, channels), sms / 2);
     const bool mx = a.in_dt == BIGEMM_MXF8;
     return 3500 + waves * a.k_blocks * (bn == 256 ? (mx ? 440 : 330) : (mx ? 360 : 260));
 }
@@ -105,6 +88,8 @@ long long many_cost(const MatmulArgs &a, int sms, int bn)
 // 256 x 4096 x 4096 bf16: 17.9 us for few (64 tokens, K in 2) against 20.4 and
 // 24.4 in pairs; 512 x 4096 x 4096: 25 against 20.9 and 24.7; 1024 x 1024 x 8192:
 // 25.5 against 34.5 and 40.9.
+// GATED: the pairs' tiles have 128 channels of each product.
+template <bool GATED = false>
 Choice choose(const MatmulArgs &a, int sms)
 {
     const bool mx = a.in_dt == BIGEMM_MXF8;
@@ -115,28 +100,26 @@ Choice choose(const MatmulArgs &a, int sms)
         // would start inside a block of scales
         if ((bn == 128 && matmul_in_pieces(a)) || (mx && bn < 64 && a.M > bn)) continue;
         if (up(a.M, bn) > 65535) continue;     // the grid's second axis
-        const long long tiles = up(a.N, 128) * up(a.M, bn);
+        const long long tiles = up(a.N, GATED ? 64 : 128) * up(a.M, bn);
         // clusters of 5 to 7 CTAs leave SMs of their neighbourhood idle (300 x 1000 x 2048: 13.6 us in
         // 7, 8.9 in 4)
         for (int split : {1, 2, 3, 4, 8}) {
             if (split > 1 && (split * 4 > a.k_blocks || tiles * split > 2ll * sms)) break;
             for (int alone = 0; alone <= (bn >= 64 && tiles * split <= sms ? 1 : 0); ++alone) {
                 const FewCut cut = {bn, split, alone != 0};
-                const long long cost = few_cost(a, sms, cut);
+                const long long cost = few_cost<GATED>(a, sms, cut);
                 if (least < 0 || cost <= least) c.few = cut, least = cost;
             }
         }
         if (bn >= a.M) break;                  // larger tiles hold no more
     }
     if (a.M > 128)
-        for (int bn = 128; bn <= 256; bn += 128) {
-            const long long cost = many_cost(a, sms, bn);
+        for (int bn = GATED ? 256 : 128; bn <= 256; bn += 128) {
+            const long long cost = many_cost(a, sms, bn, GATED ? bn / 2 : bn);
             if (least < 0 || cost < least) c.many = true, c.bn = bn, least = cost;
         }
     return c;
 }
-
-constexpr int kMaxSize = 1 << 30;   // indices within a row are in 32 bits, byte offsets in 64
 
 // 128-byte pieces of a row that one tensor-memory accumulator sums where K is
 // summed in pieces: 512 products of 16-bit operands (32 additions), 2048 of MXFP8 ones
@@ -146,13 +129,6 @@ constexpr int kMaxSize = 1 << 30;   // indices within a row are in 32 bits, byte
 // pieces of 4096 3.3e-7 and 191, of 2048 1.5e-7 and 216, of 1024 1.0e-7 and 265; a
 // plain fp32 product 1.5e-7.
 int full_segment(bool mx) { return mx ? 16 : 8; }
-
-constexpr long long kFar = 1ll << 40;           // TMA: strides below 2^40 bytes
-
-// Whether TMA can address an operand's rows.
-bool addressable(const void *p, long long ld, long long es) { return on_grid(p, ld, es, 16) && ld * es < kFar; }
-
-long long packed_bytes(long long rows, long long cols, long long es) { return up(rows * up(cols * es, 16) * 16, 256) * 256; }
 
 uint64_t workspace_for(long long M, long long N, long long K, long long es, const void *x, long long ldx, const void *w,
                        long long ldw)
@@ -167,19 +143,10 @@ uint64_t workspace_for(long long M, long long N, long long K, long long es, cons
 // 6.5 for 8 x 64 x 65 against 5.0, 360 for 1000 x 4096 x 4097 against 45.)
 cudaError_t pack(MatmulArgs &a, long long es, uint8_t *workspace, cudaStream_t stream)
 {
-    PackArgs k = {};
-    if (!addressable(a.w, a.ldw, es)) {
-        const long long pitch = up(a.K * es, 16) * 16;
-        k.op[0] = {static_cast<const uint8_t *>(a.w), workspace, a.N, a.ldw * es, pitch, a.K * es, 0};
-        a.w = workspace, a.ldw = pitch / es;
-        workspace += packed_bytes(a.N, a.K, es);
-    }
-    if (!addressable(a.x, a.ldx, es)) {
-        const long long pitch = up(a.K * es, 16) * 16;
-        k.op[1] = {static_cast<const uint8_t *>(a.x), workspace, a.M, a.ldx * es, pitch, a.K * es, 0};
-        a.x = workspace, a.ldx = pitch / es;
-    }
-    return launch_matmul_pack(k, stream);
+    PackList k(workspace);
+    k.add(a.w, a.ldw, a.N, a.K, es);
+    k.add(a.x, a.ldx, a.M, a.K, es);
+    return k.run(stream);
 }
 
 bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, void *stream)
@@ -243,6 +210,70 @@ bigemm_status product(MatmulArgs &a, void *workspace, uint64_t workspace_bytes, 
     return e == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
 }
 
+// A 16-bit output as boxes of 32 rows by 32 columns (if its rows are on the grid; true where none is needed).
+bool put_map(CUtensorMap *map, bool vec, void *p, int dt, long long rows, long long cols, long long ld)
+{
+    return !p || !vec || box_map(map, p, dt, rows, cols, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+uint64_t gated_workspace(const GatedArgs &a)
+{
+    return (uint64_t)((addressable(a.w, a.ldw, 2) ? 0 : packed_bytes(a.N, a.K, 2)) +
+                      (addressable(a.w_up, a.ldw_up, 2) ? 0 : packed_bytes(a.N, a.K, 2)) +
+                      (addressable(a.x, a.ldx, 2) ? 0 : packed_bytes(a.M, a.K, 2)));
+}
+
+bigemm_status gated(GatedArgs &a, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    if (a.M < 0 || a.N < 1 || a.K < 1 || a.act < BIGEMM_ACT_NONE || a.act > BIGEMM_ACT_SILU) return BIGEMM_ERR_INVALID_ARG;
+    if (a.M == 0) return BIGEMM_OK;
+    if (a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize) return BIGEMM_ERR_UNSUPPORTED;
+    if (!a.x || !a.w || !a.w_up || !a.out) return BIGEMM_ERR_INVALID_ARG;
+    if (a.ldx < a.K || a.ldw < a.K || a.ldw_up < a.K || a.ldo < a.N || (a.gate && a.ldgate < a.N) || (a.up && a.ldup < a.N))
+        return BIGEMM_ERR_INVALID_ARG;
+    if (!on_grid(a.x, 0, 1, 2) || !on_grid(a.w, 0, 1, 2) || !on_grid(a.w_up, 0, 1, 2) || !on_grid(a.out, 0, 1, 2) ||
+        !on_grid(a.gate, 0, 1, 2) || !on_grid(a.up, 0, 1, 2) || !on_grid(a.bias, 0, 1, 4) || !on_grid(a.bias_up, 0, 1, 4))
+        return BIGEMM_ERR_INVALID_ARG;
+    const uint64_t space = gated_workspace(a);
+    if (!on_grid(workspace, 0, 1, 16) || (space > 0 && (!workspace || workspace_bytes < space))) return BIGEMM_ERR_INVALID_ARG;
+    DeviceState *ds = device_state();
+    if (!ds) return BIGEMM_ERR_CUDA;
+    const cudaStream_t s = (cudaStream_t)stream;
+    a.vec_out = on_grid(a.out, a.ldo, 2, 16) && a.ldo * 2 < kFar;
+    a.vec_gate = on_grid(a.gate, a.ldgate, 2, 16) && a.ldgate * 2 < kFar;
+    a.vec_up = on_grid(a.up, a.ldup, 2, 16) && a.ldup * 2 < kFar;
+    a.vec_bias = on_grid(a.bias, 0, 1, 16), a.vec_bias_up = on_grid(a.bias_up, 0, 1, 16);
+    a.k_blocks = a.seg_blocks = (int)up(a.K * 2ll, kRow);
+    a.timeout_ns = wait_timeout_ns();
+    a.err = ds->err;
+    PackList k(static_cast<uint8_t *>(workspace));
+    k.add(a.w, a.ldw, a.N, a.K, 2);
+    k.add(a.w_up, a.ldw_up, a.N, a.K, 2);
+    k.add(a.x, a.ldx, a.M, a.K, 2);
+    if (k.run(s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    const Choice pick = choose<true>(a, ds->sm_count);
+    if (pick.many) {
+        const long long mt = up(a.M, kManyTokens), nt = up(a.N, 128);
+        if (mt * nt > 0x7fffffff) return BIGEMM_ERR_UNSUPPORTED;
+        a.m_tiles = (int)mt, a.n_tiles = (int)nt;
+        GatedMaps maps = {};
+        if (!operand_map(&maps.x, a.x, a.in_dt, a.M, a.K, a.ldx, 128) ||
+            !operand_map(&maps.w[0], a.w, a.in_dt, a.N, a.K, a.ldw, 128) ||
+            !operand_map(&maps.w[1], a.w_up, a.in_dt, a.N, a.K, a.ldw_up, 128) ||
+            !put_map(&maps.out, a.vec_out, a.out, a.out_dt, a.M, a.N, a.ldo) ||
+            !put_map(&maps.kept[0], a.vec_gate, a.gate, a.out_dt, a.M, a.N, a.ldgate) ||
+            !put_map(&maps.kept[1], a.vec_up, a.up, a.out_dt, a.M, a.N, a.ldup))
+            return BIGEMM_ERR_CUDA;
+        return launch_gated_many(a, maps, ds->sm_count, s) == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
+    }
+    a.split = pick.few.split;
+    CUtensorMap mg = {}, mu = {}, mxm = {};
+    if (!operand_map(&mg, a.w, a.in_dt, a.N, a.K, a.ldw, 64) || !operand_map(&mu, a.w_up, a.in_dt, a.N, a.K, a.ldw_up, 64) ||
+        !operand_map(&mxm, a.x, a.in_dt, a.M, a.K, a.ldx, pick.few.bn))
+        return BIGEMM_ERR_CUDA;
+    return launch_gated_few(a, pick.few, mg, mu, mxm, s) == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -282,6 +313,30 @@ bigemm_status matmul_mx_run(int M, int N, int K, const void *x, int64_t ldx, con
     a.xs = static_cast<const uint8_t *>(x_scale), a.ws = static_cast<const uint8_t *>(w_scale);
     a.bias = bias, a.other = other, a.out = out, a.outs = static_cast<uint8_t *>(out_scale);
     return product(a, workspace, workspace_bytes, stream);
+}
+
+uint64_t matmul_gated_workspace_bytes(int M, int N, int K, const void *x, int64_t ldx, const void *w_gate, int64_t ldw_gate,
+                                      const void *w_up, int64_t ldw_up)
+{
+    if (M < 1 || N < 1 || K < 1) return 0;
+    GatedArgs a = {};
+    a.M = M, a.N = N, a.K = K, a.x = x, a.w = w_gate, a.w_up = w_up, a.ldx = ldx, a.ldw = ldw_gate, a.ldw_up = ldw_up;
+    return gated_workspace(a);
+}
+
+bigemm_status matmul_gated_run(int M, int N, int K, bigemm_dtype dtype, const void *x, int64_t ldx, const void *w_gate,
+                               int64_t ldw_gate, const void *w_up, int64_t ldw_up, const float *bias_gate,
+                               const float *bias_up, int act, void *out, int64_t ldo, void *gate, int64_t ldgate, void *up,
+                               int64_t ldup, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    if (dtype < BIGEMM_F32 || dtype > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
+    if (dtype == BIGEMM_F32) return BIGEMM_ERR_UNSUPPORTED;
+    GatedArgs a = {};
+    a.M = M, a.N = N, a.K = K, a.in_dt = a.out_dt = dtype, a.act = act;
+    a.x = x, a.w = w_gate, a.w_up = w_up, a.ldx = ldx, a.ldw = ldw_gate, a.ldw_up = ldw_up;
+    a.bias = bias_gate, a.bias_up = bias_up, a.out = out, a.ldo = ldo;
+    a.gate = gate, a.ldgate = ldgate, a.up = up, a.ldup = ldup;
+    return gated(a, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

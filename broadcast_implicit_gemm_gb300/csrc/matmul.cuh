@@ -66,11 +66,10 @@ __device__ __forceinline__ float mm_sigmoid2(float z, float t)   // z / (1 + 2^-
 // negative z are as exact as the others.  What is left there is the exponent's
 // rounding, z^2 2^-24: 8e-7 at z = -3, 2e-6 at -6.  (0.5 z (1 + erf) takes erff, twice
 // the instructions, and loses all digits towards z = -5.5.)
-__device__ __forceinline__ float mm_gelu(float z)
+__device__ __forceinline__ float mm_normal_below(float z, float e)   // Phi(z), e = exp(-z^2 / 2)
 {
-    float t, e;
+    float t;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.305f, 1.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * (-0.5f * 1.4426950408889634f)));
     float q = fmaf(t, 0.0366991852980769f, -0.15298828749580104f);    // Phi(-|z|)
     q = fmaf(t, q, 0.1857168536271935f);
     q = fmaf(t, q, -0.0379767771644137f);
@@ -79,7 +78,14 @@ __device__ __forceinline__ float mm_gelu(float z)
     q = fmaf(t, q, 0.12246681530010683f);
     q = fmaf(t, q, 0.12163973276490539f);
     q *= t * e;
-    return z * (z < 0.f ? q : 1.f - q);
+    return z < 0.f ? q : 1.f - q;
+}
+
+__device__ __forceinline__ float mm_gelu(float z)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * (-0.5f * 1.4426950408889634f)));
+    return z * mm_normal_below(z, e);
 }
 
 template <int ACT>
@@ -217,35 +223,41 @@ __device__ __forceinline__ void mm_epilogue8(const MatmulArgs &a, int n, const f
     }
 }
 
+// 8 channels from n on of a row of N, at element `at` of a 32- or 16-bit matrix; vec:
+// its rows start on 16-byte boundaries.
 template <typename T>
-__device__ __forceinline__ void mm_store_each(const MatmulArgs &a, long long at, int n, const float (&v)[8])
+__device__ __forceinline__ void mm_store_each(void *out, long long at, int n, int N, const float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (n + j < a.N) static_cast<T *>(a.out)[at + j] = T(v[j]);
+        if (n + j < N) static_cast<T *>(out)[at + j] = T(v[j]);
+}
+
+__device__ __forceinline__ void mm_put8(void *out, long long at, int dt, bool vec, int n, int N, const float (&v)[8])
+{
+    if (vec && n + 8 <= N) {
+        if (dt == BIGEMM_F32) {
+            float *p = static_cast<float *>(out) + at;
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
+                make_uint4(mm_pack2(v[0], v[1], dt), mm_pack2(v[2], v[3], dt), mm_pack2(v[4], v[5], dt),
+                           mm_pack2(v[6], v[7], dt));
+        }
+    } else if (dt == BIGEMM_F32) {
+        mm_store_each<float>(out, at, n, N, v);
+    } else if (dt == BIGEMM_F16) {
+        mm_store_each<__half>(out, at, n, N, v);
+    } else {
+        mm_store_each<__nv_bfloat16>(out, at, n, N, v);
+    }
 }
 
 // 8 channels of a 32- or 16-bit output.
 __device__ __forceinline__ void mm_store8(const MatmulArgs &a, int m, int n, const float (&v)[8])
 {
-    const long long at = (long long)m * a.ldo + n;
-    if (a.vec_out && n + 8 <= a.N) {
-        if (a.out_dt == BIGEMM_F32) {
-            float *p = static_cast<float *>(a.out) + at;
-            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
-                make_uint4(mm_pack2(v[0], v[1], a.out_dt), mm_pack2(v[2], v[3], a.out_dt),
-                           mm_pack2(v[4], v[5], a.out_dt), mm_pack2(v[6], v[7], a.out_dt));
-        }
-    } else if (a.out_dt == BIGEMM_F32) {
-        mm_store_each<float>(a, at, n, v);
-    } else if (a.out_dt == BIGEMM_F16) {
-        mm_store_each<__half>(a, at, n, v);
-    } else {
-        mm_store_each<__nv_bfloat16>(a, at, n, v);
-    }
+    mm_put8(a.out, (long long)m * a.ldo + n, a.out_dt, a.vec_out, n, a.N, v);
 }
 
 // 8 channels of an e4m3 output, 1 / scale given.

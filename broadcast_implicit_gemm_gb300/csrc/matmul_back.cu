@@ -1,0 +1,172 @@
+// matmul_back.cu -- the products of the gradients (matmul_back.cuh), dx and dw in one
+// launch.
+//
+// Neither reads a transposed copy: d [tokens, channels], w [channels, in] and x
+// [tokens, in] are loaded as they lie, in boxes of 64 x 64, and what the summed axis is
+// not contiguous in is an MN-major operand of the MMA.  dx sums over channels (d
+// K-major, w MN-major; of both products one after the other, in one accumulator), dw
+// over tokens (d^T and x MN-major).
+//
+// A dx unit is long (4096 tokens, 2 x 16384 channels: 512 blocks) and a dw unit short
+// (64): the pairs share them as back_walk.h says (4096 x 4096 x 16384 gated: 3449
+// blocks' time per pair, 3776 in two launches).  Few tokens leave too few dx units:
+// each is cut along the summed axis then, the shares go to a workspace in fp32, and
+// launch_back_join adds them in their order.
+#include "matmul_back.cuh"
+
+#include "matmul_pair.cuh"
+
+namespace bigemm {
+
+namespace {
+
+struct BackJob {
+    using Args = BackArgs;
+    using Maps = BackMaps;
+    struct Unit {
+        int what;                    // 0: dx, 1 and 2: dw of a product
+        int m0, n0;                  // rows and columns of the result
+        int k0, k1, part;
+    };
+
+    static __device__ __forceinline__ bool unit(const Args &p, int turn, int pair, int pairs, Unit &u)
+    {
+        const int i = back_unit(p.walk, turn, pair, pairs);
+        if (i < 0) return false;
+        if (i < p.walk.dx) {
+            const int tiles = p.dx_m * p.dx_n, blocks = p.count * p.n_blocks;
+            u.part = i / tiles;
+            const Tile t = tile_in(p.dx_m, p.dx_n, i - u.part * tiles);
+            u.what = 0, u.m0 = t.m * 256, u.n0 = t.n * 256;
+            u.k0 = (int)((long long)blocks * u.part / p.split), u.k1 = (int)((long long)blocks * (u.part + 1) / p.split);
+            return true;
+        }
+        const Tile t = tile_in(p.count * p.dw_m, p.dw_n, i - p.walk.dx);
+        const int which = t.m >= p.dw_m ? 1 : 0;
+        u.what = 1 + which, u.m0 = (t.m - which * p.dw_m) * 256, u.n0 = t.n * 256;
+        u.k0 = 0, u.k1 = p.m_blocks, u.part = 0;
+        return true;
+    }
+
+    // a box's coordinates: column, row
+    static __device__ __forceinline__ void load(const Maps &maps, const Args &p, const Unit &u, int kb, int rank, uint8_t *sa,
+                                                uint8_t *sb, uint32_t bar)
+    {
+        const int m = u.m0 + rank * 128, n = u.n0 + rank * 128;
+        if (u.what == 0) {
+            const int which = kb >= p.n_blocks ? 1 : 0, k = (kb - which * p.n_blocks) * 64;
+            tma_load_2d_pair(sa, &maps.d[which], bar, k, m);
+            tma_load_2d_pair(sa + PairCfg::box, &maps.d[which], bar, k, m + 64);
+            tma_load_2d_pair(sb, &maps.w[which], bar, n, k);
+            tma_load_2d_pair(sb + PairCfg::box, &maps.w[which], bar, n + 64, k);
+        } else {
+            const CUtensorMap *d = &maps.d[u.what - 1];
+            tma_load_2d_pair(sa, d, bar, m, kb * 64);
+            tma_load_2d_pair(sa + PairCfg::box, d, bar, m + 64, kb * 64);
+            tma_load_2d_pair(sb, &maps.x, bar, n, kb * 64);
+            tma_load_2d_pair(sb + PairCfg::box, &maps.x, bar, n + 64, kb * 64);
+        }
+    }
+
+    static __device__ __forceinline__ void mma(const Args &p, const Unit &u, uint32_t d, uint32_t a, uint32_t b, uint32_t accum)
+    {
+        const uint32_t fmt = p.dt == BIGEMM_BF16 ? 1u : 0u, hi = desc_hi(1024u, 2u), b_lo = operand_lo(b, true);
+        if (u.what == 0)
+            umma4_pair<2, 128>(d, operand_lo(a, false), b_lo, hi, make_idesc(fmt, 0u, 1u, 256, 256), accum);
+        else
+            umma4_pair<128, 128>(d, operand_lo(a, true), b_lo, hi, make_idesc(fmt, 1u, 1u, 256, 256), accum);
+    }
+
+    static __device__ __forceinline__ void drain(const Maps &maps, const Args &p, const Unit &u, int rank, int q, int h,
+                                                 uint32_t tmem, uint8_t *stage, int &piece, int lane)
+    {
+        const long long m_warp = u.m0 + rank * 128 + q * 32, rows = u.what == 0 ? p.M : p.N;
+        if (m_warp >= rows) return;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            const int n = u.n0 + h * 64 + c * 32;
+            if (n >= p.K) return;
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tmem + (uint32_t)(h * 64 + c * 32), r);
+            tmem_wait_ld32(r);
+            if (u.what == 0 && p.split > 1) {
+                // 16 columns of 32 bits at a time: a box of 64 bytes by 32 rows
+#pragma unroll
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = r[i + j];
+                    const uint8_t *buf = stage_words<PairCfg::per_warp, 16>(stage, piece, lane, w);
+                    if (lane == 0 && n + i < p.K) {
+                        tma_store_3d(&maps.part, buf, n + i, (int)m_warp, u.part);
+                        bulk_commit();
+                    }
+                }
+                continue;
+            }
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            if (u.what == 0)
+                put16(&maps.dx, p.dx_rows, p.dx, p.lddx, p.dt, rows, p.K, stage, piece, lane, m_warp, n, v);
+            else
+                put16(&maps.dw[u.what - 1], p.dw_rows[u.what - 1], p.dw[u.what - 1], p.lddw[u.what - 1], p.dt, rows, p.K,
+                      stage, piece, lane, m_warp, n, v);
+        }
+    }
+};
+
+// A thread adds four columns of the shares; the shares lie in L2, where the products
+// left them.
+template <typename T>
+__global__ void __launch_bounds__(256) back_join_kernel(const float *part, int split, int M, int K, long long pitch, T *dx,
+                                                        long long lddx, bool vec, int runs)
+{
+    griddep_enter();
+    const long long item = (long long)blockIdx.x * 256 + threadIdx.x, m = item / runs;
+    const int k = (int)(item - m * runs) * 4;
+    if (m >= M) return;
+    const float4 *from = reinterpret_cast<const float4 *>(part + m * pitch + k);
+    const long long step = (long long)M * pitch / 4;
+    float4 v = from[0];
+#pragma unroll 4
+    for (int s = 1; s < split; ++s) {
+        const float4 w = from[s * step];
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    T *to = dx + m * lddx + k;
+    alignas(8) const T o[4] = {T(v.x), T(v.y), T(v.z), T(v.w)};
+    if (vec && k + 4 <= K) {
+        *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i < K) to[i] = o[i];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_back(const BackArgs &a, const BackMaps &maps, int pairs, cudaStream_t stream)
+{
+    ProfScope prof("matmul_back", stream);
+    return launch_pairs<BackJob>(a, maps, pairs, stream);
+}
+
+cudaError_t launch_back_join(const float *part, int split, int M, int K, long long pitch, void *dx, long long lddx, int dt,
+                             cudaStream_t stream)
+{
+    ProfScope prof("matmul_back_join", stream);
+    const int runs = (int)((K + 3ll) / 4);
+    const long long blocks = ((long long)M * runs + 255) / 256;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const bool vec = reinterpret_cast<uintptr_t>(dx) % 8 == 0 && lddx % 4 == 0;
+    const dim3 grid((unsigned)blocks);
+    return dt == BIGEMM_F16
+               ? launch_pdl(back_join_kernel<__half>, grid, dim3(256), 0, stream, part, split, M, K, pitch,
+                            static_cast<__half *>(dx), lddx, vec, runs)
+               : launch_pdl(back_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, part, split, M, K, pitch,
+                            static_cast<__nv_bfloat16 *>(dx), lddx, vec, runs);
+}
+
+}  // namespace bigemm

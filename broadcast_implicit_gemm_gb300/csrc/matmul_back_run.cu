@@ -1,0 +1,232 @@
+// matmul_back_run.cu -- entry points of the products' gradients (matmul_back.cuh): checks of
+// arguments, tensor maps, the cut of dx and the place of everything in the workspace.
+#include <algorithm>
+
+#include "column_sums.cuh"
+#include "matmul_back.cuh"
+#include "matmul_host.cuh"
+
+using namespace bigemm;
+
+namespace {
+
+constexpr int kPairs = 76;           // of the machine: what cuts and workspaces are made for
+
+// A product's gradients, or (count 2) a gated layer's.
+struct Problem {
+    int M, N, K, dt, count, act;
+    const void *dout, *x, *w[2], *gate, *up;
+    long long ldd, ldx, ldw[2], ldg, ldu;
+    void *dx, *dw[2];
+    long long lddx, lddw[2];
+    float *dbias[2];
+};
+
+// How many shares dx's units are cut into.  In blocks' time (0.33 us): a unit takes its
+// blocks and 6 more, all units together what they take over the pairs, and each share
+// past the first is written and read again in fp32 (at about 5 TB/s from L2).
+// Fewer shares where it makes no difference.
+int dx_split(const Problem &p)
+{
+    const long long blocks = p.count * up(p.N, 64), tiles = up(p.M, 256) * up(p.K, 256);
+    const long long dw = p.count * up(p.N, 256) * up(p.K, 256) * (up(p.M, 64) + 6);
+    long long least = -1;
+    int best = 1;
+    for (int s = 1; s <= 32 && s * 4 <= blocks; ++s) {
+        const long long unit = up(blocks, s) + 6, waves = up(tiles * s, kPairs);
+        const long long walk = std::max(up(tiles * s * unit + dw, kPairs), waves * unit);
+        const long long join = s > 1 ? 8 + (2ll * s * p.M * p.K * 4) / 1650000 : 0;
+        if (least < 0 || walk + join < least) least = walk + join, best = s;
+    }
+    return best;
+}
+
+// Runs of rows of the sums over tokens: eight blocks per SM, of 32 rows at least.
+int gate_runs(const Problem &p)
+{
+    const long long most = std::max<long long>(1, 8 * 2 * kPairs / up(p.N, kGateColumns));
+    return (int)std::min<long long>(most, up(p.M, 32));
+}
+
+struct Space {
+    uint64_t pitch, d, packed, part_pitch, part, sums, total;   // pitches in elements, places in bytes
+    int split, runs;
+};
+
+Space space_of(const Problem &p)
+{
+    Space s = {};
+    s.split = dx_split(p), s.runs = gate_runs(p);
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    if (p.count == 2) {
+        s.pitch = (uint64_t)up(p.N, 8) * 8;
+        s.d = take(2 * s.pitch * (uint64_t)p.M * 2);
+    }
+    uint64_t packed = 0;
+    if (p.count == 1 && !addressable(p.dout, p.ldd, 2)) packed += packed_bytes(p.M, p.N, 2);
+    if (!addressable(p.x, p.ldx, 2)) packed += packed_bytes(p.M, p.K, 2);
+    for (int i = 0; i < p.count; ++i)
+        if (!addressable(p.w[i], p.ldw[i], 2)) packed += packed_bytes(p.N, p.K, 2);
+    s.packed = take(packed);
+    s.part_pitch = (uint64_t)up(p.K, 4) * 4;
+    s.part = take(s.split > 1 ? (uint64_t)s.split * p.M * s.part_pitch * 4 : 0);
+    // (whether there are biases is not known to who asks for the size)
+    s.sums = take((uint64_t)p.count * s.runs * p.N * 4);
+    s.total = at;
+    return s;
+}
+
+bool sizes_fit(const Problem &p) { return p.M <= kMaxSize && p.N <= kMaxSize && p.K <= kMaxSize; }
+
+bool reach(const void *p, long long ld, long long cols) { return p && ld >= cols && on_grid(p, 0, 1, 2); }
+
+// dx's shares as boxes of 32 rows by 64 bytes.
+bool part_map(CUtensorMap *map, const void *p, const Problem &a, const Space &s)
+{
+    const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.M, (uint64_t)s.split};
+    const uint64_t strides[2] = {s.part_pitch * 4, s.part_pitch * 4 * (uint64_t)a.M};
+    const uint32_t box[3] = {16, 32, 1}, ones[3] = {1, 1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+bigemm_status zero_gradients(const Problem &p, cudaStream_t s)
+{
+    for (int i = 0; i < p.count; ++i) {
+        if (cudaMemset2DAsync(p.dw[i], (size_t)p.lddw[i] * 2, 0, (size_t)p.K * 2, (size_t)p.N, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+        if (p.dbias[i] && cudaMemsetAsync(p.dbias[i], 0, (size_t)p.N * 4, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    }
+    return BIGEMM_OK;
+}
+
+bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *stream)
+{
+    if (p.M < 0 || p.N < 1 || p.K < 1 || p.dt < BIGEMM_F32 || p.dt > BIGEMM_BF16) return BIGEMM_ERR_INVALID_ARG;
+    if (p.act < BIGEMM_ACT_NONE || p.act > BIGEMM_ACT_SILU) return BIGEMM_ERR_INVALID_ARG;
+    if (p.dt == BIGEMM_F32 || !sizes_fit(p)) return BIGEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < p.count; ++i)
+        if (!reach(p.dw[i], p.lddw[i], p.K) || !on_grid(p.dbias[i], 0, 1, 4)) return BIGEMM_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (p.M == 0) return device_state() ? zero_gradients(p, s) : BIGEMM_ERR_CUDA;
+    if (!reach(p.dout, p.ldd, p.N) || !reach(p.x, p.ldx, p.K) || !reach(p.dx, p.lddx, p.K)) return BIGEMM_ERR_INVALID_ARG;
+    for (int i = 0; i < p.count; ++i)
+        if (!reach(p.w[i], p.ldw[i], p.K)) return BIGEMM_ERR_INVALID_ARG;
+    if (p.count == 2 && (!reach(p.gate, p.ldg, p.N) || !reach(p.up, p.ldu, p.N))) return BIGEMM_ERR_INVALID_ARG;
+    const Space at = space_of(p);
+    if (!on_grid(workspace, 0, 1, 16) || !workspace || bytes < at.total) return BIGEMM_ERR_INVALID_ARG;
+    DeviceState *ds = device_state();
+    if (!ds) return BIGEMM_ERR_CUDA;
+    uint8_t *space = static_cast<uint8_t *>(workspace);
+    const int pairs_of_all = ds->sm_count / 2;
+
+    // the products' operands
+    const void *d[2] = {p.dout, nullptr};
+    long long ldd[2] = {p.ldd, 0};
+    GateBackArgs g = {};
+    g.M = p.M, g.N = p.N, g.runs = at.runs, g.act = -1;
+    g.dout = p.dout, g.gate = p.gate, g.up = p.up, g.ldd = p.ldd, g.ldg = p.ldg, g.ldu = p.ldu;
+    float *sums = reinterpret_cast<float *>(space + at.sums);
+    for (int i = 0; i < p.count; ++i) g.sums[i] = p.dbias[i] ? sums + (long long)i * at.runs * p.N : nullptr;
+    const bool biases = p.dbias[0] || p.dbias[1];
+    if (p.count == 2) {
+        g.act = p.act, g.pitch = (long long)at.pitch;
+        g.dg = space + at.d, g.du = space + at.d + at.pitch * (uint64_t)p.M * 2;
+        d[0] = g.dg, d[1] = g.du, ldd[0] = ldd[1] = g.pitch;
+    }
+    if (p.count == 2 || biases) {
+        const bool vec = on_grid(p.dout, p.ldd, 2, 16) && (p.count == 1 || (on_grid(p.gate, p.ldg, 2, 16) && on_grid(p.up, p.ldu, 2, 16)));
+        if (launch_gate_back(g, p.dt, vec, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    }
+    if (biases) {
+        ColumnSums c = {};
+        c.parts = at.runs, c.cols = p.N;
+        for (int i = 0; i < p.count; ++i)
+            if (p.dbias[i]) c.from[c.count] = g.sums[i], c.out[c.count++] = p.dbias[i];
+        if (launch_column_sums(c, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    }
+    PackList k(space + at.packed);
+    if (p.count == 1) k.add(d[0], ldd[0], p.M, p.N, 2);
+    k.add(p.x, p.ldx, p.M, p.K, 2);
+    for (int i = 0; i < p.count; ++i) k.add(p.w[i], p.ldw[i], p.N, p.K, 2);
+    if (k.run(s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+
+    BackArgs a = {};
+    BackMaps maps = {};
+    a.M = p.M, a.N = p.N, a.K = p.K, a.dt = p.dt, a.count = p.count, a.split = at.split;
+    a.n_blocks = (int)up(p.N, 64), a.m_blocks = (int)up(p.M, 64);
+    a.dx_m = (int)up(p.M, 256), a.dx_n = (int)up(p.K, 256), a.dw_m = (int)up(p.N, 256), a.dw_n = a.dx_n;
+    const long long dx_units = (long long)a.dx_m * a.dx_n * a.split, dw_units = (long long)p.count * a.dw_m * a.dw_n;
+    if (dx_units + dw_units > 0x3fffffff) return BIGEMM_ERR_UNSUPPORTED;
+    const int pairs = (int)std::min<long long>(pairs_of_all, dx_units + dw_units);
+    a.walk = make_back_walk((int)dx_units, (int)dw_units, pairs, up((long long)p.count * a.n_blocks, a.split) + 6, a.m_blocks + 6);
+    a.dx = p.dx, a.lddx = p.lddx, a.dx_rows = addressable(p.dx, p.lddx, 2);
+    a.timeout_ns = wait_timeout_ns();
+    a.err = ds->err;
+    bool ok = operand_map(&maps.x, p.x, p.dt, p.M, p.K, p.ldx, 64);
+    for (int i = 0; i < p.count; ++i) {
+        a.dw[i] = p.dw[i], a.lddw[i] = p.lddw[i], a.dw_rows[i] = addressable(p.dw[i], p.lddw[i], 2);
+        ok = ok && operand_map(&maps.d[i], d[i], p.dt, p.M, p.N, ldd[i], 64) &&
+             operand_map(&maps.w[i], p.w[i], p.dt, p.N, p.K, p.ldw[i], 64) &&
+             (!a.dw_rows[i] || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+    }
+    if (a.split > 1) ok = ok && part_map(&maps.part, space + at.part, p, at);
+    else if (a.dx_rows) ok = ok && box_map(&maps.dx, p.dx, p.dt, p.M, p.K, p.lddx, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok || launch_matmul_back(a, maps, pairs, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    if (a.split > 1 && launch_back_join(reinterpret_cast<const float *>(space + at.part), a.split, p.M, p.K, (long long)at.part_pitch,
+                                        p.dx, p.lddx, p.dt, s) != cudaSuccess)
+        return BIGEMM_ERR_CUDA;
+    return BIGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t matmul_backward_workspace_bytes(int M, int N, int K, const void *dout, int64_t lddout, const void *x, int64_t ldx,
+                                         const void *w, int64_t ldw)
+{
+    Problem p = {};
+    p.M = M, p.N = N, p.K = K, p.count = 1, p.dout = dout, p.ldd = lddout, p.x = x, p.ldx = ldx, p.w[0] = w, p.ldw[0] = ldw;
+    return M < 1 || N < 1 || K < 1 || !sizes_fit(p) ? 0 : space_of(p).total;
+}
+
+bigemm_status matmul_backward_run(int M, int N, int K, bigemm_dtype dtype, const void *dout, int64_t lddout, const void *x,
+                                  int64_t ldx, const void *w, int64_t ldw, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                                  float *dbias, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    Problem p = {};
+    p.M = M, p.N = N, p.K = K, p.dt = dtype, p.count = 1, p.dout = dout, p.ldd = lddout, p.x = x, p.ldx = ldx;
+    p.w[0] = w, p.ldw[0] = ldw, p.dx = dx, p.lddx = lddx, p.dw[0] = dw, p.lddw[0] = lddw, p.dbias[0] = dbias;
+    return gradients(p, workspace, workspace_bytes, stream);
+}
+
+uint64_t matmul_gated_backward_workspace_bytes(int M, int N, int K, const void *x, int64_t ldx, const void *w_gate,
+                                               int64_t ldw_gate, const void *w_up, int64_t ldw_up)
+{
+    Problem p = {};
+    p.M = M, p.N = N, p.K = K, p.count = 2, p.x = x, p.ldx = ldx;
+    p.w[0] = w_gate, p.ldw[0] = ldw_gate, p.w[1] = w_up, p.ldw[1] = ldw_up;
+    return M < 1 || N < 1 || K < 1 || !sizes_fit(p) ? 0 : space_of(p).total;
+}
+
+bigemm_status matmul_gated_backward_run(int M, int N, int K, bigemm_dtype dtype, const void *dout, int64_t lddout,
+                                        const void *x, int64_t ldx, const void *w_gate, int64_t ldw_gate, const void *w_up,
+                                        int64_t ldw_up, const void *gate, int64_t ldgate, const void *up, int64_t ldup,
+                                        int act, void *dx, int64_t lddx, void *dw_gate, int64_t lddw_gate, void *dw_up,
+                                        int64_t lddw_up, float *dbias_gate, float *dbias_up, void *workspace,
+                                        uint64_t workspace_bytes, void *stream)
+{
+    Problem p = {};
+    p.M = M, p.N = N, p.K = K, p.dt = dtype, p.count = 2, p.act = act, p.dout = dout, p.ldd = lddout, p.x = x, p.ldx = ldx;
+    p.w[0] = w_gate, p.ldw[0] = ldw_gate, p.w[1] = w_up, p.ldw[1] = ldw_up;
+    p.gate = gate, p.ldg = ldgate, p.up = up, p.ldu = ldup, p.dx = dx, p.lddx = lddx;
+    p.dw[0] = dw_gate, p.lddw[0] = lddw_gate, p.dw[1] = dw_up, p.lddw[1] = lddw_up;
+    p.dbias[0] = dbias_gate, p.dbias[1] = dbias_up;
+    return gradients(p, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

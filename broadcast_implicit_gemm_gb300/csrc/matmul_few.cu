@@ -21,7 +21,14 @@
 // accumulator short, so the error of one long sum grows with K (measured
 // 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
+//
+// GATED: a gated layer's two products (matmul_gated.cuh).  The 128 rows are 64 of the
+// gate's weights and the same 64 of the up product's, so that both sums of a channel
+// and token meet in one CTA: nothing else changes before the epilogue.
 #include "matmul.cuh"
+#include "matmul_gated.cuh"
+
+#include <type_traits>
 
 namespace bigemm {
 
@@ -61,12 +68,36 @@ constexpr uint32_t few_cols()
     return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
-template <int BN, bool MX, bool FULL>
-__global__ void __launch_bounds__(kFewThreads)
-    matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                      const MatmulArgs p)
+template <bool GATED>
+struct FewMaps {
+    CUtensorMap w, x;
+};
+template <>
+struct FewMaps<true> {
+    CUtensorMap w, x, up;
+};
+template <bool GATED>
+using FewArgs = std::conditional_t<GATED, GatedArgs, MatmulArgs>;
+
+// act(g) u of 8 channels from n on of token m, g and u where they are kept; channels past N are not written.
+__device__ __forceinline__ void gated_out8(const GatedArgs &p, int m, int n, float (&g)[8], const float (&u)[8])
 {
+    if (p.gate) mm_put8(p.gate, m * p.ldgate + n, p.out_dt, p.vec_gate, n, p.N, g);
+    if (p.up) mm_put8(p.up, m * p.ldup + n, p.out_dt, p.vec_up, n, p.N, u);
+    mm_act_all(p.act, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= u[j];
+    mm_store8(p, m, n, g);
+}
+
+template <int BN, bool MX, bool FULL, bool GATED = false>
+__global__ void __launch_bounds__(kFewThreads)
+    matmul_few_kernel(const __grid_constant__ FewMaps<GATED> maps, const FewArgs<GATED> p)
+{
+    static_assert(!GATED || (!MX && !FULL), "16-bit operands and outputs");
     using C = FewCfg<BN>;
+    constexpr int kChannels = GATED ? 64 : 128;      // of the output, per CTA
+    constexpr int kPieces = kChannels / 8;           // of 8 channels, per token
     const int S = p.stages;
     constexpr int ACC = FULL ? 2 : 1;
     constexpr uint32_t kCols = few_cols<BN, MX, FULL>();
@@ -84,7 +115,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = p.split;                       // CTAs of the cluster
     const int rank = split > 1 ? (int)cluster_ctarank() : 0;
-    const int ct = (int)blockIdx.x / split, n0 = ct * 128;
+    const int ct = (int)blockIdx.x / split, n0 = ct * kChannels;
     const int m0 = (int)blockIdx.y * BN;
     const int kb0 = (int)((long long)rank * p.k_blocks / split), kb1 = (int)((long long)(rank + 1) * p.k_blocks / split);
 
@@ -97,8 +128,9 @@ __global__ void __launch_bounds__(kFewThreads)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&map_w);
-        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&maps.w);
+        tma_prefetch_desc(&maps.x);
+        if constexpr (GATED) tma_prefetch_desc(&maps.up);
     }
     if (warp == 1) {
         __syncwarp();
@@ -132,8 +164,9 @@ __global__ void __launch_bounds__(kFewThreads)
                 if (!good) break;
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)(kFewA + BN * kRow + (MX ? 2 * kMxBlockBytes : 0)));
                 issued[stage] = true, last_parity[stage] = phase;
-                tma_load_2d(sa + stage * kFewA, &map_w, &full[stage], kb * per, n0);
-                tma_load_2d(sb + stage * BN * kRow, &map_x, &full[stage], kb * per, m0);
+                tma_load_2d(sa + stage * kFewA, &maps.w, &full[stage], kb * per, n0);
+                if constexpr (GATED) tma_load_2d(sa + stage * kFewA + kFewA / 2, &maps.up, &full[stage], kb * per, n0);
+                tma_load_2d(sb + stage * BN * kRow, &maps.x, &full[stage], kb * per, m0);
                 if (MX) {
                     uint8_t *s = ss + stage * 2 * kMxBlockBytes;
                     bulk_load(s, p.ws + ((long long)(n0 >> 7) * p.k_blocks + kb) * kMxBlockBytes, kMxBlockBytes,
@@ -242,14 +275,18 @@ __global__ void __launch_bounds__(kFewThreads)
     const int tokens = min(BN, p.M - m0);
     const int per_rank = ((tokens + split - 1) / split + C::group - 1) / C::group * C::group;
     const int t0 = rank * per_rank, mine = max(0, min(per_rank, tokens - t0));
-    // a thread finishes 8 channels, always the same ones, of every 16th token of the rank's; its bias
+    // a thread finishes 8 channels, always the same ones, of every 16th (GATED: 32nd) token of the rank's; its bias
     // and its first other are asked for now
-    const int c = ((int)threadIdx.x & 15) * 8;
-    float bias[8];
+    const int c = ((int)threadIdx.x & (kPieces - 1)) * 8;
+    float bias[8], bias_up[GATED ? 8 : 1];
 #pragma unroll
     for (int j = 0; j < 8; ++j) bias[j] = p.bias && n0 + c + j < p.N ? p.bias[n0 + c + j] : 0.f;
+    if constexpr (GATED) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bias_up[j] = p.bias_up && n0 + c + j < p.N ? p.bias_up[n0 + c + j] : 0.f;
+    }
     Raw8 other;
-    if ((int)threadIdx.x < mine * 16) mm_other8(p, m0 + t0 + ((int)threadIdx.x >> 4), n0 + c, other);
+    if (!GATED && (int)threadIdx.x < mine * kPieces) mm_other8(p, m0 + t0 + (int)threadIdx.x / kPieces, n0 + c, other);
     if (split > 1) {
         // the sums' memory is free: beside the stages since each peer began, over them since its
         // drain warps saw the last MMA done
@@ -301,27 +338,39 @@ __global__ void __launch_bounds__(kFewThreads)
     }
 
     // ---------------------------------------------------------- sum over the ranks and epilogue
-    // pieces of 8 channels, 16 to a token
-    for (int i0 = 0; i0 < mine * 16; i0 += kFewThreads) {
+    // pieces of 8 channels, 16 (8) to a token
+    for (int i0 = 0; i0 < mine * kPieces; i0 += kFewThreads) {
         const int i = i0 + (int)threadIdx.x;
-        const bool live = i < mine * 16;
-        const int t = t0 + (live ? i >> 4 : 0);
+        const bool live = i < mine * kPieces;
+        const int t = t0 + (live ? i / kPieces : 0);
         const Raw8 now = other;
-        if (i + kFewThreads < mine * 16) mm_other8(p, m0 + t0 + ((i + kFewThreads) >> 4), n0 + c, other);
-        float v[8];
+        if (!GATED && i + kFewThreads < mine * kPieces) mm_other8(p, m0 + t0 + (i + kFewThreads) / kPieces, n0 + c, other);
+        float v[8], up[GATED ? 8 : 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = 0.f, up[GATED ? j : 0] = 0.f;
         if (live) {
-            const float4 *from = reinterpret_cast<const float4 *>(part + (i >> 4) * 128 + c);
+            const float4 *from = reinterpret_cast<const float4 *>(part + i / kPieces * 128 + c);
 #pragma unroll 4
             for (int s = 0; s < split; ++s) {
                 const float4 u0 = from[0], u1 = from[1];
+                if constexpr (GATED) {
+                    const float4 w0 = from[16], w1 = from[17];
+                    up[0] += w0.x, up[1] += w0.y, up[2] += w0.z, up[3] += w0.w;
+                    up[4] += w1.x, up[5] += w1.y, up[6] += w1.z, up[7] += w1.w;
+                }
                 from += per_rank * 32;
                 v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
                 v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
             }
-            mm_epilogue8(p, n0 + c, bias, now, v);
+            if constexpr (GATED) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += bias[j], up[j] += bias_up[j];
+                gated_out8(p, m0 + t, n0 + c, v, up);
+            } else {
+                mm_epilogue8(p, n0 + c, bias, now, v);
+            }
         }
+        if (GATED) continue;
         if (p.out_dt == BIGEMM_MXF8) {
             float m = 0.f;
 #pragma unroll
@@ -346,12 +395,12 @@ __global__ void __launch_bounds__(kFewThreads)
     }
 }
 
-template <int BN, bool MX, bool FULL>
-cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
-                       cudaStream_t stream)
+template <int BN, bool MX, bool FULL, bool GATED = false>
+cudaError_t launch_one(FewArgs<GATED> a, int split, bool alone, const FewMaps<GATED> &maps, cudaStream_t stream)
 {
     a.stages = alone ? FewCfg<BN>::whole : FewCfg<BN>::half;
-    auto kern = matmul_few_kernel<BN, MX, FULL>;
+    auto kern = matmul_few_kernel<BN, MX, FULL, GATED>;
+    constexpr int channels = GATED ? 64 : 128;
     static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
@@ -362,7 +411,7 @@ cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &m
         if (dev < 64) attr_set |= 1ull << dev;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.N + 127ll) / 128 * split), (unsigned)((a.M + (long long)BN - 1) / BN));
+    cfg.gridDim = dim3((unsigned)((a.N + channels - 1ll) / channels * split), (unsigned)((a.M + (long long)BN - 1) / BN));
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = FewCfg<BN>::smem(a.stages);
     cfg.stream = stream;
@@ -375,21 +424,20 @@ cudaError_t launch_one(MatmulArgs a, int split, bool alone, const CUtensorMap &m
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
 template <int BN>
-cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, const CUtensorMap &mw, const CUtensorMap &mx,
-                      cudaStream_t s)
+cudaError_t launch_bn(const MatmulArgs &a, int split, bool alone, const FewMaps<false> &maps, cudaStream_t s)
 {
     if (matmul_in_pieces(a)) {
         if constexpr (BN <= 64)
-            return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, true>(a, split, alone, mw, mx, s)
-                                          : launch_one<BN, false, true>(a, split, alone, mw, mx, s);
+            return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, true>(a, split, alone, maps, s)
+                                          : launch_one<BN, false, true>(a, split, alone, maps, s);
         return cudaErrorInvalidValue;   // 128 running sums per thread would spill
     }
-    return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, false>(a, split, alone, mw, mx, s)
-                                  : launch_one<BN, false, false>(a, split, alone, mw, mx, s);
+    return a.in_dt == BIGEMM_MXF8 ? launch_one<BN, true, false>(a, split, alone, maps, s)
+                                  : launch_one<BN, false, false>(a, split, alone, maps, s);
 }
 
 }  // namespace
@@ -401,11 +449,26 @@ cudaError_t launch_matmul_few(const MatmulArgs &a, FewCut cut, const CUtensorMap
     // the scales of a 32-token tile inside a block of 128 would start at an odd column of tensor
     // memory, which the MMA does not take
     if (a.in_dt == BIGEMM_MXF8 && cut.bn < 64 && a.M > cut.bn) return cudaErrorInvalidValue;
+    const FewMaps<false> maps = {map_w, map_x};
     switch (cut.bn) {
-    case 16: return launch_bn<16>(a, cut.split, cut.alone, map_w, map_x, stream);
-    case 32: return launch_bn<32>(a, cut.split, cut.alone, map_w, map_x, stream);
-    case 64: return launch_bn<64>(a, cut.split, cut.alone, map_w, map_x, stream);
-    case 128: return launch_bn<128>(a, cut.split, cut.alone, map_w, map_x, stream);
+    case 16: return launch_bn<16>(a, cut.split, cut.alone, maps, stream);
+    case 32: return launch_bn<32>(a, cut.split, cut.alone, maps, stream);
+    case 64: return launch_bn<64>(a, cut.split, cut.alone, maps, stream);
+    case 128: return launch_bn<128>(a, cut.split, cut.alone, maps, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_gated_few(const GatedArgs &a, FewCut cut, const CUtensorMap &map_w, const CUtensorMap &map_up,
+                             const CUtensorMap &map_x, cudaStream_t stream)
+{
+    ProfScope prof("matmul_gated_few", stream);
+    const FewMaps<true> maps = {map_w, map_x, map_up};
+    switch (cut.bn) {
+    case 16: return launch_one<16, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 32: return launch_one<32, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 64: return launch_one<64, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 128: return launch_one<128, false, false, true>(a, cut.split, cut.alone, maps, stream);
     default: return cudaErrorInvalidValue;
     }
 }

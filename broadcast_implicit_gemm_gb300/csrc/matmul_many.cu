@@ -19,6 +19,7 @@
 // FULL: a 32-bit output, sums of at most 512 or 2048 elements added up in registers
 // (matmul_few.cu says why).
 #include "matmul.cuh"
+#include "matmul_drain.cuh"
 
 namespace bigemm {
 
@@ -49,19 +50,7 @@ struct ManyCfg {
     static_assert(accs * BN + (MX ? stages * (4 + BN / 32) : 0) <= 512, "tensor memory");
 };
 
-struct Tile {
-    int m, n;
-};
-
-// Eight token tiles share a sweep over the channel tiles.
-__device__ __forceinline__ Tile tile_of(const MatmulArgs &p, int t)
-{
-    constexpr int kGroup = 8;
-    const int per = kGroup * p.n_tiles;
-    const int g = t / per, r = t - g * per;
-    const int rows = min(kGroup, p.m_tiles - g * kGroup);
-    return {g * kGroup + r % rows, r / rows};
-}
+__device__ __forceinline__ Tile tile_of(const MatmulArgs &p, int t) { return tile_in(p.m_tiles, p.n_tiles, t); }
 
 // A warp's 32 tokens by 32 channels of other come as they lie in memory, 4 (or,
 // of 32 bits, 8) lanes to a token's 64 (128) bytes, and are turned round in
@@ -167,29 +156,16 @@ __device__ __forceinline__ void epilogue32(const MatmulArgs &p, uint8_t *stage, 
 }
 
 // 32 rows of WORDS 32-bit words, a lane's row in w, to global memory: through the
-// staging (two buffers of it, where two fit) by TMA.
+// staging by TMA.
 template <int PER_WARP, int WORDS>
 __device__ __forceinline__ void put_words(const MatmulArgs &p, const CUtensorMap *map, uint8_t *stage, int &piece,
                                           int lane, int m_warp, int n, const uint32_t (&w)[WORDS])
 {
-    constexpr int bytes = WORDS * 128;
-    constexpr bool two = 2 * bytes <= PER_WARP;
-    uint8_t *buf = stage + (two ? (piece & 1) * bytes : 0);
-    if (lane == 0) bulk_wait_read<two ? 1 : 0>();
-    __syncwarp();
-    // the swizzle of the output's map: rows of 128, 64 or 32 bytes
-    const int key = WORDS == 32 ? lane & 7 : WORDS == 16 ? (lane >> 1) & 3 : (lane >> 2) & 1;
-#pragma unroll
-    for (int c = 0; c < WORDS / 4; ++c)
-        *reinterpret_cast<uint4 *>(buf + lane * WORDS * 4 + ((c ^ key) << 4)) =
-            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    fence_proxy_async_smem();
-    __syncwarp();
+    const uint8_t *buf = stage_words<PER_WARP, WORDS>(stage, piece, lane, w);
     if (lane == 0 && m_warp < p.M) {
         tma_store_2d(map, buf, n, m_warp);
         bulk_commit();
     }
-    ++piece;
 }
 
 // A drain warp's output of 32 tokens by 32 channels, all inside N, a lane's
@@ -228,20 +204,6 @@ __device__ __forceinline__ uint32_t put_rows(const MatmulArgs &p, const CUtensor
     }
     put_words<PER_WARP, 16>(p, map, stage, piece, lane, m_warp, n, w);
     return 0;
-}
-
-// 16 values, a row each, to element 0 of rows ld bytes apart; `rows` of them.
-template <typename T>
-__device__ __forceinline__ void store_down(uint8_t *at, long long ld, int rows, const float (&v)[16])
-{
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        if (r < rows) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float *>(at) = v[r];
-            else *reinterpret_cast<T *>(at) = T(v[r]);
-        }
-        at += ld;
-    }
 }
 
 template <typename T>

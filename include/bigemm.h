@@ -353,6 +353,69 @@ uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, cons
                                 int64_t ldx, const void *w, int64_t ldw);
 
 /*
+ * matmul_gated_run -- the two products of a gated layer in one kernel:
+ *   g = x w_gate^T + bias_gate,  u = x w_up^T + bias_up,  out = act(g) * u
+ *   x [M,K], w_gate and w_up [N,K], out [M,N] of dtype (F16 or BF16); bias_gate,
+ *   bias_up [N] fp32, each or NULL; fp32 sums, out rounded once (g and u are not
+ *   rounded on the way to it)
+ *   gate, up [M,N] of dtype, each or NULL (not wanted): receive g and u, each rounded
+ *   once, which matmul_gated_backward_run takes
+ *   workspace: matmul_gated_workspace_bytes of device memory on a 16-byte boundary,
+ *   the call's until it is done; NULL where that is 0.
+ * Errors: as matmul_run.
+ */
+bigemm_status matmul_gated_run(int M, int N, int K, bigemm_dtype dtype, const void *x, int64_t ldx,
+                               const void *w_gate, int64_t ldw_gate, const void *w_up,
+                               int64_t ldw_up, const float *bias_gate, const float *bias_up, int act,
+                               void *out, int64_t ldo, void *gate, int64_t ldgate, void *up,
+                               int64_t ldup, void *workspace, uint64_t workspace_bytes,
+                               void *stream);
+
+/* Bytes of workspace that it needs: for a copy of each operand whose rows are off the
+ * 16-byte grid; 0 where none is. */
+uint64_t matmul_gated_workspace_bytes(int M, int N, int K, const void *x, int64_t ldx,
+                                      const void *w_gate, int64_t ldw_gate, const void *w_up,
+                                      int64_t ldw_up);
+
+/*
+ * matmul_backward_run -- gradients of out = x w^T + bias, of dout [M,N], that of out:
+ *   dx [M,K] = dout w,  dw [N,K] = dout^T x,  dbias [N] = sum over tokens of dout
+ *   all but dbias (fp32, or NULL: not wanted) of dtype (F16 or BF16); fp32 sums, each
+ *   output rounded once; the sums' order does not depend on timing.  M = 0 writes zeros
+ *   to dw and dbias.  No output may be an input.
+ *   workspace: matmul_backward_workspace_bytes of device memory on a 16-byte boundary,
+ *   the call's until it is done.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype F32; a size above 2^30), CUDA.
+ */
+bigemm_status matmul_backward_run(int M, int N, int K, bigemm_dtype dtype, const void *dout,
+                                  int64_t lddout, const void *x, int64_t ldx, const void *w,
+                                  int64_t ldw, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                                  float *dbias, void *workspace, uint64_t workspace_bytes,
+                                  void *stream);
+uint64_t matmul_backward_workspace_bytes(int M, int N, int K, const void *dout, int64_t lddout,
+                                         const void *x, int64_t ldx, const void *w, int64_t ldw);
+
+/*
+ * matmul_gated_backward_run -- gradients of matmul_gated_run, of dout [M,N], that of out,
+ * and gate and up (g and u) as that call kept them:
+ *   dg = dout u act'(g),  du = dout act(g)   in fp32, then rounded to dtype
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ *   dbias_gate, dbias_up [N] fp32, each or NULL: sums over tokens of dg and du, not rounded
+ *   (act' of relu is 0 at 0.)  Otherwise as matmul_backward_run.
+ */
+bigemm_status matmul_gated_backward_run(int M, int N, int K, bigemm_dtype dtype, const void *dout,
+                                        int64_t lddout, const void *x, int64_t ldx,
+                                        const void *w_gate, int64_t ldw_gate, const void *w_up,
+                                        int64_t ldw_up, const void *gate, int64_t ldgate,
+                                        const void *up, int64_t ldup, int act, void *dx,
+                                        int64_t lddx, void *dw_gate, int64_t lddw_gate, void *dw_up,
+                                        int64_t lddw_up, float *dbias_gate, float *dbias_up,
+                                        void *workspace, uint64_t workspace_bytes, void *stream);
+uint64_t matmul_gated_backward_workspace_bytes(int M, int N, int K, const void *x, int64_t ldx,
+                                               const void *w_gate, int64_t ldw_gate,
+                                               const void *w_up, int64_t ldw_up);
+
+/*
  * rmsnorm_run -- h = x + residual; out = h * rsqrt(mean(h^2) + eps) * weight,
  * row by row over `cols` columns, in fp32 from the inputs to one rounding of
  * each output.

@@ -80,3 +80,83 @@ def test_python_refusals():
     for call in (lambda: bg.layernorm(x), lambda: bg.layernorm_backward(x, x, v, v), lambda: bg.rmsnorm_backward(x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def gated(lib, M=4, N=8, K=16, dt=F16, x=256, ldx=16, wg=256, ldg=16, wu=256, ldu=16, bg_=None, bu=None, act=4, out=256, ldo=8,
+          g=None, ldg2=0, u=None, ldu2=0, ws=None, size=0):
+    return lib.matmul_gated_run(M, N, K, dt, x, ldx, wg, ldg, wu, ldu, bg_, bu, act, out, ldo, g, ldg2, u, ldu2, ws, size, None)
+
+
+def linear_back(lib, M=4, N=8, K=16, dt=F16, d=256, ldd=8, x=256, ldx=16, w=256, ldw=16, dx=256, lddx=16, dw=256, lddw=16, db=None,
+                ws=256, size=1 << 20):
+    return lib.matmul_backward_run(M, N, K, dt, d, ldd, x, ldx, w, ldw, dx, lddx, dw, lddw, db, ws, size, None)
+
+
+def gated_back(lib, M=4, N=8, K=16, dt=F16, d=256, ldd=8, x=256, ldx=16, wg=256, ldg=16, wu=256, ldu=16, g=256, ldg2=8, u=256, ldu2=8,
+               act=4, dx=256, lddx=16, dwg=256, lddwg=16, dwu=256, lddwu=16, dbg=None, dbu=None, ws=256, size=1 << 20):
+    return lib.matmul_gated_backward_run(M, N, K, dt, d, ldd, x, ldx, wg, ldg, wu, ldu, g, ldg2, u, ldu2, act, dx, lddx, dwg, lddwg,
+                                         dwu, lddwu, dbg, dbu, ws, size, None)
+
+
+SIZES = [{"M": -1}, {"N": 0}, {"K": 0}, {"K": -5}, {"dt": 3}, {"dt": -1}, {"x": None}, {"ldx": 15}, {"x": 257}]
+
+
+@pytest.mark.parametrize("bad", SIZES + [
+    {"wg": None}, {"wu": None}, {"out": None}, {"ldg": 15}, {"ldu": 15}, {"ldo": 7}, {"wg": 257}, {"wu": 257}, {"out": 257},
+    {"bg_": 258}, {"bu": 257}, {"act": 5}, {"act": -1}, {"g": 256, "ldg2": 7}, {"u": 256, "ldu2": 7}, {"g": 257, "ldg2": 8},
+    {"u": 257, "ldu2": 8}, {"ws": 264}, {"ldx": 17}, {"wg": 258}, {"ldu": 17, "ws": 256, "size": 255}])
+def test_gated_refuses(lib, bad):
+    assert gated(lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", SIZES + [
+    {"d": None}, {"w": None}, {"dx": None}, {"dw": None}, {"ldd": 7}, {"ldw": 15}, {"lddx": 15}, {"lddw": 15}, {"d": 257}, {"w": 257},
+    {"dx": 257}, {"dw": 257}, {"db": 258}, {"ws": None}, {"ws": 264}, {"size": 255}])
+def test_matmul_backward_refuses(lib, bad):
+    assert linear_back(lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", SIZES + [
+    {"d": None}, {"wg": None}, {"wu": None}, {"g": None}, {"u": None}, {"dx": None}, {"dwg": None}, {"dwu": None}, {"ldd": 7}, {"ldg": 15},
+    {"ldu": 15}, {"ldg2": 7}, {"ldu2": 7}, {"lddx": 15}, {"lddwg": 15}, {"lddwu": 15}, {"d": 257}, {"wg": 257}, {"wu": 257}, {"g": 257},
+    {"u": 257}, {"dx": 257}, {"dwg": 257}, {"dwu": 257}, {"dbg": 258}, {"dbu": 257}, {"act": 5}, {"act": -1}, {"ws": None}, {"ws": 264},
+    {"size": 255}])
+def test_gated_backward_refuses(lib, bad):
+    assert gated_back(lib, **bad) == INVALID
+
+
+def test_products_refuse_32_bit_operands_and_huge_sizes(lib):
+    for call in (gated, linear_back, gated_back):
+        assert call(lib, dt=F32) == UNSUPPORTED
+        assert call(lib, M=2 ** 30 + 1) == UNSUPPORTED
+
+
+def test_no_tokens_is_no_gated_layer(lib):
+    assert gated(lib, M=0) == 0
+
+
+def test_product_workspaces(lib):
+    """A copy of each operand off the 16-byte grid; the gradients' own: shares of dx, sums over runs of rows, and a gated
+    layer's two gradients."""
+    q = bg.matmul_gated_workspace_bytes
+    assert q(1000, 512, 256, 256, 256, 256, 256, 256, 256) == 0
+    assert q(1000, 512, 257, 256, 257, 256, 264, 256, 264) == -(-1000 * 528 // 256) * 256
+    assert q(1000, 512, 257, 256, 264, 256, 257, 256, 257) == 2 * -(-512 * 528 // 256) * 256
+    assert q(0, 5, 5, 256, 5, 256, 5, 256, 5) == 0
+    q = bg.matmul_backward_workspace_bytes
+    assert q(0, 5, 5, 256, 5, 256, 5, 256, 5) == 0 and q(2 ** 30 + 1, 5, 5, 256, 5, 256, 5, 256, 5) == 0
+    plain = q(4096, 4096, 4096, 256, 4096, 256, 4096, 256, 4096)
+    assert plain == 76 * 4096 * 4                              # tiles enough: no shares, runs of rows alone
+    assert q(4096, 4096, 4096, 256, 4097, 256, 4096, 256, 4096) == plain + 4096 * 4096 * 2
+    assert q(100, 4096, 4096, 256, 4096, 256, 4096, 256, 4096) > 100 * 4096 * 4
+    q = bg.matmul_gated_backward_workspace_bytes
+    assert q(4096, 4096, 4096, 256, 4096, 256, 4096, 256, 4096) == 2 * plain + 2 * 4096 * 4096 * 2
+
+
+def test_python_refusals_of_products():
+    x, w = torch.zeros(4, 16, dtype=torch.float16), torch.zeros(8, 16, dtype=torch.float16)
+    d = torch.zeros(4, 8, dtype=torch.float16)
+    for call in (lambda: bg.matmul_gated(x, w, w), lambda: bg.matmul_backward(d, x, w),
+                 lambda: bg.matmul_gated_backward(d, x, w, w, d, d)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

@@ -108,3 +108,69 @@ def act64(kind, z):
         p = torch.sigmoid(z)
         return z * p, p * (1 + z * (1 - p))
     return z, torch.ones_like(z)
+
+
+# Products.  As layer_ref derives: an instruction's 16 products and the accumulator are cut short by 2^-23 of a partial
+# sum, at most S, twice; so a sum of L products is off by (L / 16 + 9) 2^-22 S, S the sum of magnitudes.
+# Activations: an error of 2^-19 of max(|z|, 1), slopes at most 1.13; slopes are off by 2^-18 (a quotient of 2 ulp and an
+# exponential whose argument is off by |z| ulp, times factors of at most 10 where they are not negligible).
+
+def product_error(L, S):
+    return (L / 16 + 9) * 2.0 ** -22 * S
+
+
+def gated64(x, wg, wu, bg, bu, act):
+    """{name: (value, bound)} of y, g and u."""
+    x, wg, wu = x.double(), wg.double(), wu.double()
+    K = x.shape[1]
+    both = []
+    for w, b in ((wg, bg), (wu, bu)):
+        z, e = x @ w.T, product_error(K, x.abs() @ w.abs().T)
+        if b is not None:
+            z = z + b.double()
+            e = e + 2 * U * (z.abs() + b.double().abs())
+        both.append((z, e))
+    (g, eg), (u, eu) = both
+    a = act64(act, g)[0]
+    ea = 1.13 * eg + 2.0 ** -19 * g.abs().clamp(min=1) * (act not in ("relu", "none"))
+    y = a * u
+    return {"y": (y, ea * u.abs() + a.abs() * eu + ea * eu + 2 * U * y.abs()), "g": (g, eg), "u": (u, eu)}
+
+
+def product_backward64(dout, x, w):
+    """{name: (value, bound)} of dx, dw and db of one product of d (its own error: ed)."""
+    d, x, w = dout.double(), x.double(), w.double()
+    M, N = d.shape
+    return {"dx": (d @ w, product_error(N + 512, d.abs() @ w.abs())), "dw": (d.T @ x, product_error(M, d.abs().T @ x.abs())),
+            "db": (d.sum(0), column_adds(M) * U * d.abs().sum(0))}
+
+
+def gated_backward64(dout, x, wg, wu, g, u, act):
+    """{name: (value, bound)}: dg and du are off by the slopes' error and a rounding to the operands' type each."""
+    kind = x.dtype
+    d, x, wg, wu, g, u = (t.double() for t in (dout, x, wg, wu, g, u))
+    M, N = d.shape
+    a, s = act64(act, g)
+    smooth = act not in ("relu", "none")
+    dg, du = d * u * s, d * a
+    eg = (d * u).abs() * 2.0 ** -18 * smooth + 3 * U * dg.abs()
+    eu = d.abs() * 2.0 ** -19 * g.abs().clamp(min=1) * smooth + 2 * U * du.abs()
+    n = column_adds(M)
+    out = {"dbg": (dg.sum(0), eg.sum(0) + n * U * dg.abs().sum(0)), "dbu": (du.sum(0), eu.sum(0) + n * U * du.abs().sum(0))}
+    eg = eg + HALF[kind] * dg.abs() + TINY[kind]
+    eu = eu + HALF[kind] * du.abs() + TINY[kind]
+    S = dg.abs() @ wg.abs() + du.abs() @ wu.abs()
+    out["dx"] = (dg @ wg + du @ wu, eg @ wg.abs() + eu @ wu.abs() + product_error(2 * N + 640, S))
+    out["dwg"] = (dg.T @ x, eg.T @ x.abs() + product_error(M, dg.abs().T @ x.abs()))
+    out["dwu"] = (du.T @ x, eu.T @ x.abs() + product_error(M, du.abs().T @ x.abs()))
+    return out
+
+
+def check_norm(got, ref, roundings, what=""):
+    """The 2-norm of the error of independent roundings to got's type, each of at most half a step and of a third of its
+    square on average, with a half on top: an error in a few elements that each element's bound would hide."""
+    if ref.numel() < 2000:
+        return
+    rel = float((got.double() - ref).norm() / ref.norm().clamp(min=1e-300))
+    most = 1.5 * HALF[got.dtype] * math.sqrt(roundings / 3)
+    assert rel <= most, f"{what}: 2-norm {rel:.3e}, at most {most:.3e}"
