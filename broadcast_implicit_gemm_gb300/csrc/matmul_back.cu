@@ -81,37 +81,62 @@ struct BackJob {
                                                  uint32_t tmem, uint8_t *stage, int &piece, int lane)
     {
         const long long m_warp = u.m0 + rank * 128 + q * 32, rows = u.what == 0 ? p.M : p.N;
-        if (m_warp >= rows) return;
+        const int n = u.n0 + h * 64;
+        if (m_warp >= rows || n >= p.K) return;
+        const uint32_t from = tmem + (uint32_t)(h * 64);
+        if (u.what == 0 && p.split > 1) {
+            // a share: 32 columns of 32 bits at a time
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-            const int n = u.n0 + h * 64 + c * 32;
-            if (n >= p.K) return;
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tmem + (uint32_t)(h * 64 + c * 32), r);
-            tmem_wait_ld32(r);
-            if (u.what == 0 && p.split > 1) {
-                // 16 columns of 32 bits at a time: a box of 64 bytes by 32 rows
-#pragma unroll
-                for (int i = 0; i < 32; i += 16) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = r[i + j];
-                    const uint8_t *buf = stage_words<PairCfg::per_warp, 16>(stage, piece, lane, w);
-                    if (lane == 0 && n + i < p.K) {
-                        tma_store_3d(&maps.part, buf, n + i, (int)m_warp, u.part);
-                        bulk_commit();
-                    }
+            for (int c = 0; c < 64 && n + c < p.K; c += 32) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(from + (uint32_t)c, r);
+                tmem_wait_ld32(r);
+                const uint8_t *buf = stage_words<PairCfg::per_warp, 32>(stage, piece, lane, r);
+                if (lane == 0) {
+                    tma_store_3d(&maps.part, buf, n + c, (int)m_warp, u.part);
+                    bulk_commit();
                 }
-                continue;
             }
+            return;
+        }
+        const int w = max(0, u.what - 1);
+        const bool dx = u.what == 0;
+        if (dx ? p.dx_rows : p.dw_rows[w]) {
+            // 64 columns, a row of 128 bytes, by one TMA store: what is past the matrix it leaves alone
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(from + (uint32_t)(c * 32), r);
+                tmem_wait_ld32(r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t q4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        q4[j] = mm_pack2(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]), p.dt);
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c * 4 + i) ^ (lane & 7)) << 4)) =
+                        make_uint4(q4[0], q4[1], q4[2], q4[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(dx ? &maps.dx : &maps.dw[w], stage, n, (int)m_warp);
+                bulk_commit();
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int c = 0; c < 64 && n + c < p.K; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(from + (uint32_t)c, r);
+            tmem_wait_ld32(r);
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            if (u.what == 0)
-                put16(&maps.dx, p.dx_rows, p.dx, p.lddx, p.dt, rows, p.K, stage, piece, lane, m_warp, n, v);
-            else
-                put16(&maps.dw[u.what - 1], p.dw_rows[u.what - 1], p.dw[u.what - 1], p.lddw[u.what - 1], p.dt, rows, p.K,
-                      stage, piece, lane, m_warp, n, v);
+            put_turned(dx ? p.dx : p.dw[w], dx ? p.lddx : p.lddw[w], p.dt, rows, p.K, stage, lane, m_warp, n + c, v);
         }
     }
 };
@@ -129,7 +154,7 @@ __global__ void __launch_bounds__(256) back_join_kernel(const float *part, int s
     const float4 *from = reinterpret_cast<const float4 *>(part + m * pitch + k);
     const long long step = (long long)M * pitch / 4;
     float4 v = from[0];
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 1; s < split; ++s) {
         const float4 w = from[s * step];
         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;

@@ -28,7 +28,8 @@ struct BackArgs {
     int *err;
 };
 
-// All operands and outputs of 64 x 64 and 32 x 32 boxes; part: dx's shares, [split][M][K] fp32.
+// Operands as boxes of 64 x 64, outputs of 32 rows by 64; part: dx's shares, [split][M][K]
+// fp32, 32 by 32.
 struct BackMaps {
     CUtensorMap d[2], w[2], x, dx, dw[2], part;
 };
@@ -39,7 +40,8 @@ cudaError_t launch_back_join(const float *part, int split, int M, int K, long lo
                              cudaStream_t stream);
 
 // Before the products (gate_back.cu): d_g and d_u, rounded to the operands' type, and
-// sums over runs of rows where `sums` is not null: [runs][N] of d_g, the same of d_u.
+// sums over runs of rows where `sums` is not null: [runs][sum_pitch(N)] of d_g, the
+// same of d_u.
 // Or, for a plain product, the sums of d alone.
 struct GateBackArgs {
     int M, N, runs;
@@ -50,6 +52,7 @@ struct GateBackArgs {
     float *sums[2];
 };
 constexpr int kGateColumns = 256;    // of a block
+constexpr int kGateBeside(bool vec) { return vec ? 2 : 3; }      // blocks that an SM's registers hold
 cudaError_t launch_gate_back(const GateBackArgs &a, int dt, bool vec, cudaStream_t stream);
 
 }  // namespace bigemm

@@ -41,11 +41,15 @@ int dx_split(const Problem &p)
     return best;
 }
 
-// Runs of rows of the sums over tokens: eight blocks per SM, of 32 rows at least.
-int gate_runs(const Problem &p)
+// Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least, and
+// no second wave that is not a whole one (777 x 5001: 22 runs, not 25).  The sums of few
+// tokens of a plain product are a single run's, which needs no second launch.
+int gate_runs(const Problem &p, bool vec)
 {
-    const long long most = std::max<long long>(1, 8 * 2 * kPairs / up(p.N, kGateColumns));
-    return (int)std::min<long long>(most, up(p.M, 32));
+    if (p.count == 1 && p.M <= 512) return 1;
+    const long long across = up(p.N, kGateColumns), wave = 2ll * kPairs * kGateBeside(vec);
+    const long long want = std::min(std::max<long long>(1, 8 * 2 * kPairs / across), up(p.M, 32));
+    return (int)(want * across > wave && want * across < 2 * wave && across <= wave ? wave / across : want);
 }
 
 struct Space {
@@ -56,7 +60,7 @@ struct Space {
 Space space_of(const Problem &p)
 {
     Space s = {};
-    s.split = dx_split(p), s.runs = gate_runs(p);
+    s.split = dx_split(p), s.runs = std::max(gate_runs(p, false), gate_runs(p, true));
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -75,8 +79,8 @@ Space space_of(const Problem &p)
     s.packed = take(packed);
     s.part_pitch = (uint64_t)up(p.K, 4) * 4;
     s.part = take(s.split > 1 ? (uint64_t)s.split * p.M * s.part_pitch * 4 : 0);
-    // (whether there are biases is not known to who asks for the size)
-    s.sums = take((uint64_t)p.count * s.runs * p.N * 4);
+    // (whether there are biases, and how they lie, is not known to who asks for the size)
+    s.sums = take((uint64_t)p.count * s.runs * sum_pitch(p.N) * 4);
     s.total = at;
     return s;
 }
@@ -85,13 +89,13 @@ bool sizes_fit(const Problem &p) { return p.M <= kMaxSize && p.N <= kMaxSize && 
 
 bool reach(const void *p, long long ld, long long cols) { return p && ld >= cols && on_grid(p, 0, 1, 2); }
 
-// dx's shares as boxes of 32 rows by 64 bytes.
+// dx's shares as boxes of 32 rows by 128 bytes.
 bool part_map(CUtensorMap *map, const void *p, const Problem &a, const Space &s)
 {
     const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.M, (uint64_t)s.split};
     const uint64_t strides[2] = {s.part_pitch * 4, s.part_pitch * 4 * (uint64_t)a.M};
-    const uint32_t box[3] = {16, 32, 1}, ones[3] = {1, 1, 1};
-    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_64B);
+    const uint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bigemm_status zero_gradients(const Problem &p, cudaStream_t s)
@@ -127,23 +131,22 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     const void *d[2] = {p.dout, nullptr};
     long long ldd[2] = {p.ldd, 0};
     GateBackArgs g = {};
-    g.M = p.M, g.N = p.N, g.runs = at.runs, g.act = -1;
+    const bool vec = on_grid(p.dout, p.ldd, 2, 16) && (p.count == 1 || (on_grid(p.gate, p.ldg, 2, 16) && on_grid(p.up, p.ldu, 2, 16)));
+    g.M = p.M, g.N = p.N, g.runs = gate_runs(p, vec), g.act = -1;
     g.dout = p.dout, g.gate = p.gate, g.up = p.up, g.ldd = p.ldd, g.ldg = p.ldg, g.ldu = p.ldu;
     float *sums = reinterpret_cast<float *>(space + at.sums);
-    for (int i = 0; i < p.count; ++i) g.sums[i] = p.dbias[i] ? sums + (long long)i * at.runs * p.N : nullptr;
+    for (int i = 0; i < p.count; ++i)        // (a single run's sums are the result)
+        g.sums[i] = p.dbias[i] && g.runs > 1 ? sums + i * g.runs * sum_pitch(p.N) : p.dbias[i];
     const bool biases = p.dbias[0] || p.dbias[1];
     if (p.count == 2) {
         g.act = p.act, g.pitch = (long long)at.pitch;
         g.dg = space + at.d, g.du = space + at.d + at.pitch * (uint64_t)p.M * 2;
         d[0] = g.dg, d[1] = g.du, ldd[0] = ldd[1] = g.pitch;
     }
-    if (p.count == 2 || biases) {
-        const bool vec = on_grid(p.dout, p.ldd, 2, 16) && (p.count == 1 || (on_grid(p.gate, p.ldg, 2, 16) && on_grid(p.up, p.ldu, 2, 16)));
-        if (launch_gate_back(g, p.dt, vec, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
-    }
-    if (biases) {
+    if ((p.count == 2 || biases) && launch_gate_back(g, p.dt, vec, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    if (biases && g.runs > 1) {
         ColumnSums c = {};
-        c.parts = at.runs, c.cols = p.N;
+        c.parts = g.runs, c.cols = p.N;
         for (int i = 0; i < p.count; ++i)
             if (p.dbias[i]) c.from[c.count] = g.sums[i], c.out[c.count++] = p.dbias[i];
         if (launch_column_sums(c, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
@@ -171,10 +174,10 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
         a.dw[i] = p.dw[i], a.lddw[i] = p.lddw[i], a.dw_rows[i] = addressable(p.dw[i], p.lddw[i], 2);
         ok = ok && operand_map(&maps.d[i], d[i], p.dt, p.M, p.N, ldd[i], 64) &&
              operand_map(&maps.w[i], p.w[i], p.dt, p.N, p.K, p.ldw[i], 64) &&
-             (!a.dw_rows[i] || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+             (!a.dw_rows[i] || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
     }
     if (a.split > 1) ok = ok && part_map(&maps.part, space + at.part, p, at);
-    else if (a.dx_rows) ok = ok && box_map(&maps.dx, p.dx, p.dt, p.M, p.K, p.lddx, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    else if (a.dx_rows) ok = ok && box_map(&maps.dx, p.dx, p.dt, p.M, p.K, p.lddx, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok || launch_matmul_back(a, maps, pairs, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
     if (a.split > 1 && launch_back_join(reinterpret_cast<const float *>(space + at.part), a.split, p.M, p.K, (long long)at.part_pitch,
                                         p.dx, p.lddx, p.dt, s) != cudaSuccess)

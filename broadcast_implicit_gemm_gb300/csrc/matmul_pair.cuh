@@ -5,7 +5,7 @@
 //
 // As in matmul_many.cu: a pair of CTAs (cta_group::2) per 256 x 256 tile, each CTA
 // with 128 of its rows and half of the other operand in 32 KB stages of 64 elements of
-// the summed axis (6 of them), 4 MMAs of 128 cycles each; one warp loads, one issues,
+// the summed axis (5 of them), 4 MMAs of 128 cycles each; one warp loads, one issues,
 // sixteen drain, and two accumulators fill tensor memory, so that a tile's epilogue
 // runs beside the next one's MMAs.  One block per SM walks over its pair's units.
 #pragma once
@@ -22,9 +22,9 @@ struct PairCfg {
     static constexpr int drain = 16, threads = 128 + 32 * drain;
     static constexpr int launch_regs = 96, lead_regs = 56, drain_regs = 104;
     static_assert(lead_regs + drain / 4 * drain_regs <= threads / 128 * launch_regs, "a larger sum would wait for ever");
-    static constexpr int bn = 256, stages = 6;
+    static constexpr int bn = 256, stages = 5;
     static constexpr int operand = 128 * kRow, box = 64 * kRow;      // bytes a CTA stages of each; of a TMA box
-    static constexpr int per_warp = 2048;                            // output staging
+    static constexpr int per_warp = 4096;                            // output staging
     static constexpr int smem = stages * 2 * operand + drain * per_warp + 256 + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
 };

@@ -148,7 +148,7 @@ def back_case(which, rows, cols, kind="bf16", dsum=True, affine=True, pad=0, off
 
 @pytest.mark.parametrize("which", ["layer", "rms"])
 @pytest.mark.parametrize("cols", [1, 2, 7, 8, 33, 200, 256, 257, 264, 511, 1000, 2048, 2049, 4096, 5000, 8184, 8191, 8192, 8193, 8200,
-                                  16384, 20001])
+                                  12001, 16384, 20001, 33000, 65536, 65537, 70008])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_backward_widths(which, cols, kind):
     back_case(which, 7, cols, kind, seed=cols)
@@ -164,14 +164,14 @@ def test_backward_rows(which, rows, cols):
 @pytest.mark.parametrize("which", ["layer", "rms"])
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("dsum,affine", [(False, False), (True, False), (False, True), (True, True)])
-@pytest.mark.parametrize("cols", [392, 9000])
+@pytest.mark.parametrize("cols", [392, 9000, 66000])
 def test_backward_forms(which, kind, dsum, affine, cols):
     back_case(which, 33, cols, kind, dsum, affine)
 
 
 @pytest.mark.parametrize("which", ["layer", "rms"])
 @pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 8), (3, 1), (24, 16)])
-@pytest.mark.parametrize("cols", [200, 2049, 9001])
+@pytest.mark.parametrize("cols", [200, 2049, 9001, 66001])
 @pytest.mark.parametrize("kind", ["f16", "f32"])
 def test_backward_strides(which, pad, offset, cols, kind):
     back_case(which, 40, cols, kind, pad=pad, offset=offset)
@@ -179,7 +179,7 @@ def test_backward_strides(which, pad, offset, cols, kind):
 
 @pytest.mark.parametrize("which", ["layer", "rms"])
 @pytest.mark.parametrize("inplace", ["dout", "dsum"])
-@pytest.mark.parametrize("rows,cols", [(2000, 264), (400, 4096), (30, 10000), (700, 333)])
+@pytest.mark.parametrize("rows,cols", [(2000, 264), (400, 4096), (30, 10000), (700, 333), (200, 9999), (9, 70000)])
 def test_backward_in_place(which, inplace, rows, cols):
     back_case(which, rows, cols, "bf16", inplace=inplace)
 
@@ -188,6 +188,9 @@ def test_backward_in_place(which, inplace, rows, cols):
 def test_backward_many_rows(which):
     back_case(which, 3000, 8192, "bf16", seed=1)
     back_case(which, 3001, 1003, "bf16", seed=2)
+    back_case(which, 700, 16384, "f16", seed=3)
+    back_case(which, 301, 30001, "f16", seed=4)
+    back_case(which, 2000, 100, "f32", seed=5, pad=1)
 
 
 def test_backward_of_nothing():
@@ -232,6 +235,20 @@ def test_backward_follows_differences():
         return float((x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w6 * d).sum())
     slope = (rms(x6 + step * v6) - rms(x6 - step * v6)) / (2 * step)
     assert abs(float((dx.double() * v6).sum()) - slope) < 1e-5 * float((dx.double() * v6).abs().sum()) + 1e-5
+
+
+@pytest.mark.parametrize("which", ["layer", "rms"])
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+def test_backward_at_the_matrix_ends(which, kind):
+    """Rows off the grid in tensors of their own size: nothing before the first element or behind the last is there."""
+    for rows, cols in ((3, 77), (2, 1001), (5, 8195)):
+        back_case(which, rows, cols, kind, pad=0, offset=0)
+        x = rand((rows * cols + 5,), 1).to(TD[kind])[3: 3 + rows * cols].view(rows, cols)
+        d = rand((rows * cols + 1,), 2).to(TD[kind])[1:].view(rows, cols)
+        got = bg.rmsnorm_backward(d, x)
+        ref = tr.rmsnorm_backward64(d, x, None, 1e-6, None)
+        tr.check(got[0], *ref["dx"], "dx")
+        tr.check(got[1], *ref["dw"], "dw")
 
 
 def test_backward_in_a_graph():
