@@ -491,6 +491,7 @@ def _layer():
         loader.exec_module(module)
         module.init((torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn),
                     (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _workspace,
+                    torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
                                     lib.matmul_workspace_bytes, lib.layernorm_run, lib.layernorm_backward_run,
@@ -678,13 +679,17 @@ def layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None
 # inputs; outputs that are not given are made.  No autograd: a torch.autograd.Function is a call of each kind.
 
 def _gradient(out, like, stream):
+    if out is not None:
+        return out
     import torch
-    return _new(torch.empty, like.shape, like.dtype, like.device, stream) if out is None else out
+    return _new(torch.empty, like.shape, like.dtype, like.device, stream)
 
 
-def _sums(out, n, device, stream):
+def _sums(out, like, stream):
+    if out is not None:
+        return out
     import torch
-    return _new(torch.empty, (n,), torch.float32, device, stream) if out is None else out
+    return _new(torch.empty, (like.shape[-1],), torch.float32, like.device, stream)
 
 
 def layernorm_backward(dout, x, mean, rstd, weight=None, dsum=None, dx=None, dweight=None, dbias=None, stream=None):
@@ -692,7 +697,7 @@ def layernorm_backward(dout, x, mean, rstd, weight=None, dsum=None, dx=None, dwe
     from its call.  dsum, the gradient that reaches h along the residual stream, is added to dx, which may be dout or
     dsum itself.  dout, dsum and dx are of x's dtype, dweight and dbias float32."""
     dx = _gradient(dx, x, stream)
-    dweight, dbias = _sums(dweight, x.shape[-1], x.device, stream), _sums(dbias, x.shape[-1], x.device, stream)
+    dweight, dbias = _sums(dweight, x, stream), _sums(dbias, x, stream)
     args = (dout, x, mean, rstd, weight, 0.0, dsum, dx, dweight, dbias, stream)
     status = (_layer_module or _layer()).norm_backward(*args)
     if status:
@@ -702,7 +707,7 @@ def layernorm_backward(dout, x, mean, rstd, weight=None, dsum=None, dx=None, dwe
 
 def rmsnorm_backward(dout, x, weight=None, eps=1e-6, dsum=None, dx=None, dweight=None, stream=None):
     """(dx, dweight) of rmsnorm with this weight and eps, otherwise as layernorm_backward."""
-    dx, dweight = _gradient(dx, x, stream), _sums(dweight, x.shape[-1], x.device, stream)
+    dx, dweight = _gradient(dx, x, stream), _sums(dweight, x, stream)
     args = (dout, x, None, None, weight, eps, dsum, dx, dweight, None, stream)
     status = (_layer_module or _layer()).norm_backward(*args)
     if status:

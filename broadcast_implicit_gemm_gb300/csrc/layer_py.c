@@ -15,7 +15,7 @@ enum { DT_COUNT = 4, OTHER_DEVICE = -1 };
 
 static PyObject *g_dtypes[DT_COUNT];                 /* torch dtypes of F32, F16, BF16, MXF8 */
 static PyObject *g_scale_types[2];                   /* uint8, float8_e8m0fnu */
-static PyObject *g_current_stream, *g_current_device, *g_workspace;
+static PyObject *g_current_stream, *g_current_device, *g_workspace, *g_alloc, *g_free;
 static PyObject *s_shape, *s_stride, *s_device, *s_ptr, *s_dtype, *s_numel, *s_contiguous;
 
 static bigemm_status (*p_matmul)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *,
@@ -231,23 +231,55 @@ static int stream_on(PyObject *s, long device, void **stream)
     return !*stream && PyErr_Occurred() ? -1 : 0;
 }
 
-/* `bytes` of torch's memory (none for 0) beside t, the stream's until the call is done: it may be given out again
- * after this returns. */
-static int space_for(uint64_t bytes, PyObject *t, PyObject *stream, PyObject **workspace, void **space)
+/* A call's memory from torch, the stream's until the call is done: it may be given out again after this returns. */
+typedef struct {
+    PyObject *tensor, *address;      /* on a stream of its own, or on the current one */
+    void *ptr;
+} Space;
+
+/* `bytes` of it (none for 0) beside t, for a call on `stream`, given as s.  On the current stream it comes as an address:
+ * making a tensor takes 1.6 us by itself, and 7 between launches, whose code and data it drives out of the host's caches
+ * (8 x 256 rmsnorm_backward 12.8 us, 8.0 so). */
+static int space_for(uint64_t bytes, PyObject *t, PyObject *s, void *stream, Space *space)
 {
-    *workspace = NULL, *space = NULL;
+    space->tensor = space->address = NULL, space->ptr = NULL;
     if (bytes == 0) return 0;
     PyObject *b = PyLong_FromUnsignedLongLong(bytes);
     if (!b) return -1;
-    PyObject *const args[3] = {b, t, stream};
-    *workspace = PyObject_Vectorcall(g_workspace, args, 3, NULL);
+    if (s == Py_None) {
+        PyObject *h = PyLong_FromVoidPtr(stream);
+        if (h) {
+            PyObject *const args[2] = {b, h};
+            space->address = PyObject_Vectorcall(g_alloc, args, 2, NULL);
+            Py_DECREF(h);
+        }
+        Py_DECREF(b);
+        if (!space->address) return -1;
+        space->ptr = PyLong_AsVoidPtr(space->address);
+        return !space->ptr && PyErr_Occurred() ? -1 : 0;
+    }
+    PyObject *const args[3] = {b, t, s};
+    space->tensor = PyObject_Vectorcall(g_workspace, args, 3, NULL);
     Py_DECREF(b);
-    if (!*workspace) return -1;
-    if (pointer_of(*workspace, space) < 0) {
-        Py_CLEAR(*workspace);
+    if (!space->tensor) return -1;
+    if (pointer_of(space->tensor, &space->ptr) < 0) {
+        Py_CLEAR(space->tensor);
         return -1;
     }
     return 0;
+}
+
+/* The call's answer, its memory given back. */
+static PyObject *done(Space *space, bigemm_status st)
+{
+    Py_XDECREF(space->tensor);
+    if (space->address) {
+        PyObject *r = PyObject_CallOneArg(g_free, space->address);
+        Py_DECREF(space->address);
+        if (!r) return NULL;
+        Py_DECREF(r);
+    }
+    return PyLong_FromLong(st);
 }
 
 static int arity(const char *name, Py_ssize_t got, Py_ssize_t want)
@@ -261,7 +293,8 @@ static int arity(const char *name, Py_ssize_t got, Py_ssize_t want)
 static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix x, w, o = {0}, y;
-    void *xs = NULL, *ws = NULL, *ys = NULL, *bias, *stream, *space = NULL;
+    void *xs = NULL, *ws = NULL, *ys = NULL, *bias, *stream;
+    Space space;
     if (arity("product", n, 11) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 ||
         matrix(a[2], "w", &w, x.device, -1, x.cols) < 0)
         return NULL;
@@ -287,20 +320,19 @@ static PyObject *product(PyObject *self, PyObject *const *a, Py_ssize_t n)
     uint64_t bytes = 0;
     if (x.rows > 0)
         bytes = p_workspace((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld);
-    PyObject *workspace;
-    if (space_for(bytes, a[0], a[10], &workspace, &space) < 0) return NULL;
+    if (space_for(bytes, a[0], a[10], stream, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (mx)
         st = p_matmul_mx((int)x.rows, (int)w.rows, (int)x.cols, x.ptr, x.ld, xs, w.ptr, w.ld, ws, bias, act, combine,
-                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, space, bytes, stream);
+                         (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, ys, space.ptr, bytes,
+                         stream);
     else
         st = p_matmul((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, w.ptr, w.ld, bias, act,
-                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, space, bytes,
+                      combine, (bigemm_dtype)o.dtype, o.ptr, o.ld, (bigemm_dtype)y.dtype, y.ptr, y.ld, space.ptr, bytes,
                       stream);
     Py_END_ALLOW_THREADS
-    Py_XDECREF(workspace);
-    return PyLong_FromLong(st);
+    return done(&space, st);
 }
 
 /* norm(x, weight, residual, eps, sum_out, out, out_scale, stream) -> status */
@@ -382,7 +414,7 @@ static PyObject *layernorm(PyObject *self, PyObject *const *a, Py_ssize_t n)
 static PyObject *norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix d, x, sum = {0}, dx;
-    void *mean = NULL, *rstd = NULL, *weight, *dweight, *dbias = NULL, *stream, *space;
+    void *mean = NULL, *rstd = NULL, *weight, *dweight, *dbias = NULL, *stream;
     if (arity("norm_backward", n, 11) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
         matrix(a[0], "dout", &d, x.device, x.rows, x.cols) < 0)
         return NULL;
@@ -404,19 +436,18 @@ static PyObject *norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
     const uint64_t bytes = p_norm_workspace((int)x.rows, (int)x.cols);
-    PyObject *workspace;
-    if (space_for(bytes, a[1], a[10], &workspace, &space) < 0) return NULL;
+    Space space;
+    if (space_for(bytes, a[1], a[10], stream, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (layer)
         st = p_layernorm_backward((int)x.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, mean, rstd, weight,
-                                  sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, dbias, space, bytes, stream);
+                                  sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, dbias, space.ptr, bytes, stream);
     else
         st = p_rmsnorm_backward((int)x.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, weight, (float)eps,
-                                sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, space, bytes, stream);
+                                sum.ptr, sum.ld, dx.ptr, dx.ld, dweight, space.ptr, bytes, stream);
     Py_END_ALLOW_THREADS
-    Py_XDECREF(workspace);
-    return PyLong_FromLong(st);
+    return done(&space, st);
 }
 
 /* A matrix of x's type, or nothing for None where `optional`. */
@@ -433,7 +464,7 @@ static int beside(PyObject *t, const char *name, Matrix *m, const Matrix *x, lon
 static PyObject *gated(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix x, wg, wu, y, g = {0}, u = {0};
-    void *bg, *bu, *stream, *space;
+    void *bg, *bu, *stream;
     if (arity("gated", n, 10) < 0 || matrix(a[0], "x", &x, -1, -1, -1) < 0 || beside(a[1], "w_gate", &wg, &x, -1, x.cols, 0) < 0 ||
         beside(a[2], "w_up", &wu, &x, wg.rows, x.cols, 0) < 0 || vector(a[3], "bias_gate", wg.rows, x.device, &bg) < 0 ||
         vector(a[4], "bias_up", wg.rows, x.device, &bu) < 0)
@@ -447,22 +478,21 @@ static PyObject *gated(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
     const uint64_t bytes = p_gated_workspace((int)x.rows, (int)wg.rows, (int)x.cols, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr, wu.ld);
-    PyObject *workspace;
-    if (space_for(bytes, a[0], a[9], &workspace, &space) < 0) return NULL;
+    Space space;
+    if (space_for(bytes, a[0], a[9], stream, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     st = p_gated((int)x.rows, (int)wg.rows, (int)x.cols, (bigemm_dtype)x.dtype, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr, wu.ld, bg, bu,
-                 act, y.ptr, y.ld, g.ptr, g.ld, u.ptr, u.ld, space, bytes, stream);
+                 act, y.ptr, y.ld, g.ptr, g.ld, u.ptr, u.ld, space.ptr, bytes, stream);
     Py_END_ALLOW_THREADS
-    Py_XDECREF(workspace);
-    return PyLong_FromLong(st);
+    return done(&space, st);
 }
 
 /* product_backward(dout, x, w, dx, dw, dbias, stream) -> status */
 static PyObject *product_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix d, x, w, dx, dw;
-    void *dbias, *stream, *space;
+    void *dbias, *stream;
     if (arity("product_backward", n, 7) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
         beside(a[2], "w", &w, &x, -1, x.cols, 0) < 0 || beside(a[0], "dout", &d, &x, x.rows, w.rows, 0) < 0 ||
         beside(a[3], "dx", &dx, &x, x.rows, x.cols, 0) < 0 || beside(a[4], "dw", &dw, &x, w.rows, x.cols, 0) < 0 ||
@@ -472,22 +502,21 @@ static PyObject *product_backward(PyObject *self, PyObject *const *a, Py_ssize_t
     if (r < 0) return NULL;
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
     const uint64_t bytes = p_backward_workspace((int)x.rows, (int)w.rows, (int)x.cols, d.ptr, d.ld, x.ptr, x.ld, w.ptr, w.ld);
-    PyObject *workspace;
-    if (space_for(bytes, a[1], a[6], &workspace, &space) < 0) return NULL;
+    Space space;
+    if (space_for(bytes, a[1], a[6], stream, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     st = p_backward((int)x.rows, (int)w.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, w.ptr, w.ld, dx.ptr,
-                    dx.ld, dw.ptr, dw.ld, dbias, space, bytes, stream);
+                    dx.ld, dw.ptr, dw.ld, dbias, space.ptr, bytes, stream);
     Py_END_ALLOW_THREADS
-    Py_XDECREF(workspace);
-    return PyLong_FromLong(st);
+    return done(&space, st);
 }
 
 /* gated_backward(dout, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, dbias_gate, dbias_up, stream) -> status */
 static PyObject *gated_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     Matrix d, x, wg, wu, g, u, dx, dwg, dwu;
-    void *dbg, *dbu, *stream, *space;
+    void *dbg, *dbu, *stream;
     if (arity("gated_backward", n, 13) < 0 || matrix(a[1], "x", &x, -1, -1, -1) < 0 ||
         beside(a[2], "w_gate", &wg, &x, -1, x.cols, 0) < 0 || beside(a[3], "w_up", &wu, &x, wg.rows, x.cols, 0) < 0 ||
         beside(a[0], "dout", &d, &x, x.rows, wg.rows, 0) < 0 || beside(a[4], "gate", &g, &x, x.rows, wg.rows, 0) < 0 ||
@@ -504,26 +533,27 @@ static PyObject *gated_backward(PyObject *self, PyObject *const *a, Py_ssize_t n
     if (r > 0) return PyLong_FromLong(OTHER_DEVICE);
     const uint64_t bytes = p_gated_backward_workspace((int)x.rows, (int)wg.rows, (int)x.cols, x.ptr, x.ld, wg.ptr, wg.ld, wu.ptr,
                                                       wu.ld);
-    PyObject *workspace;
-    if (space_for(bytes, a[1], a[12], &workspace, &space) < 0) return NULL;
+    Space space;
+    if (space_for(bytes, a[1], a[12], stream, &space) < 0) return NULL;
     bigemm_status st;
     Py_BEGIN_ALLOW_THREADS
     st = p_gated_backward((int)x.rows, (int)wg.rows, (int)x.cols, (bigemm_dtype)x.dtype, d.ptr, d.ld, x.ptr, x.ld, wg.ptr, wg.ld,
                           wu.ptr, wu.ld, g.ptr, g.ld, u.ptr, u.ld, act, dx.ptr, dx.ld, dwg.ptr, dwg.ld, dwu.ptr, dwu.ld, dbg,
-                          dbu, space, bytes, stream);
+                          dbu, space.ptr, bytes, stream);
     Py_END_ALLOW_THREADS
-    Py_XDECREF(workspace);
-    return PyLong_FromLong(st);
+    return done(&space, st);
 }
 
-/* init(dtypes, scale_types, current_stream, current_device, workspace, functions) */
+/* init(dtypes, scale_types, current_stream, current_device, workspace, alloc, free, functions): workspace(bytes, tensor,
+ * stream) makes a tensor, alloc(bytes, stream) an address for free */
 static PyObject *init(PyObject *self, PyObject *args)
 {
-    PyObject *d, *st, *cs, *cd, *ws;
+    PyObject *d, *st, *cs, *cd, *ws, *al, *fr;
     PyObject *functions;
     enum { COUNT = 15 };
     unsigned long long f[COUNT];
-    if (!PyArg_ParseTuple(args, "O!O!OOOO!", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &PyTuple_Type, &functions))
+    if (!PyArg_ParseTuple(args, "O!O!OOOOOO!", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &al, &fr, &PyTuple_Type,
+                          &functions))
         return NULL;
     if (PyTuple_GET_SIZE(functions) != COUNT) return PyErr_Format(PyExc_ValueError, "init: wrong number of functions");
     for (int i = 0; i < COUNT; ++i) {
@@ -537,6 +567,8 @@ static PyObject *init(PyObject *self, PyObject *args)
     g_current_stream = Py_NewRef(cs);
     g_current_device = Py_NewRef(cd);
     g_workspace = Py_NewRef(ws);
+    g_alloc = Py_NewRef(al);
+    g_free = Py_NewRef(fr);
     p_matmul = (void *)(uintptr_t)f[0];
     p_matmul_mx = (void *)(uintptr_t)f[1];
     p_norm = (void *)(uintptr_t)f[2];

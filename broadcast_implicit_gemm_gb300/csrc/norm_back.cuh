@@ -271,42 +271,44 @@ __device__ __forceinline__ void st_shared_element(uint32_t at, T v)
 }
 
 // A thread's piece of a row to shared memory: its words are 512 bytes apart, the ring's `by`;
-// `left` bytes of the row from the first on.
+// bytes: of each word, inside the row.
 template <typename T>
-__device__ __forceinline__ void copy_piece(uint32_t to, uint32_t by, const uint8_t *from, int left)
+__device__ __forceinline__ void copy_piece(uint32_t to, uint32_t by, const uint8_t *from, const int (&bytes)[2], bool there)
 {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-        const int bytes = min(16, left - i * 512);
-        if (bytes > 0) cp_async16_part(to + i * by, from + i * 512, bytes);
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) cp_async16_part(to + i * by, from + i * 512, there ? bytes[i] : 0);
 }
 
 template <typename T>
-__device__ __forceinline__ void ring_piece(uint32_t from, uint32_t by, int left, Pair (&p)[kPairs])
+__device__ __forceinline__ void ring_piece(uint32_t from, uint32_t by, Pair (&p)[kPairs])
 {
     Raw<T> r;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = left > i * 512 ? ld_shared16(from + i * by) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = ld_shared16(from + i * by);
     pairs_of<T>(r, p);
 }
 
-// Thread t of tpr's share of the words that `count` elements from `from` on touch.  A word
-// that reaches past the matrix (its first or last) comes by its elements.
+// Thread t of tpr's share of the words that `count` elements from `from` on touch.  `edge`:
+// the matrix's first or last row, whose words may reach past it and come by elements then.
 template <typename T>
-__device__ __forceinline__ void copy_words(uint32_t to, const T *from, int count, int t, int tpr, const Span &span)
+__device__ __forceinline__ void copy_words(uint32_t to, const T *from, int count, int t, int tpr, bool edge, const Span &span)
 {
     const int skew = (int)(reinterpret_cast<uintptr_t>(from) & 15), words = (skew + count * (int)sizeof(T) + 15) >> 4;
     const uint8_t *first = reinterpret_cast<const uint8_t *>(from) - skew;
+    if (!edge) {
 #pragma unroll
-    for (int k = 0; k <= (int)sizeof(T) / 2; ++k) {
-        const int w = t + k * tpr;
-        if (w >= words) break;
-        const uint8_t *at = first + 16ll * w;
+        for (int k = 0; k <= (int)sizeof(T) / 2; ++k) {
+            const int w = t + k * tpr;
+            cp_async16_part(to + w * 16, first + 16 * w, w < words ? 16 : 0);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int w = t; w < words; w += tpr) {
+        const uint8_t *at = first + 16 * w;
         if (at >= span.begin && at + 16 <= span.end) {
             cp_async16_part(to + w * 16, at, 16);
         } else {
-#pragma unroll 1
             for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
                 const T *e = reinterpret_cast<const T *>(at) + i;
                 if (e >= from && e < from + count) st_shared_element(to + w * 16 + i * (int)sizeof(T), *e);
@@ -326,8 +328,8 @@ __device__ __forceinline__ void word_values(uint32_t words, const uint8_t *from,
         if (c.whole) {
             uint32_t w[kPairs];
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                w[i] = at & 2 ? __funnelshift_r(ld_shared4(at - 2 + 128 * i), ld_shared4(at + 2 + 128 * i), 16) : ld_shared4(at + 128 * i);
+            for (int i = 0; i < kPairs; ++i)         // (an even start needs one of the two: no branch)
+                w[i] = __funnelshift_r(ld_shared4((at & ~3u) + 128 * i), ld_shared4((at & ~3u) + 4 + 128 * i), (at & 2) * 8);
             Raw<T> r;
             r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
             pairs_of<T>(r, p);
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), 1024 / norm_threads(TPR)) n
     const Span d_span = span_of(a.dout, a.rows, a.ldd, a.cols, sizeof(T)), x_span = span_of(a.x, a.rows, a.ldx, a.cols, sizeof(T));
     const Span s_span = SUM ? span_of(a.dsum, a.rows, a.lds, a.cols, sizeof(T)) : d_span;
     // the next row to ask for, from this thread's first column on, or this block's
-    const int first = VEC ? c.c0 : base, inside = VEC ? (a.cols - c.c0) * (int)sizeof(T) : columns;
+    const int first = VEC ? c.c0 : base, left = (a.cols - c.c0) * (int)sizeof(T);
+    const int inside[2] = {max(0, min(16, left)), max(0, min(16, left - 512))};
     auto start = [&](const void *p, long long ld) { return static_cast<const uint8_t *>(p) + ((long long)r * ld + first) * (int)sizeof(T); };
     const uint8_t *next_d = start(a.dout, a.ldd), *next_x = start(a.x, a.ldx), *next_s = SUM ? start(a.dsum, a.lds) : nullptr;
     T *out = static_cast<T *>(a.dx) + (long long)r * a.ldo;
@@ -401,16 +404,16 @@ __global__ void __launch_bounds__(norm_threads(TPR), 1024 / norm_threads(TPR)) n
     const uint32_t ring1 = ring0 + S * turn_bytes;
     uint32_t now = ring0, fill = ring0;
     auto fetch = [&]() {
-        if (ahead < rows) {
-            if constexpr (VEC) {
-                copy_piece<T>(fill, by, next_d, inside);
-                copy_piece<T>(fill + apart, by, next_x, inside);
-                if (SUM) copy_piece<T>(fill + 2 * apart, by, next_s, inside);
-            } else {
-                copy_words<T>(fill, reinterpret_cast<const T *>(next_d), inside, t, tpr, d_span);
-                copy_words<T>(fill + apart, reinterpret_cast<const T *>(next_x), inside, t, tpr, x_span);
-                if (SUM) copy_words<T>(fill + 2 * apart, reinterpret_cast<const T *>(next_s), inside, t, tpr, s_span);
-            }
+        const bool there = ahead < rows;
+        if constexpr (VEC) {
+            copy_piece<T>(fill, by, next_d, inside, there);
+            copy_piece<T>(fill + apart, by, next_x, inside, there);
+            if (SUM) copy_piece<T>(fill + 2 * apart, by, next_s, inside, there);
+        } else if (there) {
+            const bool edge = ahead == 0 || ahead == rows - 1 || a.cols * (int)sizeof(T) < 16;
+            copy_words<T>(fill, reinterpret_cast<const T *>(next_d), columns, t, tpr, edge, d_span);
+            copy_words<T>(fill + apart, reinterpret_cast<const T *>(next_x), columns, t, tpr, edge, x_span);
+            if (SUM) copy_words<T>(fill + 2 * apart, reinterpret_cast<const T *>(next_s), columns, t, tpr, edge, s_span);
         }
         ahead += a.step, next_d += a.step_d, next_x += a.step_x;
         if (SUM) next_s += a.step_s;
@@ -418,6 +421,13 @@ __global__ void __launch_bounds__(norm_threads(TPR), 1024 / norm_threads(TPR)) n
         if (fill == ring1) fill = ring0;
         cp_async_commit();
     };
+    if (VEC && left <= (R::q - 1) * 512) {
+        // words past the row: zeros, once
+        for (uint32_t i = ring0; i != ring1; i += apart)
+            for (int k = 0; k < R::q; ++k)
+                if (inside[k] == 0)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(i + k * by), "r"(0) : "memory");
+    }
     Pair dw[kPairs], db[LAYER ? kPairs : 1], w[kPairs];
     {
         float f[kPiece];
@@ -450,20 +460,18 @@ __global__ void __launch_bounds__(norm_threads(TPR), 1024 / norm_threads(TPR)) n
         Pair d[kPairs], x[kPairs];
         cp_async_wait<S - 2>();
         if constexpr (VEC) {
-            // (a warp past the last row, a word past the row: what is there is nothing's)
-            const int left = ROWS == 1 || live ? inside : 0;
-            ring_piece<T>(now, by, left, d);
-            ring_piece<T>(now + apart, by, left, x);
+            ring_piece<T>(now, by, d);
+            ring_piece<T>(now + apart, by, x);
         } else {
             // the row's words of all its threads; and all have done with the stage before
             if (TPR == 32) __syncwarp();
             else __syncthreads();
             word_values<T>(now, now_d, base, c, a.cols, d);
             word_values<T>(now + apart, now_x, base, c, a.cols, x);
-            if (ROWS > 1 && !live) {
+        }
+        if (ROWS > 1 && !live) {             // a warp past the last row: what its words hold is nothing's
 #pragma unroll
-                for (int i = 0; i < kPairs; ++i) d[i] = x[i] = pair(0.f, 0.f);
-            }
+            for (int i = 0; i < kPairs; ++i) d[i] = x[i] = pair(0.f, 0.f);
         }
         fetch();
         float rstd = LAYER ? __shfl_sync(0xffffffffu, root, n & 31) : 0.f;
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), 1024 / norm_threads(TPR)) n
             }
             const Pair scale = pair(rstd, rstd);
             Pair s[kPairs];
-            if constexpr (SUM && VEC) ring_piece<T>(now + 2 * apart, by, inside, s);
+            if constexpr (SUM && VEC) ring_piece<T>(now + 2 * apart, by, s);
             if constexpr (SUM && !VEC) word_values<T>(now + 2 * apart, now_s, base, c, a.cols, s);
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {

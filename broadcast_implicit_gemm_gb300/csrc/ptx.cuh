@@ -200,10 +200,12 @@ __device__ __forceinline__ void cp_async16(void *dst_smem, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src)
                  : "memory");
 }
-// The first `bytes` (0 to 16) of the 16 from there, zeros after them.
+// The first `bytes` (at most 16) of the 16 from there, zeros after them; nothing for 0 or less.
 __device__ __forceinline__ void cp_async16_part(uint32_t dst_smem, const void *src, int bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(bytes)
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.gt.s32 p, %2, 0;\n\t"
+                 "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst_smem), "l"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
