@@ -71,21 +71,21 @@ __device__ __forceinline__ void slopes_of(int act, const float (&d)[kPiece], flo
     }
 }
 
-// A lane's 8 of a block's 256 columns: consecutive ones on the 16-byte grid; off it a pair
-// of each 64, so that a warp's plain loads cover consecutive elements, and d_g and d_u,
-// which are on the grid, are written in words (lanes with 8 consecutive ones, in two
-// aligned loads and a shift: 777 x 5001 f16 gelu 27 us, 13 so).
+// A lane's 8 of a block's 256 columns: consecutive ones on the 16-byte grid; off it one
+// of each 32, so that a warp's plain loads cover consecutive elements (lanes with 8
+// consecutive ones, in two aligned loads and a shift: 777 x 5001 f16 gelu 27 us; with
+// pairs 18).
 template <bool VEC>
-__device__ __forceinline__ int gate_column(int lane, int i) { return VEC ? lane * kPiece + i : i / 2 * 64 + lane * 2 + i % 2; }
+__device__ __forceinline__ int gate_column(int lane, int i) { return VEC ? lane * kPiece + i : i * 32 + lane; }
 
 template <typename T, bool VEC>
 struct GateRaw {
-    std::conditional_t<VEC, Raw<T>, uint32_t[kPiece / 2]> d;
+    std::conditional_t<VEC, Raw<T>, T[kPiece]> d;
 
     __device__ __forceinline__ void load(const T *row, int c0, int lane, int cols)
     {
-        const int c = c0 + gate_column<VEC>(lane, 0);
         if constexpr (VEC) {
+            const int c = c0 + lane * kPiece;
             if (c + kPiece <= cols) {
                 d.q[0] = *reinterpret_cast<const uint4 *>(row + c);
                 return;
@@ -93,25 +93,10 @@ struct GateRaw {
             T *e = reinterpret_cast<T *>(&d);
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) e[i] = c + i < cols ? row[c + i] : from_f32<T>(0.f);
-        } else if (c0 + kGateColumns > cols) {
-            const uint16_t *e = reinterpret_cast<const uint16_t *>(row);
-#pragma unroll
-            for (int i = 0; i < kPiece / 2; ++i) {
-                const int at = c + i * 64;
-                d[i] = (at < cols ? (uint32_t)e[at] : 0u) | (at + 1 < cols ? (uint32_t)e[at + 1] : 0u) << 16;
-            }
-        } else if (reinterpret_cast<uintptr_t>(row) % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < kPiece / 2; ++i) d[i] = *reinterpret_cast<const uint32_t *>(row + c + i * 64);
         } else {
-            // words of a lane's second and its neighbour's first element; the warp's first and last by themselves
-            const uint16_t *e = reinterpret_cast<const uint16_t *>(row) + c;
+            const T *e = row + c0 + lane;
 #pragma unroll
-            for (int i = 0; i < kPiece / 2; ++i, e += 64) {
-                const uint32_t w = lane < 31 ? *reinterpret_cast<const uint32_t *>(e + 1) : (uint32_t)e[1];
-                const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1);
-                d[i] = (lane > 0 ? before >> 16 : (uint32_t)e[0]) | w << 16;
-            }
+            for (int i = 0; i < kPiece; ++i) d[i] = c0 + i * 32 + lane < cols ? e[i * 32] : from_f32<T>(0.f);
         }
     }
     __device__ __forceinline__ void values(float (&v)[kPiece]) const
@@ -119,25 +104,23 @@ struct GateRaw {
         if constexpr (VEC) {
             unpack<T>(d, v);
         } else {
-            constexpr int dt = std::is_same_v<T, __half> ? BIGEMM_F16 : BIGEMM_BF16;
-            mm_unpack8(make_uint4(d[0], d[1], d[2], d[3]), dt, v);
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) v[i] = to_f32<T>(d[i]);
         }
     }
 };
 
-// Rows of d_g and d_u start on the 16-byte grid and have room for whole words.
+// Rows of d_g and d_u start on the 16-byte grid.
 template <typename T, bool VEC>
 __device__ __forceinline__ void gate_store(T *row, int c0, int lane, int cols, const float (&v)[kPiece])
 {
     if constexpr (VEC) {
         store_piece<T, true>(row, c0 + lane * kPiece, cols, v);
     } else {
-        constexpr int dt = std::is_same_v<T, __half> ? BIGEMM_F16 : BIGEMM_BF16;
-        T *to = row + c0 + lane * 2;
+        T *e = row + c0 + lane;
 #pragma unroll
-        for (int i = 0; i < kPiece / 2; ++i)
-            if (c0 + kGateColumns <= cols || c0 + lane * 2 + i * 64 < cols)
-                *reinterpret_cast<uint32_t *>(to + i * 64) = mm_pack2(v[2 * i], v[2 * i + 1], dt);
+        for (int i = 0; i < kPiece; ++i)
+            if (c0 + i * 32 + lane < cols) e[i * 32] = from_f32<T>(v[i]);
     }
 }
 
@@ -155,7 +138,7 @@ __global__ void __launch_bounds__(256, kGateBeside(VEC)) gate_back_kernel(const 
     float sg[SUMS ? kPiece : 1], su[SUMS && GATED ? kPiece : 1];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] = 0.f, su[SUMS && GATED ? i : 0] = 0.f;
-    constexpr int U = !GATED ? (VEC ? 8 : 4) : VEC ? 2 : 1;       // rows whose loads leave together
+        constexpr int U = !GATED ? (VEC ? 8 : 4) : VEC ? 2 : 1;       // rows whose loads leave together
     for (long long r = r0 + warp; r < r1; r += 8 * U) {
         GateRaw<T, VEC> d[U], g[GATED ? U : 1], u[GATED ? U : 1];
 #pragma unroll
