@@ -428,9 +428,10 @@ struct PackOperand {
     uint8_t *dst;
     long long rows, src_pitch, dst_pitch, bytes, runs;     // bytes: of a row
 };
+constexpr int kPackMost = 3;
 struct PackArgs {
-    PackOperand op[2];
-    long long items0;
+    PackOperand op[kPackMost];
+    long long items[kPackMost];      // up to the end of each
 };
 cudaError_t launch_matmul_pack(PackArgs &a, cudaStream_t stream);
 

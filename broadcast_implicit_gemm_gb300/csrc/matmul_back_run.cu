@@ -23,17 +23,20 @@ struct Problem {
 };
 
 // How many shares dx's units are cut into.  In blocks' time (0.33 us): a unit takes its
-// blocks and 6 more, all units together what they take over the pairs, and each share
-// past the first is written and read again in fp32 (at about 5 TB/s from L2).
-// Fewer shares where it makes no difference.
+// blocks and kUnitCost more, all units together what they take over the pairs, and each
+// share past the first is written and read again in fp32 (at about 5 TB/s from L2).
+// Fewer shares where it makes no difference.  100 x 4096 x 4096: 30.1 us whole, 25.7 in 2,
+// 25.3 in 4, 27.4 in 8; 777 x 5001 x 1000: 43.3, 32.8, 27.5 and 36.6; 1024 x 4096 x 4096:
+// 47.0, 64, 73 and 103.  (kUnitCost 2, 4, 6, 10: 64 x 8192 x 8192 82, 60, 64 and 71 us.)
+constexpr int kUnitCost = 4;
 int dx_split(const Problem &p)
 {
     const long long blocks = p.count * up(p.N, 64), tiles = up(p.M, 256) * up(p.K, 256);
-    const long long dw = p.count * up(p.N, 256) * up(p.K, 256) * (up(p.M, 64) + 6);
+    const long long dw = p.count * up(p.N, 256) * up(p.K, 256) * (up(p.M, 64) + kUnitCost);
     long long least = -1;
     int best = 1;
     for (int s = 1; s <= 32 && s * 4 <= blocks; ++s) {
-        const long long unit = up(blocks, s) + 6, waves = up(tiles * s, kPairs);
+        const long long unit = up(blocks, s) + kUnitCost, waves = up(tiles * s, kPairs);
         const long long walk = std::max(up(tiles * s * unit + dw, kPairs), waves * unit);
         const long long join = s > 1 ? 8 + (2ll * s * p.M * p.K * 4) / 1650000 : 0;
         if (least < 0 || walk + join < least) least = walk + join, best = s;
@@ -165,7 +168,7 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     const long long dx_units = (long long)a.dx_m * a.dx_n * a.split, dw_units = (long long)p.count * a.dw_m * a.dw_n;
     if (dx_units + dw_units > 0x3fffffff) return BIGEMM_ERR_UNSUPPORTED;
     const int pairs = (int)std::min<long long>(pairs_of_all, dx_units + dw_units);
-    a.walk = make_back_walk((int)dx_units, (int)dw_units, pairs, up((long long)p.count * a.n_blocks, a.split) + 6, a.m_blocks + 6);
+    a.walk = make_back_walk((int)dx_units, (int)dw_units, pairs, up((long long)p.count * a.n_blocks, a.split) + kUnitCost, a.m_blocks + kUnitCost);
     a.dx = p.dx, a.lddx = p.lddx, a.dx_rows = addressable(p.dx, p.lddx, 2);
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;

@@ -45,10 +45,11 @@ inline bool operand_map(CUtensorMap *map, const void *p, int dt, long long rows,
     return box_map(map, p, dt, rows, cols, ld, box_rows, dt == BIGEMM_MXF8 ? kRow : kRow / 2, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Operands that TMA cannot address, copied to `space` one after the other.
+// Operands that TMA cannot address, at most kPackMost, copied to `space` one after the
+// other.
 struct PackList {
     uint8_t *space;
-    PackOperand op[4] = {};
+    PackArgs args = {};
     int count = 0;
 
     explicit PackList(uint8_t *to) : space(to) {}
@@ -57,21 +58,11 @@ struct PackList {
     {
         if (addressable(p, ld, es)) return;
         const long long pitch = up(cols * es, 16) * 16;
-        op[count++] = {static_cast<const uint8_t *>(p), space, rows, ld * es, pitch, cols * es, 0};
+        args.op[count++] = {static_cast<const uint8_t *>(p), space, rows, ld * es, pitch, cols * es, 0};
         p = space, ld = pitch / es;
         space += packed_bytes(rows, cols, es);
     }
-    cudaError_t run(cudaStream_t stream) const
-    {
-        for (int i = 0; i < count; i += 2) {
-            PackArgs k = {};
-            k.op[0] = op[i];
-            if (i + 1 < count) k.op[1] = op[i + 1];
-            const cudaError_t e = launch_matmul_pack(k, stream);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
-    }
+    cudaError_t run(cudaStream_t stream) { return count > 0 ? launch_matmul_pack(args, stream) : cudaSuccess; }
 };
 
 }  // namespace

@@ -1,5 +1,5 @@
 // matmul_pack.cu -- a matrix product's operands whose rows are off the 16-byte
-// grid, copied to rows that are on it, both in one launch.  Bound by memory: a
+// grid, copied to rows that are on it, all in one launch.  Bound by memory: a
 // warp takes a run of 128 pieces of 16 bytes of a row, four per lane in flight.
 #include "matmul.cuh"
 #include "unaligned.cuh"
@@ -14,9 +14,11 @@ __global__ void __launch_bounds__(256) matmul_pack_kernel(const PackArgs a)
     constexpr int U = 4;
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const bool second = item >= a.items0;
-    const PackOperand &o = second ? a.op[1] : a.op[0];
-    const long long i = second ? item - a.items0 : item;
+    int which = 0;
+#pragma unroll
+    for (int k = 0; k + 1 < kPackMost; ++k) which += item >= a.items[k] ? 1 : 0;
+    const PackOperand &o = a.op[which];
+    const long long i = which > 0 ? item - a.items[which - 1] : item;
     const long long row = i / o.runs;
     if (row >= o.rows) return;
     const long long p0 = (i - row * o.runs) * 32 * U + lane;
@@ -42,9 +44,13 @@ __global__ void __launch_bounds__(256) matmul_pack_kernel(const PackArgs a)
 cudaError_t launch_matmul_pack(PackArgs &a, cudaStream_t stream)
 {
     ProfScope prof("matmul_pack", stream);
-    for (PackOperand &o : a.op) o.runs = o.bytes > 2048 ? (o.bytes + 2047) / 2048 : 1;
-    a.items0 = a.op[0].rows * a.op[0].runs;
-    const long long blocks = (a.items0 + a.op[1].rows * a.op[1].runs + 7) / 8;
+    long long end = 0;
+    for (int k = 0; k < kPackMost; ++k) {
+        PackOperand &o = a.op[k];
+        o.runs = o.bytes > 2048 ? (o.bytes + 2047) / 2048 : 1;
+        a.items[k] = end += o.rows * o.runs;
+    }
+    const long long blocks = (end + 7) / 8;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return launch_pdl(matmul_pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
 }
