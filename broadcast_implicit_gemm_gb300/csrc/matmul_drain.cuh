@@ -28,6 +28,7 @@ template <int PER_WARP, int WORDS>
 __device__ __forceinline__ const uint8_t *stage_words(uint8_t *stage, int &piece, int lane, const uint32_t (&w)[WORDS])
 {
     constexpr int bytes = WORDS * 128;
+    static_assert(bytes <= PER_WARP, "the next warp's staging follows");
     constexpr bool two = 2 * bytes <= PER_WARP;
     uint8_t *buf = stage + (two ? (piece & 1) * bytes : 0);
     if (lane == 0) bulk_wait_read<two ? 1 : 0>();

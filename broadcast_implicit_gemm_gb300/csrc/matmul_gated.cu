@@ -15,6 +15,8 @@ namespace bigemm {
 namespace {
 
 struct GatedJob {
+    // (five stages and twice the staging: 8192 x 4096 -> 16384 bf16 1102 us, 1084 so)
+    static constexpr int stages = 6, per_warp = 2048;
     using Args = GatedArgs;
     using Maps = GatedMaps;
     struct Unit {
@@ -83,11 +85,11 @@ struct GatedJob {
         float v[32];
         if (p.gate) {
             sums<32>(from[0], p.bias, p.vec_bias, n, p.N, v);
-            put16(&maps.kept[0], p.vec_gate, p.gate, p.ldgate, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
+            put16<per_warp>(&maps.kept[0], p.vec_gate, p.gate, p.ldgate, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
         }
         if (p.up) {
             sums<32>(from[1], p.bias_up, p.vec_bias_up, n, p.N, v);
-            put16(&maps.kept[1], p.vec_up, p.up, p.ldup, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
+            put16<per_warp>(&maps.kept[1], p.vec_up, p.up, p.ldup, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
         }
         // sixteen at a time: g and u together
 #pragma unroll
@@ -99,7 +101,7 @@ struct GatedJob {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[c + i] = g[i] * w[i];
         }
-        put16(&maps.out, p.vec_out, p.out, p.ldo, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
+        put16<per_warp>(&maps.out, p.vec_out, p.out, p.ldo, p.out_dt, p.M, p.N, stage, piece, lane, m_warp, n, v);
     }
 };
 

@@ -5,7 +5,7 @@
 //
 // As in matmul_many.cu: a pair of CTAs (cta_group::2) per 256 x 256 tile, each CTA
 // with 128 of its rows and half of the other operand in 32 KB stages of 64 elements of
-// the summed axis (5 of them), 4 MMAs of 128 cycles each; one warp loads, one issues,
+// the summed axis (5 or 6 of them), 4 MMAs of 128 cycles each; one warp loads, one issues,
 // sixteen drain, and two accumulators fill tensor memory, so that a tile's epilogue
 // runs beside the next one's MMAs.  One block per SM walks over its pair's units.
 #pragma once
@@ -22,11 +22,9 @@ struct PairCfg {
     static constexpr int drain = 16, threads = 128 + 32 * drain;
     static constexpr int launch_regs = 96, lead_regs = 56, drain_regs = 104;
     static_assert(lead_regs + drain / 4 * drain_regs <= threads / 128 * launch_regs, "a larger sum would wait for ever");
-    static constexpr int bn = 256, stages = 5;
+    static constexpr int bn = 256;
     static constexpr int operand = 128 * kRow, box = 64 * kRow;      // bytes a CTA stages of each; of a TMA box
-    static constexpr int per_warp = 4096;                            // output staging
-    static constexpr int smem = stages * 2 * operand + drain * per_warp + 256 + 1024;
-    static_assert(smem <= 227 * 1024, "shared memory");
+    static constexpr int smem(int stages, int per_warp) { return stages * 2 * operand + drain * per_warp + 256 + 1024; }
 };
 
 // The four MMAs of 64 elements of the summed axis for a CTA pair; an operand's start
@@ -89,6 +87,7 @@ __device__ __forceinline__ void put_turned(void *out, long long ld, int dt, long
 }
 
 // The same to a 16-bit matrix, whole boxes on the 16-byte grid by TMA.
+template <int PER_WARP>
 __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void *out, long long ld, int dt, long long rows,
                                       long long cols, uint8_t *stage, int &piece, int lane, long long m_warp, int n,
                                       const float (&v)[32])
@@ -102,7 +101,7 @@ __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_BF16);
         }
-        const uint8_t *buf = stage_words<PairCfg::per_warp, 16>(stage, piece, lane, w);
+        const uint8_t *buf = stage_words<PER_WARP, 16>(stage, piece, lane, w);
         if (lane == 0 && m_warp < rows) {
             tma_store_2d(map, buf, n, (int)m_warp);
             bulk_commit();
@@ -113,6 +112,7 @@ __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void
 }
 
 // Job:
+//   stages of both operands, per_warp bytes of output staging
 //   Args (with timeout_ns, err), Maps, Unit (with k0, k1: its blocks of the summed axis)
 //   static bool unit(p, turn, pair, pairs, Unit &)   the pair's unit of this turn; false: none left
 //   static void load(maps, p, u, kb, rank, sa, sb, bar)   this CTA's 2 x 16 KB of a block, counted on bar
@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(PairCfg::threads, 1)
     matmul_pair_kernel(const __grid_constant__ typename Job::Maps maps, const typename Job::Args p)
 {
     using C = PairCfg;
-    constexpr int S = C::stages;
+    constexpr int S = Job::stages, PER_WARP = Job::per_warp;
+    static_assert(C::smem(S, PER_WARP) <= 227 * 1024, "shared memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sa = smem, *sb = sa + S * C::operand, *out_stage = sb + S * C::operand;
-    uint64_t *full = reinterpret_cast<uint64_t *>(out_stage + C::drain * C::per_warp);
+    uint64_t *full = reinterpret_cast<uint64_t *>(out_stage + C::drain * PER_WARP);
     uint64_t *empty = full + S, *tfull = empty + S, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(PairCfg::threads, 1)
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
         const uint32_t tempty_even = mapa_shared(smem_u32(tempty), 0);
-        uint8_t *stage = out_stage + (warp - 4) * C::per_warp;
+        uint8_t *stage = out_stage + (warp - 4) * PER_WARP;
         int a = 0, piece = 0;
         uint32_t acc_phase = 0;
         typename Job::Unit u;
@@ -263,11 +264,12 @@ template <class Job>
 cudaError_t launch_pairs(const typename Job::Args &a, const typename Job::Maps &maps, int pairs, cudaStream_t stream)
 {
     auto kern = matmul_pair_kernel<Job>;
+    constexpr int smem = PairCfg::smem(Job::stages, Job::per_warp);
     static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         // the split of registers counts on what the block is launched with
         cudaFuncAttributes fa;
@@ -279,7 +281,7 @@ cudaError_t launch_pairs(const typename Job::Args &a, const typename Job::Maps &
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2u * (unsigned)pairs);
     cfg.blockDim = dim3(PairCfg::threads);
-    cfg.dynamicSmemBytes = PairCfg::smem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
