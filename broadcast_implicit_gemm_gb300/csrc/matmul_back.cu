@@ -156,11 +156,13 @@ __global__ void __launch_bounds__(256) back_join_kernel(const float *part, int s
     if (m >= M) return;
     const float4 *from = reinterpret_cast<const float4 *>(part + m * pitch + k);
     const long long step = (long long)M * pitch / 4;
-    float4 v = from[0];
-#pragma unroll 8
-    for (int s = 1; s < split; ++s) {
-        const float4 w = from[s * step];
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < split; s += 8) {         // eight loads leave together, however few shares there are
+        float4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = s + i < split ? from[(s + i) * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
     }
     T *to = dx + m * lddx + k;
     alignas(8) const T o[4] = {T(v.x), T(v.y), T(v.z), T(v.w)};

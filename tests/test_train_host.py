@@ -68,7 +68,7 @@ def test_norm_backward_workspace(lib):
     assert q(0, 8) == 0 and q(8, 0) == 0
     assert q(1, 8192) == 2 * 8192 * 4                          # a row of partial sums of each gradient
     assert q(10000, 8192) == 152 * 2 * 8192 * 4                # one of each block of a wave
-    assert q(10000, 256) == 152 * 8 * 2 * 256 * 4
+    assert q(10000, 256) == 152 * 4 * 2 * 256 * 4              # (blocks beside each other have four turns each)
     assert q(10000, 20000) == 38 * 2 * 20000 * 4               # or of a cluster of four
     assert q(5, 65537) == (5 * 2 * 65540 + 5) * 4              # and a root per row of longer ones
     assert q(2 ** 31 - 1, 2 ** 30) == (2 * 2 ** 30 + 2 ** 31 - 1) * 4
