@@ -43,6 +43,7 @@ bigemm_status norm_backward(NormBackArgs &a, bool layer, int dtype, void *worksp
         return launch_column_sums(sums, s) == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
     }
     const size_t es = dtype_size(dtype);
+    if (a.dweight == a.dbias) return BIGEMM_ERR_INVALID_ARG;
     if (!a.dout || !a.x || !a.dx || (layer && (!a.mean || !a.rstd))) return BIGEMM_ERR_INVALID_ARG;
     if (a.ldd < a.cols || a.ldx < a.cols || a.ldo < a.cols || (a.dsum && a.lds < a.cols)) return BIGEMM_ERR_INVALID_ARG;
     if (!aligned(a.dout, 0, 1, es) || !aligned(a.x, 0, 1, es) || !aligned(a.dx, 0, 1, es) || !aligned(a.dsum, 0, 1, es) ||
@@ -92,6 +93,7 @@ bigemm_status layernorm_run(int rows, int cols, bigemm_dtype in_dtype, const voi
         !aligned(weight, 0, 1, 4) || !aligned(bias, 0, 1, 4) || !aligned(out_scale, 0, 1, 16) || !aligned(mean, 0, 1, 4) ||
         !aligned(rstd, 0, 1, 4))
         return BIGEMM_ERR_INVALID_ARG;
+    if (out == sum_out || (mean && mean == rstd)) return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();
     if (!ds) return BIGEMM_ERR_CUDA;
     const bool vec = aligned(x, ldx, es, 16) && aligned(residual, ldr, es, 16) && aligned(sum_out, lds, es, 16) &&

@@ -234,6 +234,7 @@ bigemm_status gated(GatedArgs &a, void *workspace, uint64_t workspace_bytes, voi
     if (!on_grid(a.x, 0, 1, 2) || !on_grid(a.w, 0, 1, 2) || !on_grid(a.w_up, 0, 1, 2) || !on_grid(a.out, 0, 1, 2) ||
         !on_grid(a.gate, 0, 1, 2) || !on_grid(a.up, 0, 1, 2) || !on_grid(a.bias, 0, 1, 4) || !on_grid(a.bias_up, 0, 1, 4))
         return BIGEMM_ERR_INVALID_ARG;
+    if (!distinct({a.x, a.w, a.w_up, a.out, a.gate, a.up}, 3)) return BIGEMM_ERR_INVALID_ARG;
     const uint64_t space = gated_workspace(a);
     if (!on_grid(workspace, 0, 1, 16) || (space > 0 && (!workspace || workspace_bytes < space))) return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();

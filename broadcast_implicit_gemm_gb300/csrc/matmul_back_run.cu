@@ -123,6 +123,8 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     for (int i = 0; i < p.count; ++i)
         if (!reach(p.w[i], p.ldw[i], p.K)) return BIGEMM_ERR_INVALID_ARG;
     if (p.count == 2 && (!reach(p.gate, p.ldg, p.N) || !reach(p.up, p.ldu, p.N))) return BIGEMM_ERR_INVALID_ARG;
+    if (!distinct({p.dout, p.x, p.w[0], p.w[1], p.gate, p.up, p.dx, p.dw[0], p.dw[1], p.dbias[0], p.dbias[1]}, 6))
+        return BIGEMM_ERR_INVALID_ARG;
     const Space at = space_of(p);
     if (!on_grid(workspace, 0, 1, 16) || !workspace || bytes < at.total) return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();

@@ -359,7 +359,7 @@ uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, cons
  *   bias_up [N] fp32, each or NULL; fp32 sums, out rounded once (g and u are not
  *   rounded on the way to it)
  *   gate, up [M,N] of dtype, each or NULL (not wanted): receive g and u, each rounded
- *   once, which matmul_gated_backward_run takes
+ *   once, which matmul_gated_backward_run takes.  out, gate and up are buffers of their own
  *   workspace: matmul_gated_workspace_bytes of device memory on a 16-byte boundary,
  *   the call's until it is done; NULL where that is 0.
  * Errors: as matmul_run.
@@ -382,7 +382,7 @@ uint64_t matmul_gated_workspace_bytes(int M, int N, int K, const void *x, int64_
  *   dx [M,K] = dout w,  dw [N,K] = dout^T x,  dbias [N] = sum over tokens of dout
  *   all but dbias (fp32, or NULL: not wanted) of dtype (F16 or BF16); fp32 sums, each
  *   output rounded once; the sums' order does not depend on timing.  M = 0 writes zeros
- *   to dw and dbias.  No output may be an input.
+ *   to dw and dbias.  The outputs are buffers of their own.
  *   workspace: matmul_backward_workspace_bytes of device memory on a 16-byte boundary,
  *   the call's until it is done.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype F32; a size above 2^30), CUDA.

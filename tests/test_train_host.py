@@ -16,13 +16,13 @@ def lib():
     return bg.load_library()
 
 
-def layernorm(lib, rows=2, cols=8, dt=F16, x=256, ldx=8, r=None, ldr=0, g=None, b=None, h=None, ldh=0, out_dt=F16, out=256,
+def layernorm(lib, rows=2, cols=8, dt=F16, x=256, ldx=8, r=None, ldr=0, g=None, b=None, h=None, ldh=0, out_dt=F16, out=512,
               ldo=8, s=None, mean=None, rstd=None):
     return lib.layernorm_run(rows, cols, dt, x, ldx, r, ldr, g, b, 1e-5, h, ldh, out_dt, out, ldo, s, mean, rstd, None)
 
 
-def layer_back(lib, rows=2, cols=8, dt=F16, d=256, ldd=8, x=256, ldx=8, mean=256, rstd=256, w=None, s=None, lds=0, dx=256,
-               ldo=8, dw=256, db=256, space=256, size=1 << 20):
+def layer_back(lib, rows=2, cols=8, dt=F16, d=256, ldd=8, x=256, ldx=8, mean=256, rstd=256, w=None, s=None, lds=0, dx=512,
+               ldo=8, dw=1024, db=2048, space=256, size=1 << 20):
     return lib.layernorm_backward_run(rows, cols, dt, d, ldd, x, ldx, mean, rstd, w, s, lds, dx, ldo, dw, db, space, size, None)
 
 
@@ -34,7 +34,7 @@ def rms_back(lib, rows=2, cols=8, dt=F16, d=256, ldd=8, x=256, ldx=8, w=None, s=
 @pytest.mark.parametrize("bad", [
     {"rows": -1}, {"cols": 0}, {"dt": 3}, {"dt": -1}, {"out_dt": 4}, {"x": None}, {"out": None}, {"ldx": 7}, {"ldo": 7},
     {"r": 256, "ldr": 7}, {"h": 256, "ldh": 7}, {"x": 257}, {"r": 257, "ldr": 8}, {"g": 258}, {"b": 257}, {"out_dt": MX},
-    {"s": 256}, {"out_dt": MX, "s": 264}, {"mean": 258}, {"rstd": 257}])
+    {"s": 256}, {"out_dt": MX, "s": 264}, {"mean": 258}, {"rstd": 257}, {"mean": 1024, "rstd": 1024}, {"h": 512, "ldh": 8}])
 def test_layernorm_refuses(lib, bad):
     assert layernorm(lib, **bad) == INVALID
 
@@ -49,7 +49,7 @@ BACK = [{"rows": -1}, {"cols": 0}, {"dt": 3}, {"dt": -1}, {"d": None}, {"x": Non
         {"space": None}, {"space": 264}, {"size": 63}]
 
 
-@pytest.mark.parametrize("bad", BACK + [{"db": None}, {"db": 257}, {"mean": None}, {"rstd": None}, {"mean": 258}, {"rstd": 258}])
+@pytest.mark.parametrize("bad", BACK + [{"db": None}, {"db": 257}, {"mean": None}, {"rstd": None}, {"mean": 258}, {"rstd": 258}, {"db": 1024}])
 def test_layernorm_backward_refuses(lib, bad):
     assert layer_back(lib, **bad) == INVALID
 
@@ -83,18 +83,18 @@ def test_python_refusals():
             call()
 
 
-def gated(lib, M=4, N=8, K=16, dt=F16, x=256, ldx=16, wg=256, ldg=16, wu=256, ldu=16, bg_=None, bu=None, act=4, out=256, ldo=8,
+def gated(lib, M=4, N=8, K=16, dt=F16, x=256, ldx=16, wg=256, ldg=16, wu=256, ldu=16, bg_=None, bu=None, act=4, out=512, ldo=8,
           g=None, ldg2=0, u=None, ldu2=0, ws=None, size=0):
     return lib.matmul_gated_run(M, N, K, dt, x, ldx, wg, ldg, wu, ldu, bg_, bu, act, out, ldo, g, ldg2, u, ldu2, ws, size, None)
 
 
-def linear_back(lib, M=4, N=8, K=16, dt=F16, d=256, ldd=8, x=256, ldx=16, w=256, ldw=16, dx=256, lddx=16, dw=256, lddw=16, db=None,
+def linear_back(lib, M=4, N=8, K=16, dt=F16, d=256, ldd=8, x=256, ldx=16, w=256, ldw=16, dx=512, lddx=16, dw=1024, lddw=16, db=None,
                 ws=256, size=1 << 20):
     return lib.matmul_backward_run(M, N, K, dt, d, ldd, x, ldx, w, ldw, dx, lddx, dw, lddw, db, ws, size, None)
 
 
 def gated_back(lib, M=4, N=8, K=16, dt=F16, d=256, ldd=8, x=256, ldx=16, wg=256, ldg=16, wu=256, ldu=16, g=256, ldg2=8, u=256, ldu2=8,
-               act=4, dx=256, lddx=16, dwg=256, lddwg=16, dwu=256, lddwu=16, dbg=None, dbu=None, ws=256, size=1 << 20):
+               act=4, dx=512, lddx=16, dwg=1024, lddwg=16, dwu=2048, lddwu=16, dbg=None, dbu=None, ws=256, size=1 << 20):
     return lib.matmul_gated_backward_run(M, N, K, dt, d, ldd, x, ldx, wg, ldg, wu, ldu, g, ldg2, u, ldu2, act, dx, lddx, dwg, lddwg,
                                          dwu, lddwu, dbg, dbu, ws, size, None)
 
@@ -105,14 +105,16 @@ SIZES = [{"M": -1}, {"N": 0}, {"K": 0}, {"K": -5}, {"dt": 3}, {"dt": -1}, {"x": 
 @pytest.mark.parametrize("bad", SIZES + [
     {"wg": None}, {"wu": None}, {"out": None}, {"ldg": 15}, {"ldu": 15}, {"ldo": 7}, {"wg": 257}, {"wu": 257}, {"out": 257},
     {"bg_": 258}, {"bu": 257}, {"act": 5}, {"act": -1}, {"g": 256, "ldg2": 7}, {"u": 256, "ldu2": 7}, {"g": 257, "ldg2": 8},
-    {"u": 257, "ldu2": 8}, {"ws": 264}, {"ldx": 17}, {"wg": 258}, {"ldu": 17, "ws": 256, "size": 255}])
+    {"u": 257, "ldu2": 8}, {"ws": 264}, {"ldx": 17}, {"wg": 258}, {"ldu": 17, "ws": 256, "size": 255},
+    {"g": 512, "ldg2": 8}, {"g": 1024, "ldg2": 8, "u": 1024, "ldu2": 8}, {"u": 256, "ldu2": 8}])
 def test_gated_refuses(lib, bad):
     assert gated(lib, **bad) == INVALID
 
 
 @pytest.mark.parametrize("bad", SIZES + [
     {"d": None}, {"w": None}, {"dx": None}, {"dw": None}, {"ldd": 7}, {"ldw": 15}, {"lddx": 15}, {"lddw": 15}, {"d": 257}, {"w": 257},
-    {"dx": 257}, {"dw": 257}, {"db": 258}, {"ws": None}, {"ws": 264}, {"size": 255}])
+    {"dx": 257}, {"dw": 257}, {"db": 258}, {"ws": None}, {"ws": 264}, {"size": 255},
+    {"dx": 256}, {"dw": 256}, {"dw": 512}, {"db": 1024}])
 def test_matmul_backward_refuses(lib, bad):
     assert linear_back(lib, **bad) == INVALID
 
@@ -121,7 +123,7 @@ def test_matmul_backward_refuses(lib, bad):
     {"d": None}, {"wg": None}, {"wu": None}, {"g": None}, {"u": None}, {"dx": None}, {"dwg": None}, {"dwu": None}, {"ldd": 7}, {"ldg": 15},
     {"ldu": 15}, {"ldg2": 7}, {"ldu2": 7}, {"lddx": 15}, {"lddwg": 15}, {"lddwu": 15}, {"d": 257}, {"wg": 257}, {"wu": 257}, {"g": 257},
     {"u": 257}, {"dx": 257}, {"dwg": 257}, {"dwu": 257}, {"dbg": 258}, {"dbu": 257}, {"act": 5}, {"act": -1}, {"ws": None}, {"ws": 264},
-    {"size": 255}])
+    {"size": 255}, {"dwg": 256}, {"dwu": 1024}, {"dx": 2048}, {"dbg": 4096, "dbu": 4096}])
 def test_gated_backward_refuses(lib, bad):
     assert gated_back(lib, **bad) == INVALID
 
