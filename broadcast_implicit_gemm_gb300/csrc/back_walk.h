@@ -1,9 +1,10 @@
 // back_walk.h -- which unit of the gradients' products (matmul_back.cu) a pair of CTAs
 // takes at each turn.
 //
-// Units 0 to dx - 1 are dx's, long ones, and dx to dx + dw - 1 are dw's.  The pairs take
-// the dx units in turn; the `late` ones that get one fewer take `ahead` dw units each
-// meanwhile, and then all walk the rest in turn.
+// There are long units, 0 to dx - 1, and short ones, dx to dx + dw - 1 (where dw's units
+// are the longer ones they come first).  The pairs take the long ones in turn; the `late`
+// ones that get one fewer take `ahead` short units each meanwhile, and then all walk the
+// rest in turn.
 //
 // No CUDA dependency on the host side, so that a plain C++ test can check it.
 #pragma once
@@ -17,14 +18,15 @@
 namespace bigemm {
 
 struct BackWalk {
-    int dx, dw;                      // units
+    int dx, dw;                      // long and short units
     int late, ahead;
+    int whole, extra;                // long ones of every pair, and pairs that have one more
 };
 
 // dx_time, dw_time: a unit's, in the same measure.
 BIGEMM_BW_HD BackWalk make_back_walk(int dx, int dw, int pairs, long long dx_time, long long dw_time)
 {
-    BackWalk w = {dx, dw, 0, 0};
+    BackWalk w = {dx, dw, 0, 0, dx / pairs, dx % pairs};
     if (dx % pairs) {
         w.late = pairs - dx % pairs;
         const long long fit = dx_time / dw_time, most = dw / w.late;
@@ -38,7 +40,7 @@ BIGEMM_BW_HD int back_unit(const BackWalk &w, int turn, int pair, int pairs)
 {
     const int i = turn * pairs + pair;
     if (i < w.dx) return i;
-    const int first = pairs - w.late, behind = w.dx / pairs + (pair < w.dx % pairs ? 1 : 0);
+    const int first = pairs - w.late, behind = w.whole + (pair < w.extra ? 1 : 0);
     int j = turn - behind;           // turns since this pair's last dx unit
     int k;
     if (pair >= first && j < w.ahead) {

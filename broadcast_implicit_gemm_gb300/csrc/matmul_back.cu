@@ -9,9 +9,9 @@
 //
 // A dx unit is long (4096 tokens, 2 x 16384 channels: 512 blocks) and a dw unit short
 // (64): the pairs share them as back_walk.h says (4096 x 4096 x 16384 gated: 3449
-// blocks' time per pair, 3776 in two launches).  Few tokens leave too few dx units:
-// each is cut along the summed axis then, the shares go to a workspace in fp32, and
-// launch_back_join adds them in their order.
+// blocks' time per pair, 3776 in two launches).  Few tokens leave too few dx units, and
+// few channels too few dw units: each is cut along the summed axis then, the shares go to
+// a workspace in fp32, and launch_back_join adds them in their order.
 #include "matmul_back.cuh"
 
 #include "matmul_pair.cuh"
@@ -34,21 +34,32 @@ struct BackJob {
 
     static __device__ __forceinline__ bool unit(const Args &p, int turn, int pair, int pairs, Unit &u)
     {
-        const int i = back_unit(p.walk, turn, pair, pairs);
+        int i = back_unit(p.walk, turn, pair, pairs);
         if (i < 0) return false;
-        if (i < p.walk.dx) {
-            const int tiles = p.dx_m * p.dx_n, blocks = p.count * p.n_blocks;
-            u.part = i / tiles;
-            const Tile t = tile_in(p.dx_m, p.dx_n, i - u.part * tiles);
+        const bool first = i < p.walk.dx;
+        if (!first) i -= p.walk.dx;
+        if (first != p.dw_first) {
+            const Tile t = place(p.to_dx, i, u);
             u.what = 0, u.m0 = t.m * 256, u.n0 = t.n * 256;
-            u.k0 = (int)((long long)blocks * u.part / p.split), u.k1 = (int)((long long)blocks * (u.part + 1) / p.split);
-            return true;
+        } else {
+            const Tile t = place(p.to_dw, i, u);
+            const int which = t.m >= p.dw_m ? 1 : 0;
+            u.what = 1 + which, u.m0 = (t.m - which * p.dw_m) * 256, u.n0 = t.n * 256;
         }
-        const Tile t = tile_in(p.count * p.dw_m, p.dw_n, i - p.walk.dx);
-        const int which = t.m >= p.dw_m ? 1 : 0;
-        u.what = 1 + which, u.m0 = (t.m - which * p.dw_m) * 256, u.n0 = t.n * 256;
-        u.k0 = 0, u.k1 = p.m_blocks, u.part = 0;
         return true;
+    }
+
+    // Tile and share of a result's unit, in tile_in's order.
+    static __device__ __forceinline__ Tile place(const UnitGrid &g, int i, Unit &u)
+    {
+        uint32_t t;
+        u.part = (int)fd_divmod((uint32_t)i, g.tiles, &t);
+        u.k0 = (int)fd_div((uint32_t)(g.blocks * u.part), g.shares);
+        u.k1 = (int)fd_div((uint32_t)(g.blocks * (u.part + 1)), g.shares);
+        uint32_t r;
+        const int m = (int)fd_divmod(t, g.group, &r) * 8, rows = min(8, g.m - m);
+        if (rows == 8) return {m + (int)(r & 7), (int)(r >> 3)};
+        return {m + (int)r % rows, (int)r / rows};
     }
 
     // a box's coordinates: column, row
@@ -87,7 +98,9 @@ struct BackJob {
         const int n = u.n0 + h * 64;
         if (m_warp >= rows || n >= p.K) return;
         const uint32_t from = tmem + (uint32_t)(h * 64);
-        if (u.what == 0 && p.split > 1) {
+        const bool dx = u.what == 0;
+        const int w = max(0, u.what - 1);
+        if ((dx ? p.to_dx.split : p.to_dw.split) > 1) {
             // a share: 32 columns of 32 bits at a time
 #pragma unroll 1
             for (int c = 0; c < 64 && n + c < p.K; c += 32) {
@@ -96,83 +109,104 @@ struct BackJob {
                 tmem_wait_ld32(r);
                 const uint8_t *buf = stage_words<per_warp, 32>(stage, piece, lane, r);
                 if (lane == 0) {
-                    tma_store_3d(&maps.part, buf, n + c, (int)m_warp, u.part);
+                    tma_store_3d(dx ? &maps.part[0] : &maps.part[1], buf, n + c, (int)m_warp, u.part + (dx ? 0 : w * p.to_dw.split));
                     bulk_commit();
                 }
             }
             return;
         }
-        const int w = max(0, u.what - 1);
-        const bool dx = u.what == 0;
+        // 64 columns, a row of 128 bytes, by one TMA store: what is past the matrix it leaves alone
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t r[32], q[16];
+            tmem_ld_32x32b_x32(from + (uint32_t)(c * 32), r);
+            tmem_wait_ld32(r);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            words_of(v, p.dt, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c * 4 + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+        }
         if (dx ? p.dx_rows : p.dw_rows[w]) {
-            // 64 columns, a row of 128 bytes, by one TMA store: what is past the matrix it leaves alone
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(from + (uint32_t)(c * 32), r);
-                tmem_wait_ld32(r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t q4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        q4[j] = mm_pack2(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]), p.dt);
-                    *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c * 4 + i) ^ (lane & 7)) << 4)) =
-                        make_uint4(q4[0], q4[1], q4[2], q4[3]);
-                }
-            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 tma_store_2d(dx ? &maps.dx : &maps.dw[w], stage, n, (int)m_warp);
                 bulk_commit();
             }
-            return;
-        }
-#pragma unroll 1
-        for (int c = 0; c < 64 && n + c < p.K; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(from + (uint32_t)c, r);
-            tmem_wait_ld32(r);
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            put_turned(dx ? p.dx : p.dw[w], dx ? p.lddx : p.lddw[w], p.dt, rows, p.K, stage, lane, m_warp, n + c, v);
+        } else {
+            __syncwarp();
+            put_off_grid<32>(dx ? p.dx : p.dw[w], dx ? p.lddx : p.lddw[w], rows, p.K, stage, lane, m_warp, n);
         }
     }
 };
 
-// A thread adds four columns of the shares; the shares lie in L2, where the products
-// left them.
+// A warp adds 128 columns of a row's shares, which lie in L2, where the products left
+// them; eight loads of a lane leave together, however few shares there are.
 template <typename T>
-__global__ void __launch_bounds__(256) back_join_kernel(const float *part, int split, int M, int K, long long pitch, T *dx,
-                                                        long long lddx, bool vec, int runs)
+__global__ void __launch_bounds__(256) back_join_kernel(const JoinArgs a)
 {
     griddep_enter();
-    const long long item = (long long)blockIdx.x * 256 + threadIdx.x, m = item / runs;
-    const int k = (int)(item - m * runs) * 4;
-    if (m >= M) return;
-    const float4 *from = reinterpret_cast<const float4 *>(part + m * pitch + k);
-    const long long step = (long long)M * pitch / 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < split; s += 8) {         // eight loads leave together, however few shares there are
-        float4 w[8];
+    const int lane = (int)threadIdx.x & 31;
+    long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int which = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = s + i < split ? from[(s + i) * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k + 1 < kJoinMost; ++k) which += item >= a.items[k] ? 1 : 0;
+    if (which >= a.count) return;
+    const JoinResult &o = a.result[which];
+    if (which > 0) item -= a.items[which - 1];
+    const long long m = item / a.runs;
+    const int k0 = (int)(item - m * a.runs) * 128;
+    if (m >= o.rows) return;
+    T *row = static_cast<T *>(o.out) + m * o.ld;
+    const float *from = o.part + m * a.pitch + k0;
+    const long long step = (long long)o.rows * a.pitch;
+    if (o.vec) {
+        // four columns a lane (the rows' last words have room)
+        const int k = k0 + lane * 4;
+        if (k >= a.cols) return;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < o.split; s += 8) {
+            float4 w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
+            for (int i = 0; i < 8; ++i)
+                w[i] = s + i < o.split ? *reinterpret_cast<const float4 *>(from + (s + i) * step + lane * 4)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
+        }
+        alignas(8) const T t[4] = {T(v.x), T(v.y), T(v.z), T(v.w)};
+        if (k + 4 <= a.cols) {
+            *reinterpret_cast<uint2 *>(row + k) = *reinterpret_cast<const uint2 *>(t);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < a.cols) row[k + i] = t[i];
+        }
+        return;
     }
-    T *to = dx + m * lddx + k;
-    alignas(8) const T o[4] = {T(v.x), T(v.y), T(v.z), T(v.w)};
-    if (vec && k + 4 <= K) {
-        *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(o);
-    } else {
+    // one of each 32 a lane
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < o.split; s += 2) {
+        float w[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (k + i < K) to[i] = o[i];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[i][j] = s + i < o.split && k0 + j * 32 + lane < a.cols ? from[(s + i) * step + j * 32 + lane] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += w[i][j];
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (k0 + j * 32 + lane < a.cols) row[k0 + j * 32 + lane] = T(v[j]);
 }
 
 }  // namespace
@@ -183,20 +217,17 @@ cudaError_t launch_matmul_back(const BackArgs &a, const BackMaps &maps, int pair
     return launch_pairs<BackJob>(a, maps, pairs, stream);
 }
 
-cudaError_t launch_back_join(const float *part, int split, int M, int K, long long pitch, void *dx, long long lddx, int dt,
-                             cudaStream_t stream)
+cudaError_t launch_back_join(JoinArgs &a, int dt, cudaStream_t stream)
 {
     ProfScope prof("matmul_back_join", stream);
-    const int runs = (int)((K + 3ll) / 4);
-    const long long blocks = ((long long)M * runs + 255) / 256;
+    a.runs = (a.cols + 127ll) / 128;
+    long long end = 0;
+    for (int k = 0; k < kJoinMost; ++k) a.items[k] = end += k < a.count ? a.result[k].rows * a.runs : 0;
+    const long long blocks = (end + 7) / 8;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const bool vec = reinterpret_cast<uintptr_t>(dx) % 8 == 0 && lddx % 4 == 0;
     const dim3 grid((unsigned)blocks);
-    return dt == BIGEMM_F16
-               ? launch_pdl(back_join_kernel<__half>, grid, dim3(256), 0, stream, part, split, M, K, pitch,
-                            static_cast<__half *>(dx), lddx, vec, runs)
-               : launch_pdl(back_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, part, split, M, K, pitch,
-                            static_cast<__nv_bfloat16 *>(dx), lddx, vec, runs);
+    return dt == BIGEMM_F16 ? launch_pdl(back_join_kernel<__half>, grid, dim3(256), 0, stream, a)
+                            : launch_pdl(back_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, a);
 }
 
 }  // namespace bigemm

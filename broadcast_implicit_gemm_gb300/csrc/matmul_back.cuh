@@ -8,18 +8,31 @@
 // with one d for a plain product and two for a gated one.
 #pragma once
 #include "back_walk.h"
+#include "fastdiv.h"
 #include "matmul.cuh"
 
 namespace bigemm {
 
-// Units of 256 x 256 sums; of the products' summed axis, blocks of 64.
+// A result's units: tiles of 256 x 256 sums, each in `split` shares of its summed axis of
+// `blocks` blocks of 64.  Divisors are the launch's: a unit of one block (few tokens) is
+// done in less time than divisions take (64 x 8192 x 8192: 60 us with some, 73 with more).
+struct UnitGrid {
+    int m, n, split, blocks;
+    FastDiv tiles, group, shares;    // by m * n, 8 * n and split
+};
+inline UnitGrid make_unit_grid(int m, int n, int split, int blocks)
+{
+    return {m, n, split, blocks, make_fastdiv((uint32_t)(m * n)), make_fastdiv(8u * (uint32_t)n), make_fastdiv((uint32_t)split)};
+}
+
 struct BackArgs {
     int M, N, K;                     // tokens, output channels (of each product), input channels
     int dt;                          // bigemm_dtype of everything
     int count;                       // products: 1 or 2
-    int n_blocks, m_blocks;          // of one d's channels, of the tokens
-    int dx_m, dx_n, split;           // dx: tiles, and shares of the summed axis that a tile is cut into
-    int dw_m, dw_n;                  // dw: tiles of one of them
+    int n_blocks;                    // blocks of one d's channels
+    UnitGrid to_dx, to_dw;           // dw: of both products, one below the other
+    int dw_m;                        // tiles of one
+    bool dw_first;                   // the walk's first units are dw's (the longer ones)
     BackWalk walk;
     void *dx, *dw[2];
     long long lddx, lddw[2];
@@ -28,16 +41,30 @@ struct BackArgs {
     int *err;
 };
 
-// Operands as boxes of 64 x 64, outputs of 32 rows by 64; part: dx's shares, [split][M][K]
-// fp32, 32 by 32.
+// Operands as boxes of 64 x 64, outputs of 32 rows by 64; part: shares of dx, [split][M][K]
+// fp32, and of dw, [count * dw_split][N][K], 32 by 32.
 struct BackMaps {
-    CUtensorMap d[2], w[2], x, dx, dw[2], part;
+    CUtensorMap d[2], w[2], x, dx, dw[2], part[2];
 };
 cudaError_t launch_matmul_back(const BackArgs &a, const BackMaps &maps, int pairs, cudaStream_t stream);
 
-// dx from its shares (rows of `pitch` elements), added in their order.
-cudaError_t launch_back_join(const float *part, int split, int M, int K, long long pitch, void *dx, long long lddx, int dt,
-                             cudaStream_t stream);
+// Results from their shares, [split][rows][pitch] fp32 each, added in their order: up to
+// three in a launch.
+struct JoinResult {
+    const float *part;
+    void *out;
+    long long ld;
+    int rows, split;
+    bool vec;                        // rows start on 8-byte boundaries
+};
+constexpr int kJoinMost = 3;
+struct JoinArgs {
+    JoinResult result[kJoinMost];
+    int count, cols;
+    long long pitch, runs;           // of 128 columns: of a row
+    long long items[kJoinMost];      // runs up to the end of each result
+};
+cudaError_t launch_back_join(JoinArgs &a, int dt, cudaStream_t stream);
 
 // Before the products (gate_back.cu): d_g and d_u, rounded to the operands' type, and
 // sums over runs of rows where `sums` is not null: [runs][sum_pitch(N)] of d_g, the

@@ -22,24 +22,38 @@ struct Problem {
     float *dbias[2];
 };
 
-// How many shares dx's units are cut into.  In blocks' time (0.33 us): a unit takes its
-// blocks and kUnitCost more, all units together what they take over the pairs, and each
-// share past the first is written and read again in fp32 (at about 5 TB/s from L2).
-// Fewer shares where it makes no difference.  100 x 4096 x 4096: 30.1 us whole, 25.7 in 2,
-// 25.3 in 4, 27.4 in 8; 777 x 5001 x 1000: 43.3, 32.8, 27.5 and 36.6; 1024 x 4096 x 4096:
-// 47.0, 64, 73 and 103.  (kUnitCost 2, 4, 6, 10: 64 x 8192 x 8192 82, 60, 64 and 71 us.)
+// How many shares the units of dx and of dw are cut into along their summed axis.  In
+// blocks' time (0.33 us): a unit takes its blocks and kUnitCost more, all units together
+// what they take over the pairs, no less than the longest or the waves of the longer kind,
+// and each result's shares are written and read again in fp32 (at about 5 TB/s from L2)
+// and joined.  Fewer shares where it makes no difference.  dx, 100 x 4096 x 4096: 30.1 us
+// whole, 25.7 in 2, 25.3 in 4, 27.4 in 8; 777 x 5001 x 1000: 43.3, 32.8, 27.5 and 36.6;
+// 1024 x 4096 x 4096: 47.0, 64, 73 and 103.  (kUnitCost 2, 4, 6, 10: 64 x 8192 x 8192 82,
+// 60, 64 and 71 us.)
 constexpr int kUnitCost = 4;
-int dx_split(const Problem &p)
+struct Cut {
+    int dx, dw;
+};
+Cut cut_of(const Problem &p)
 {
-    const long long blocks = p.count * up(p.N, 64), tiles = up(p.M, 256) * up(p.K, 256);
-    const long long dw = p.count * up(p.N, 256) * up(p.K, 256) * (up(p.M, 64) + kUnitCost);
+    const long long blocks = p.count * up(p.N, 64), m_blocks = up(p.M, 64);
+    const long long tiles = up(p.M, 256) * up(p.K, 256), dw_tiles = p.count * up(p.N, 256) * up(p.K, 256);
     long long least = -1;
-    int best = 1;
-    for (int s = 1; s <= 32 && s * 4 <= blocks; ++s) {
-        const long long unit = up(blocks, s) + kUnitCost, waves = up(tiles * s, kPairs);
-        const long long walk = std::max(up(tiles * s * unit + dw, kPairs), waves * unit);
-        const long long join = s > 1 ? 8 + (2ll * s * p.M * p.K * 4) / 1650000 : 0;
-        if (least < 0 || walk + join < least) least = walk + join, best = s;
+    Cut best = {1, 1};
+    // (no more units than two waves of pairs: what is chosen from stays short, it is done twice a call)
+    for (int t : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        if (t > 1 && (t * 4 > m_blocks || t * dw_tiles > 2 * kPairs)) break;
+        for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (s > 1 && (s * 4 > blocks || s * tiles > 2 * kPairs)) break;
+            const long long unit = up(blocks, s) + kUnitCost, dw_unit = up(m_blocks, t) + kUnitCost;
+            const long long waves = unit >= dw_unit ? up(tiles * s, kPairs) * unit : up(dw_tiles * t, kPairs) * dw_unit;
+            const long long walk = std::max(up(tiles * s * unit + dw_tiles * t * dw_unit, kPairs), waves);
+            long long moved = 0;
+            if (s > 1) moved += 2ll * s * p.M * p.K * 4;
+            if (t > 1) moved += 2ll * t * p.count * p.N * p.K * 4;
+            const long long cost = walk + (s > 1 || t > 1 ? 8 : 0) + moved / 1650000;
+            if (least < 0 || cost < least) least = cost, best = {s, t};
+        }
     }
     return best;
 }
@@ -56,14 +70,15 @@ int gate_runs(const Problem &p, bool vec)
 }
 
 struct Space {
-    uint64_t pitch, d, packed, part_pitch, part, sums, total;   // pitches in elements, places in bytes
-    int split, runs;
+    uint64_t pitch, d, packed, part_pitch, part, dw_part, sums, total;   // pitches in elements, places in bytes
+    int runs;
+    Cut cut;
 };
 
 Space space_of(const Problem &p)
 {
     Space s = {};
-    s.split = dx_split(p), s.runs = std::max(gate_runs(p, false), gate_runs(p, true));
+    s.cut = cut_of(p), s.runs = std::max(gate_runs(p, false), gate_runs(p, true));
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -81,7 +96,8 @@ Space space_of(const Problem &p)
         if (!addressable(p.w[i], p.ldw[i], 2)) packed += packed_bytes(p.N, p.K, 2);
     s.packed = take(packed);
     s.part_pitch = (uint64_t)up(p.K, 4) * 4;
-    s.part = take(s.split > 1 ? (uint64_t)s.split * p.M * s.part_pitch * 4 : 0);
+    s.part = take(s.cut.dx > 1 ? (uint64_t)s.cut.dx * p.M * s.part_pitch * 4 : 0);
+    s.dw_part = take(s.cut.dw > 1 ? (uint64_t)s.cut.dw * p.count * p.N * s.part_pitch * 4 : 0);
     // (whether there are biases, and how they lie, is not known to who asks for the size)
     s.sums = take((uint64_t)p.count * s.runs * sum_pitch(p.N) * 4);
     s.total = at;
@@ -92,13 +108,18 @@ bool sizes_fit(const Problem &p) { return p.M <= kMaxSize && p.N <= kMaxSize && 
 
 bool reach(const void *p, long long ld, long long cols) { return p && ld >= cols && on_grid(p, 0, 1, 2); }
 
-// dx's shares as boxes of 32 rows by 128 bytes.
-bool part_map(CUtensorMap *map, const void *p, const Problem &a, const Space &s)
+// Shares, [count][rows][K], as boxes of 32 rows by 128 bytes.
+bool part_map(CUtensorMap *map, const void *p, int count, int rows, int K, const Space &s)
 {
-    const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.M, (uint64_t)s.split};
-    const uint64_t strides[2] = {s.part_pitch * 4, s.part_pitch * 4 * (uint64_t)a.M};
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)rows, (uint64_t)count};
+    const uint64_t strides[2] = {s.part_pitch * 4, s.part_pitch * 4 * (uint64_t)rows};
     const uint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+JoinResult join_result(const void *part, int split, int rows, void *out, long long ld)
+{
+    return {static_cast<const float *>(part), out, ld, rows, split, on_grid(out, ld, 2, 8)};
 }
 
 bigemm_status zero_gradients(const Problem &p, cudaStream_t s)
@@ -164,13 +185,18 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
 
     BackArgs a = {};
     BackMaps maps = {};
-    a.M = p.M, a.N = p.N, a.K = p.K, a.dt = p.dt, a.count = p.count, a.split = at.split;
-    a.n_blocks = (int)up(p.N, 64), a.m_blocks = (int)up(p.M, 64);
-    a.dx_m = (int)up(p.M, 256), a.dx_n = (int)up(p.K, 256), a.dw_m = (int)up(p.N, 256), a.dw_n = a.dx_n;
-    const long long dx_units = (long long)a.dx_m * a.dx_n * a.split, dw_units = (long long)p.count * a.dw_m * a.dw_n;
+    a.M = p.M, a.N = p.N, a.K = p.K, a.dt = p.dt, a.count = p.count;
+    const long long dx_m = up(p.M, 256), dw_m = up(p.N, 256), n = up(p.K, 256);
+    const long long dx_units = dx_m * n * at.cut.dx, dw_units = p.count * dw_m * n * at.cut.dw;
     if (dx_units + dw_units > 0x3fffffff) return BIGEMM_ERR_UNSUPPORTED;
+    a.n_blocks = (int)up(p.N, 64), a.dw_m = (int)dw_m;
+    a.to_dx = make_unit_grid((int)dx_m, (int)n, at.cut.dx, p.count * a.n_blocks);
+    a.to_dw = make_unit_grid((int)(p.count * dw_m), (int)n, at.cut.dw, (int)up(p.M, 64));
     const int pairs = (int)std::min<long long>(pairs_of_all, dx_units + dw_units);
-    a.walk = make_back_walk((int)dx_units, (int)dw_units, pairs, up((long long)p.count * a.n_blocks, a.split) + kUnitCost, a.m_blocks + kUnitCost);
+    const long long dx_time = up(a.to_dx.blocks, at.cut.dx) + kUnitCost, dw_time = up(a.to_dw.blocks, at.cut.dw) + kUnitCost;
+    a.dw_first = dw_time > dx_time;
+    a.walk = a.dw_first ? make_back_walk((int)dw_units, (int)dx_units, pairs, dw_time, dx_time)
+                        : make_back_walk((int)dx_units, (int)dw_units, pairs, dx_time, dw_time);
     a.dx = p.dx, a.lddx = p.lddx, a.dx_rows = addressable(p.dx, p.lddx, 2);
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
@@ -179,15 +205,23 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
         a.dw[i] = p.dw[i], a.lddw[i] = p.lddw[i], a.dw_rows[i] = addressable(p.dw[i], p.lddw[i], 2);
         ok = ok && operand_map(&maps.d[i], d[i], p.dt, p.M, p.N, ldd[i], 64) &&
              operand_map(&maps.w[i], p.w[i], p.dt, p.N, p.K, p.ldw[i], 64) &&
-             (!a.dw_rows[i] || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
+             (!a.dw_rows[i] || at.cut.dw > 1 || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
     }
-    if (a.split > 1) ok = ok && part_map(&maps.part, space + at.part, p, at);
-    else if (a.dx_rows) ok = ok && box_map(&maps.dx, p.dx, p.dt, p.M, p.K, p.lddx, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (at.cut.dx == 1 && a.dx_rows) ok = ok && box_map(&maps.dx, p.dx, p.dt, p.M, p.K, p.lddx, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    JoinArgs join = {};
+    join.cols = p.K, join.pitch = (long long)at.part_pitch;
+    if (at.cut.dx > 1) {
+        ok = ok && part_map(&maps.part[0], space + at.part, at.cut.dx, p.M, p.K, at);
+        join.result[join.count++] = join_result(space + at.part, at.cut.dx, p.M, p.dx, p.lddx);
+    }
+    if (at.cut.dw > 1) {
+        ok = ok && part_map(&maps.part[1], space + at.dw_part, p.count * at.cut.dw, p.N, p.K, at);
+        for (int i = 0; i < p.count; ++i)
+            join.result[join.count++] = join_result(space + at.dw_part + (uint64_t)i * at.cut.dw * p.N * at.part_pitch * 4, at.cut.dw,
+                                                    p.N, p.dw[i], p.lddw[i]);
+    }
     if (!ok || launch_matmul_back(a, maps, pairs, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
-    if (a.split > 1 && launch_back_join(reinterpret_cast<const float *>(space + at.part), a.split, p.M, p.K, (long long)at.part_pitch,
-                                        p.dx, p.lddx, p.dt, s) != cudaSuccess)
-        return BIGEMM_ERR_CUDA;
-    return BIGEMM_OK;
+    return join.count == 0 || launch_back_join(join, p.dt, s) == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
 }
 
 }  // namespace

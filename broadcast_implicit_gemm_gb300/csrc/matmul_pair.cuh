@@ -57,57 +57,65 @@ __device__ __forceinline__ void umma4_pair(uint32_t d, uint32_t a_lo, uint32_t b
 // groups of 8 of them 1 KB apart.  MN-major: two boxes of 64 elements, 8 KB apart.
 __device__ __forceinline__ uint32_t operand_lo(uint32_t addr, bool mn) { return desc_lo(addr, mn ? (uint32_t)PairCfg::box : 16u); }
 
-// A warp's 32 x 32 sums, a lane's row in v, to a 16-bit matrix of `rows` x `cols` whose
-// rows are off the 16-byte grid or end inside: turned round in shared memory, 16 rows
-// at a time, so that the warp's plain stores cover a row's 32 columns at once.
-__device__ __forceinline__ void put_turned(void *out, long long ld, int dt, long long rows, long long cols, uint8_t *stage,
-                                           int lane, long long m_warp, int n, const float (&v)[32])
+// A lane's 32 sums as 16 words of 16-bit values.
+__device__ __forceinline__ void words_of(const float (&v)[32], int dt, uint32_t (&w)[16])
 {
-    float *turn = reinterpret_cast<float *>(stage);
-    const bool in = n + lane < cols;
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        if (lane >> 4 == half) {
+    if (dt == BIGEMM_F16) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) turn[(lane & 15) * 32 + (i ^ (lane & 15))] = v[i];
-        }
-        __syncwarp();
-        const long long m0 = m_warp + half * 16;
-        const int count = in ? (int)max(0ll, min(16ll, rows - m0)) : 0;      // that this lane writes
-        float y[16];
+        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_F16);
+    } else {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) y[r] = turn[r * 32 + (lane ^ r)];
-        uint8_t *at = static_cast<uint8_t *>(out) + (m0 * ld + n + lane) * 2;
-        if (dt == BIGEMM_F16) store_down<__half>(at, ld * 2, count, y);
-        else store_down<__nv_bfloat16>(at, ld * 2, count, y);
-        __syncwarp();
+        for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_BF16);
     }
 }
 
-// The same to a 16-bit matrix, whole boxes on the 16-byte grid by TMA.
+// A warp's 32 rows of WORDS 32-bit words of 16-bit values, in its staging as stage_words
+// leaves them, to a matrix of `rows` x `cols` whose rows are off the 16-byte grid: a lane
+// a word of a row, which a row that starts on an odd element shifts by its neighbour's.
+// (A lane a column of 16 rows: 16 x 5632 x 7449 gradients 84 us.)
+template <int WORDS>
+__device__ __forceinline__ void put_off_grid(void *out, long long ld, long long rows, long long cols, const uint8_t *buf,
+                                             int lane, long long m_warp, int n)
+{
+    constexpr int PER = 32 / WORDS;              // rows at once
+    const int l = lane % WORDS, sub = lane / WORDS;
+    const long long c = n + 2 * l;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += PER) {
+        if (m_warp + r0 >= rows) break;
+        const int r = r0 + sub, key = WORDS == 32 ? r & 7 : (r >> 1) & 3;
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(buf + r * WORDS * 4 + (((l >> 2) ^ key) << 4) + (l & 3) * 4);
+        const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1, WORDS);
+        uint16_t *row = static_cast<uint16_t *>(out) + (m_warp + r) * ld, *at = row + c;
+        if (m_warp + r >= rows) continue;
+        if (reinterpret_cast<uintptr_t>(row) % 4 == 0) {     // (n is even)
+            if (c + 1 < cols) *reinterpret_cast<uint32_t *>(at) = w;
+            else if (c < cols) *at = (uint16_t)w;
+        } else {
+            if (l > 0 && c < cols) *reinterpret_cast<uint32_t *>(at - 1) = __funnelshift_r(before, w, 16);
+            if (l > 0 && c == cols) at[-1] = (uint16_t)(before >> 16);
+            if (l == 0 && c < cols) *at = (uint16_t)w;
+            if (l == WORDS - 1 && c + 1 < cols) at[1] = (uint16_t)(w >> 16);
+        }
+    }
+    __syncwarp();                                // before the staging is written again
+}
+
+// A warp's 32 x 32 sums, a lane's row in v, to a 16-bit matrix, on the 16-byte grid
+// (by_rows) by TMA, which leaves alone what is past the matrix.
 template <int PER_WARP>
 __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void *out, long long ld, int dt, long long rows,
                                       long long cols, uint8_t *stage, int &piece, int lane, long long m_warp, int n,
                                       const float (&v)[32])
 {
-    if (by_rows && n + 32 <= cols) {
-        uint32_t w[16];
-        if (dt == BIGEMM_F16) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_F16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = mm_pack2(v[2 * i], v[2 * i + 1], BIGEMM_BF16);
-        }
-        const uint8_t *buf = stage_words<PER_WARP, 16>(stage, piece, lane, w);
-        if (lane == 0 && m_warp < rows) {
-            tma_store_2d(map, buf, n, (int)m_warp);
-            bulk_commit();
-        }
-    } else if (n < cols) {
-        put_turned(out, ld, dt, rows, cols, stage, lane, m_warp, n, v);
+    uint32_t w[16];
+    words_of(v, dt, w);
+    const uint8_t *buf = stage_words<PER_WARP, 16>(stage, piece, lane, w);
+    if (!by_rows) {
+        put_off_grid<16>(out, ld, rows, cols, buf, lane, m_warp, n);
+    } else if (lane == 0 && m_warp < rows) {
+        tma_store_2d(map, buf, n, (int)m_warp);
+        bulk_commit();
     }
 }
 

@@ -168,6 +168,28 @@ def test_linear_backward_shares():
         linear_case(M, N, K, seed=M, bias=False)
 
 
+def test_linear_backward_shares_of_dw():
+    """Many tokens and few outputs: dw's units are cut along the tokens, alone and with dx's."""
+    for M, N, K in ((3296, 73, 288), (9000, 16, 40), (5000, 200, 513), (4096, 128, 2048), (1500, 700, 90)):
+        linear_case(M, N, K, seed=M)
+    linear_case(6000, 100, 264, "f16", pad=1)
+
+
+def test_gated_backward_shares_of_dw():
+    back_case(4608, 176, 320, "f16", "none")
+    back_case(5730, 90, 129, "bf16", "silu")
+
+
+@pytest.mark.parametrize("M", [1, 31, 33, 255])
+@pytest.mark.parametrize("N,K", [(40, 1), (31, 63), (65, 65), (100, 127), (300, 1025)])
+def test_linear_backward_off_the_grid(M, N, K):
+    """Odd rows of outputs, whole matrices and columns of wider ones."""
+    linear_case(M, N, K, "bf16", pad=0, seed=K)
+    linear_case(M, N, K, "f16", pad=3, offset=1, seed=K)
+    gated_case(M, N, K, "bf16", pad=0, seed=K)
+    gated_case(M, K, N, "f16", pad=1, offset=1, seed=K)
+
+
 def test_linear_backward_many_units():
     linear_case(3000, 2500, 1800, "bf16")
     linear_case(5000, 72, 2064, "f16")
