@@ -489,9 +489,8 @@ def _layer():
         loader = importlib.machinery.ExtensionFileLoader("_layer", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_layer", path, loader=loader))
         loader.exec_module(module)
-        module.init((torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn),
-                    (torch.uint8, torch.float8_e8m0fnu), torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _workspace,
-                    torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete,
+        module.init(_workspace, torch._C._cuda_cudaCachingAllocator_raw_alloc,
+                    torch._C._cuda_cudaCachingAllocator_raw_delete,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (lib.matmul_run, lib.matmul_mx_run, lib.rmsnorm_run, lib.mx_quantize_run,
                                     lib.matmul_workspace_bytes, lib.layernorm_run, lib.layernorm_backward_run,
@@ -573,7 +572,7 @@ def matmul(x, w, bias=None, act=ACT_NONE, other=None, combine=None, out_dtype=No
 
     `combine` is COMBINE_ADD (a residual; the default when `other` is given) or COMBINE_MUL (a gate).
     Sums in fp32; out is x's type unless out_dtype (float32, float16, bfloat16) or out says otherwise.
-    Forward only, like the calls below: the result carries no gradient.
+    The result carries no gradient, like those of the calls below; gradients are calls of their own.
     """
     if combine is None:
         combine = COMBINE_NONE if other is None else COMBINE_ADD

@@ -1,14 +1,15 @@
 """Compile the CUDA library (csrc/*.cu) into libbigemm.so, in place, for sm_103a.
 
 Each translation unit is compiled by nvcc in parallel; the objects are linked
-into one shared library next to this file, and layer_py.c is compiled into the
-extension module _layer.so beside it.  Rebuilds only when a source or a header
+into one shared library next to this file, and layer_py.c and layer_tensor.cpp
+are compiled into the extension module _layer.so beside it.  Rebuilds only when a source or a header
 is newer than the libraries.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -40,7 +41,7 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.c"))
+            + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cpp"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
@@ -64,16 +65,29 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _build_module() -> None:
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if not cc:
-        raise RuntimeError("no C compiler found: gcc is required to build _layer.so")
-    tmp = MODULE + f".tmp{os.getpid()}"
-    cmd = [cc, "-O2", "-std=c11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "layer_py.c"), "-o", tmp]
+def _run(cmd: list[str], what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed on layer_py.c:\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on {what}:\n{r.stderr}")
+
+
+def _build_module() -> None:
+    cc, cxx = shutil.which("gcc") or shutil.which("cc"), shutil.which("g++") or shutil.which("c++")
+    if not cc or not cxx:
+        raise RuntimeError("no C and C++ compiler found: gcc and g++ are required to build _layer.so")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = MODULE + f".tmp{os.getpid()}"
+    objs = [os.path.join(BUILD, n) for n in ("layer_py.o", "layer_tensor.o")]
+    common = ["-O2", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC, "-I", sysconfig.get_paths()["include"]]
+    _run([cc, "-std=c11", *common, "-c", os.path.join(CSRC, "layer_py.c"), "-o", objs[0]], "layer_py.c")
+    # (torch's own headers, whose warnings are not ours)
+    _run([cxx, "-std=c++17", *common, "-isystem", os.path.join(torch, "include"), "-isystem",
+          os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"), "-c",
+          os.path.join(CSRC, "layer_tensor.cpp"), "-o", objs[1]], "layer_tensor.cpp")
+    # torch has loaded its libraries by the time this one is
+    _run([cxx, "-shared", *objs, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+          "-lc10"], "_layer.so")
     os.replace(tmp, MODULE)
 
 

@@ -1,5 +1,5 @@
 /* layer_py.c -- the Python side of the transformer-layer calls: checks of their
- * tensors, and the call into libbigemm.
+ * tensors (layer_tensor.cpp reads them), and the call into libbigemm.
  *
  * A call for a single token runs for 2 us on the GPU; reading and checking its
  * tensors' shapes, strides, types and addresses in Python took 6 us beside the
@@ -10,13 +10,11 @@
 #include <Python.h>
 
 #include "../../include/bigemm.h"
+#include "layer_tensor.h"
 
-enum { DT_COUNT = 4, OTHER_DEVICE = -1 };
+enum { OTHER_DEVICE = -1 };
 
-static PyObject *g_dtypes[DT_COUNT];                 /* torch dtypes of F32, F16, BF16, MXF8 */
-static PyObject *g_scale_types[2];                   /* uint8, float8_e8m0fnu */
-static PyObject *g_current_stream, *g_current_device, *g_workspace, *g_alloc, *g_free;
-static PyObject *s_shape, *s_stride, *s_device, *s_ptr, *s_dtype, *s_numel, *s_contiguous;
+static PyObject *g_workspace, *g_alloc, *g_free;
 
 static bigemm_status (*p_matmul)(int, int, int, bigemm_dtype, const void *, int64_t, const void *, int64_t, const float *,
                                  int, int, bigemm_dtype, const void *, int64_t, bigemm_dtype, void *, int64_t, void *,
@@ -59,67 +57,14 @@ typedef struct {
     long device;
 } Matrix;
 
-static int as_ll(PyObject *o, long long *v)          /* steals o */
-{
-    if (!o) return -1;
-    *v = PyLong_AsLongLong(o);
-    Py_DECREF(o);
-    return *v == -1 && PyErr_Occurred() ? -1 : 0;
-}
-
-static int dtype_of(PyObject *t, const char *name, int *code)
-{
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
-    if (!d) return -1;
-    Py_DECREF(d);                    /* torch's dtypes live for ever */
-    for (int i = 0; i < DT_COUNT; ++i)
-        if (d == g_dtypes[i]) {
-            *code = i;
-            return 0;
-        }
-    PyErr_Format(PyExc_TypeError, "%s: unsupported dtype %R", name, d);
-    return -1;
-}
-
-static int device_of(PyObject *t, long *dev)
-{
-    long long v;
-    if (as_ll(PyObject_CallMethodNoArgs(t, s_device), &v) < 0) return -1;
-    *dev = (long)v;
-    return 0;
-}
-
-static int pointer_of(PyObject *t, void **p)
-{
-    PyObject *o = PyObject_CallMethodNoArgs(t, s_ptr);
-    if (!o) return -1;
-    *p = PyLong_AsVoidPtr(o);
-    Py_DECREF(o);
-    return !*p && PyErr_Occurred() ? -1 : 0;
-}
-
-/* Two integers of a shape or a stride (steals o); 1 if there are not two. */
-static int pair(PyObject *o, long long *a, long long *b)
-{
-    if (!o) return -1;
-    int r = 1;
-    if (PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 2) {
-        *a = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 0));
-        *b = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 1));
-        r = PyErr_Occurred() ? -1 : 0;
-    }
-    Py_DECREF(o);
-    return r;
-}
-
 /* A 2-D CUDA tensor with a contiguous last axis.  like: its device, and rows and
  * cols where those are not negative, have to be these. */
-static int matrix(PyObject *t, const char *name, Matrix *m, long device, long long rows, long long cols)
+static int matrix(PyObject *o, const char *name, Matrix *m, long device, long long rows, long long cols)
 {
-    long long one;
-    int r = pair(PyObject_GetAttr(t, s_shape), &m->rows, &m->cols);
-    if (r < 0 || device_of(t, &m->device) < 0) return -1;
-    if (r || m->device < 0) {
+    LayerTensor t;
+    if (layer_tensor(o, name, &t) < 0) return -1;
+    m->rows = t.size[0], m->cols = t.size[1], m->ld = t.stride[0], m->device = t.device, m->ptr = t.ptr, m->dtype = t.type;
+    if (t.dims != 2 || m->device < 0) {
         PyErr_Format(PyExc_ValueError, "%s: expected a 2-D CUDA tensor", name);
         return -1;
     }
@@ -132,12 +77,7 @@ static int matrix(PyObject *t, const char *name, Matrix *m, long device, long lo
         PyErr_Format(PyExc_ValueError, "%s: on cuda:%ld, expected cuda:%ld", name, m->device, device);
         return -1;
     }
-    r = pair(PyObject_CallMethodNoArgs(t, s_stride), &m->ld, &one);
-    if (r) {
-        if (r > 0) PyErr_Format(PyExc_ValueError, "%s: no strides", name);
-        return -1;
-    }
-    if (one != 1 && m->cols > 1) {
+    if (t.stride[1] != 1 && m->cols > 1) {
         PyErr_Format(PyExc_ValueError, "%s: the last axis must be contiguous", name);
         return -1;
     }
@@ -152,79 +92,58 @@ static int matrix(PyObject *t, const char *name, Matrix *m, long device, long lo
         PyErr_Format(PyExc_ValueError, "%s: too large", name);
         return -1;
     }
-    return dtype_of(t, name, &m->dtype) < 0 || pointer_of(t, &m->ptr) < 0 ? -1 : 0;
+    if (m->dtype < BIGEMM_F32 || m->dtype > BIGEMM_MXF8) {
+        PyObject *d = PyObject_GetAttrString(o, "dtype");
+        if (d) PyErr_Format(PyExc_TypeError, "%s: unsupported dtype %R", name, d);
+        Py_XDECREF(d);
+        return -1;
+    }
+    return 0;
 }
 
 /* The address of a float32 vector of n elements, or null for None. */
-static int vector(PyObject *t, const char *name, long long n, long device, void **p)
+static int vector(PyObject *o, const char *name, long long n, long device, void **p)
 {
+    LayerTensor t;
     *p = NULL;
-    if (t == Py_None) return 0;
-    long dev;
-    int ok = 0;
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
-    if (!d) return -1;
-    Py_DECREF(d);
-    if (device_of(t, &dev) < 0) return -1;
-    PyObject *shape = PyObject_GetAttr(t, s_shape);
-    if (!shape) return -1;
-    if (PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 1) ok = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0)) == n;
-    Py_DECREF(shape);
-    PyObject *c = PyObject_CallMethodNoArgs(t, s_contiguous);
-    if (!c) return -1;
-    ok = ok && c == Py_True && d == g_dtypes[BIGEMM_F32] && dev == device;
-    Py_DECREF(c);
-    if (!ok) {
+    if (o == Py_None) return 0;
+    if (layer_tensor(o, name, &t) < 0) return -1;
+    if (t.dims != 1 || t.size[0] != n || !t.contiguous || t.type != BIGEMM_F32 || t.device != device) {
         PyErr_Format(PyExc_ValueError, "%s: expected a contiguous float32 vector of %lld elements on cuda:%ld", name, n,
                      device);
         return -1;
     }
-    return pointer_of(t, p);
+    *p = t.ptr;
+    return 0;
 }
 
 /* The address of the scales of a rows x cols MXFP8 matrix. */
-static int scales(PyObject *t, const char *name, long long rows, long long cols, long device, void **p)
+static int scales(PyObject *o, const char *name, long long rows, long long cols, long device, void **p)
 {
-    long dev;
-    long long n;
+    LayerTensor t;
     const long long a = (rows + 127) / 128, b = (cols + 127) / 128;
-    if (t == Py_None) {
+    if (o == Py_None) {
         PyErr_Format(PyExc_ValueError, "%s: missing", name);
         return -1;
     }
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
-    if (!d) return -1;
-    Py_DECREF(d);
-    if (device_of(t, &dev) < 0 || as_ll(PyObject_CallMethodNoArgs(t, s_numel), &n) < 0) return -1;
-    PyObject *c = PyObject_CallMethodNoArgs(t, s_contiguous);
-    if (!c) return -1;
-    const int ok = c == Py_True && dev == device && n == a * b * 512 && (d == g_scale_types[0] || d == g_scale_types[1]);
-    Py_DECREF(c);
-    if (!ok) {
+    if (layer_tensor(o, name, &t) < 0) return -1;
+    if (!t.contiguous || t.device != device || t.numel != a * b * 512 || (t.type != TYPE_SCALE_U8 && t.type != TYPE_SCALE_E8M0)) {
         PyErr_Format(PyExc_ValueError, "%s: expected contiguous scales of shape (%lld, %lld, 32, 4, 4) on cuda:%ld", name, a, b,
                      device);
         return -1;
     }
-    return pointer_of(t, p);
+    *p = t.ptr;
+    return 0;
 }
 
 /* The stream to use, as an address; 1 if another device than `device` is current. */
 static int stream_on(PyObject *s, long device, void **stream)
 {
-    long long current;
-    if (as_ll(PyObject_CallNoArgs(g_current_device), &current) < 0) return -1;
+    long current;
+    if (layer_current(device, &current, stream) < 0) return -1;
     if (current != device) return 1;
-    PyObject *o;
-    if (s == Py_None) {
-        PyObject *d = PyLong_FromLong(device);
-        if (!d) return -1;
-        o = PyObject_CallOneArg(g_current_stream, d);
-        Py_DECREF(d);
-    } else if (PyLong_Check(s)) {
-        o = Py_NewRef(s);
-    } else {
-        o = PyObject_GetAttrString(s, "cuda_stream");
-    }
+    if (s == Py_None) return 0;
+    PyObject *o = PyLong_Check(s) ? Py_NewRef(s) : PyObject_GetAttrString(s, "cuda_stream");
     if (!o) return -1;
     *stream = PyLong_AsVoidPtr(o);
     Py_DECREF(o);
@@ -262,10 +181,12 @@ static int space_for(uint64_t bytes, PyObject *t, PyObject *s, void *stream, Spa
     space->tensor = PyObject_Vectorcall(g_workspace, args, 3, NULL);
     Py_DECREF(b);
     if (!space->tensor) return -1;
-    if (pointer_of(space->tensor, &space->ptr) < 0) {
+    LayerTensor made;
+    if (layer_tensor(space->tensor, "workspace", &made) < 0) {
         Py_CLEAR(space->tensor);
         return -1;
     }
+    space->ptr = made.ptr;
     return 0;
 }
 
@@ -544,28 +465,19 @@ static PyObject *gated_backward(PyObject *self, PyObject *const *a, Py_ssize_t n
     return done(&space, st);
 }
 
-/* init(dtypes, scale_types, current_stream, current_device, workspace, alloc, free, functions): workspace(bytes, tensor,
- * stream) makes a tensor, alloc(bytes, stream) an address for free */
+/* init(workspace, alloc, free, functions): workspace(bytes, tensor, stream) makes a tensor, alloc(bytes, stream) an
+ * address for free */
 static PyObject *init(PyObject *self, PyObject *args)
 {
-    PyObject *d, *st, *cs, *cd, *ws, *al, *fr;
-    PyObject *functions;
+    PyObject *ws, *al, *fr, *functions;
     enum { COUNT = 15 };
     unsigned long long f[COUNT];
-    if (!PyArg_ParseTuple(args, "O!O!OOOOOO!", &PyTuple_Type, &d, &PyTuple_Type, &st, &cs, &cd, &ws, &al, &fr, &PyTuple_Type,
-                          &functions))
-        return NULL;
+    if (!PyArg_ParseTuple(args, "OOOO!", &ws, &al, &fr, &PyTuple_Type, &functions)) return NULL;
     if (PyTuple_GET_SIZE(functions) != COUNT) return PyErr_Format(PyExc_ValueError, "init: wrong number of functions");
     for (int i = 0; i < COUNT; ++i) {
         f[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(functions, i));
         if (PyErr_Occurred()) return NULL;
     }
-    if (PyTuple_GET_SIZE(d) != DT_COUNT || PyTuple_GET_SIZE(st) != 2)
-        return PyErr_Format(PyExc_ValueError, "init: wrong number of dtypes");
-    for (int i = 0; i < DT_COUNT; ++i) g_dtypes[i] = Py_NewRef(PyTuple_GET_ITEM(d, i));
-    for (int i = 0; i < 2; ++i) g_scale_types[i] = Py_NewRef(PyTuple_GET_ITEM(st, i));
-    g_current_stream = Py_NewRef(cs);
-    g_current_device = Py_NewRef(cd);
     g_workspace = Py_NewRef(ws);
     g_alloc = Py_NewRef(al);
     g_free = Py_NewRef(fr);
@@ -601,15 +513,4 @@ static PyMethodDef methods[] = {
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit__layer(void)
-{
-    s_shape = PyUnicode_InternFromString("shape");
-    s_stride = PyUnicode_InternFromString("stride");
-    s_device = PyUnicode_InternFromString("get_device");
-    s_ptr = PyUnicode_InternFromString("data_ptr");
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_numel = PyUnicode_InternFromString("numel");
-    s_contiguous = PyUnicode_InternFromString("is_contiguous");
-    if (!s_shape || !s_stride || !s_device || !s_ptr || !s_dtype || !s_numel || !s_contiguous) return NULL;
-    return PyModule_Create(&module);
-}
+PyMODINIT_FUNC PyInit__layer(void) { return PyModule_Create(&module); }

@@ -163,3 +163,21 @@ def test_python_refusals_of_products():
                  lambda: bg.matmul_gated_backward(d, x, w, w, d, d)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_what_is_no_tensor_or_has_no_memory():
+    """Errors are Python's, also where torch's C++ side throws: a fake tensor has no address."""
+    x = torch.zeros(4, 16, dtype=torch.float16)
+    for bad in (None, 3, [1.0], "x"):
+        with pytest.raises((TypeError, AttributeError)):
+            bg.matmul(bad, x, out=x)
+        with pytest.raises(TypeError, match="expected a tensor"):
+            bg._layer().gated(bad, x, x, None, None, 0, x, None, None, None)
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        fake = torch.empty((4, 16), dtype=torch.float16, device="cuda")
+        with pytest.raises((RuntimeError, ValueError)):
+            bg.matmul(fake, fake, out=fake)
+    for t in (torch.zeros(4, dtype=torch.float16), torch.zeros(2, 2, 2), torch.zeros(())):
+        with pytest.raises(ValueError, match="2-D CUDA"):
+            bg._layer().quantize(t, t, t, None)
