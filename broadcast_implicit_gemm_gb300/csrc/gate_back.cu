@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256, kGateBeside(VEC)) gate_back_kernel(const 
     float sg[SUMS ? kPiece : 1], su[SUMS && GATED ? kPiece : 1];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) sg[SUMS ? i : 0] = 0.f, su[SUMS && GATED ? i : 0] = 0.f;
-        constexpr int U = !GATED ? (VEC ? 8 : 4) : VEC ? 2 : 1;       // rows whose loads leave together
+    constexpr int U = !GATED ? (VEC ? 8 : 4) : VEC ? 2 : 1;       // rows whose loads leave together
     for (long long r = r0 + warp; r < r1; r += 8 * U) {
         GateRaw<T, VEC> d[U], g[GATED ? U : 1], u[GATED ? U : 1];
 #pragma unroll

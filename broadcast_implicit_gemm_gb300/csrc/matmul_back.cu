@@ -49,6 +49,33 @@ struct BackJob {
         return true;
     }
 
+    // Sums of dout's columns over a few tokens, 32 columns a turn, sixteen rows in flight.
+    static __device__ __forceinline__ void beside(const Args &p, int i, int count, int lane)
+    {
+        if (!p.sums) return;
+        if (p.dt == BIGEMM_F16) sums_of<__half>(p, i, count, lane);
+        else sums_of<__nv_bfloat16>(p, i, count, lane);
+    }
+
+    template <typename T>
+    static __device__ __forceinline__ void sums_of(const Args &p, int i, int count, int lane)
+    {
+        for (long long c = i * 32ll + lane; c < p.N; c += count * 32ll) {
+            const T *at = static_cast<const T *>(p.dout) + c;
+            float v = 0.f;
+            for (int r = 0; r < p.M; r += 16, at += 16 * p.ldd) {
+                T row[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (r + k < p.M) row[k] = at[k * p.ldd];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (r + k < p.M) v += (float)row[k];
+            }
+            p.sums[c] = v;
+        }
+    }
+
     // Tile and share of a result's unit, in tile_in's order.
     static __device__ __forceinline__ Tile place(const UnitGrid &g, int i, Unit &u)
     {
@@ -192,15 +219,15 @@ __global__ void __launch_bounds__(256) back_join_kernel(const JoinArgs a)
     }
     // one of each 32 a lane
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < o.split; s += 2) {
-        float w[2][4];
+    for (int s = 0; s < o.split; s += 8) {
+        float w[8][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 w[i][j] = s + i < o.split && k0 + j * 32 + lane < a.cols ? from[(s + i) * step + j * 32 + lane] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += w[i][j];
     }

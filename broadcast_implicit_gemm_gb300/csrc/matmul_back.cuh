@@ -37,6 +37,9 @@ struct BackArgs {
     void *dx, *dw[2];
     long long lddx, lddw[2];
     bool dx_rows, dw_rows[2];        // by TMA
+    const void *dout;                // sums of its columns go to `sums`, if that is not null
+    long long ldd;
+    float *sums;
     unsigned long long timeout_ns;
     int *err;
 };
@@ -69,7 +72,11 @@ cudaError_t launch_back_join(JoinArgs &a, int dt, cudaStream_t stream);
 // Before the products (gate_back.cu): d_g and d_u, rounded to the operands' type, and
 // sums over runs of rows where `sums` is not null: [runs][sum_pitch(N)] of d_g, the
 // same of d_u.
-// Or, for a plain product, the sums of d alone.
+// Or, for a plain product of more than kSumsBeside tokens, the sums of d alone.  Those of
+// fewer are taken by two warps of each block that the products leave idle, a column a lane
+// (100 x 4096 x 4096 f16 30 us with a launch for them, 23.7 so; 64 x 4096 x 256 9.7 and 8.0,
+// 128 x 4096 x 256 11.6 and 9.5, 7.5 to 9.1 without sums; more rows take those warps longer
+// than the launch: 256 x 4096 x 256 12.8 in a launch, 24 beside).
 struct GateBackArgs {
     int M, N, runs;
     int act;                         // -1: sums of dout alone
@@ -78,6 +85,7 @@ struct GateBackArgs {
     void *dg, *du;                   // rows of `pitch` elements, on the 16-byte grid
     float *sums[2];
 };
+constexpr int kSumsBeside = 128;
 constexpr int kGateColumns = 256;    // of a block
 constexpr int kGateBeside(bool vec) { return vec ? 2 : 3; }      // blocks that an SM's registers hold
 cudaError_t launch_gate_back(const GateBackArgs &a, int dt, bool vec, cudaStream_t stream);

@@ -59,11 +59,9 @@ Cut cut_of(const Problem &p)
 }
 
 // Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least, and
-// no second wave that is not a whole one (777 x 5001: 22 runs, not 25).  The sums of few
-// tokens of a plain product are a single run's, which needs no second launch.
+// no second wave that is not a whole one (777 x 5001: 22 runs, not 25).
 int gate_runs(const Problem &p, bool vec)
 {
-    if (p.count == 1 && p.M <= 512) return 1;
     const long long across = up(p.N, kGateColumns), wave = 2ll * kPairs * kGateBeside(vec);
     const long long want = std::min(std::max<long long>(1, 8 * 2 * kPairs / across), up(p.M, 32));
     return (int)(want * across > wave && want * across < 2 * wave && across <= wave ? wave / across : want);
@@ -169,8 +167,9 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
         g.dg = space + at.d, g.du = space + at.d + at.pitch * (uint64_t)p.M * 2;
         d[0] = g.dg, d[1] = g.du, ldd[0] = ldd[1] = g.pitch;
     }
-    if ((p.count == 2 || biases) && launch_gate_back(g, p.dt, vec, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
-    if (biases && g.runs > 1) {
+    const bool beside = p.count == 1 && p.M <= kSumsBeside;
+    if ((p.count == 2 || (biases && !beside)) && launch_gate_back(g, p.dt, vec, s) != cudaSuccess) return BIGEMM_ERR_CUDA;
+    if (biases && !beside && g.runs > 1) {
         ColumnSums c = {};
         c.parts = g.runs, c.cols = p.N;
         for (int i = 0; i < p.count; ++i)
@@ -198,6 +197,7 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     a.walk = a.dw_first ? make_back_walk((int)dw_units, (int)dx_units, pairs, dw_time, dx_time)
                         : make_back_walk((int)dx_units, (int)dw_units, pairs, dx_time, dw_time);
     a.dx = p.dx, a.lddx = p.lddx, a.dx_rows = addressable(p.dx, p.lddx, 2);
+    if (beside) a.dout = p.dout, a.ldd = p.ldd, a.sums = p.dbias[0];
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
     bool ok = operand_map(&maps.x, p.x, p.dt, p.M, p.K, p.ldx, 64);

@@ -33,6 +33,8 @@ struct GatedJob {
         return true;
     }
 
+    static __device__ __forceinline__ void beside(const Args &, int, int, int) {}
+
     static __device__ __forceinline__ void load(const Maps &maps, const Args &, const Unit &u, int kb, int rank, uint8_t *sa,
                                                 uint8_t *sb, uint32_t bar)
     {

@@ -125,6 +125,7 @@ __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void
 //   static bool unit(p, turn, pair, pairs, Unit &)   the pair's unit of this turn; false: none left
 //   static void load(maps, p, u, kb, rank, sa, sb, bar)   this CTA's 2 x 16 KB of a block, counted on bar
 //   static void mma(p, u, d, a, b, accum)   a block's MMAs from shared addresses a and b
+//   static void beside(p, i, count, lane)   what one of the `count` warps does that are left over
 //   static void drain(maps, p, u, rank, q, h, tmem, stage, piece, lane)   a warp's 32 rows (q of 4)
 //       by 64 columns (h of 4) of this CTA's sums, at tensor-memory address tmem (of the quarter's lanes, column 0)
 template <class Job>
@@ -234,6 +235,8 @@ __global__ void __launch_bounds__(PairCfg::threads, 1)
                     mbar_wait(drain, 0, p.timeout_ns, &local_abort, p.err);
                 }
             }
+        } else {
+            Job::beside(p, (int)blockIdx.x * 2 + warp - 2, 2 * (int)gridDim.x, lane);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::drain_regs));
