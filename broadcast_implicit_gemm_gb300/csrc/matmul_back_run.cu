@@ -29,8 +29,10 @@ struct Problem {
 // and joined.  Fewer shares where it makes no difference.  dx, 100 x 4096 x 4096: 30.1 us
 // whole, 25.7 in 2, 25.3 in 4, 27.4 in 8; 777 x 5001 x 1000: 43.3, 32.8, 27.5 and 36.6;
 // 1024 x 4096 x 4096: 47.0, 64, 73 and 103.  (kUnitCost 2, 4, 6, 10: 64 x 8192 x 8192 82,
-// 60, 64 and 71 us.)
-constexpr int kUnitCost = 4;
+// 60, 64 and 71 us.)  A dw unit whose rows are off the 16-byte grid, written by plain
+// stores, counts kOffGridCost when the pairs share the units out (4, 6, 8, 12, 16:
+// 32 x 8782 x 1845 52, 42, 42, 42 and 44; 103 x 9152 x 12238 246, 228, 218, 226 and 228).
+constexpr int kUnitCost = 4, kOffGridCost = 8;
 struct Cut {
     int dx, dw;
 };
@@ -192,7 +194,13 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     a.to_dx = make_unit_grid((int)dx_m, (int)n, at.cut.dx, p.count * a.n_blocks);
     a.to_dw = make_unit_grid((int)(p.count * dw_m), (int)n, at.cut.dw, (int)up(p.M, 64));
     const int pairs = (int)std::min<long long>(pairs_of_all, dx_units + dw_units);
-    const long long dx_time = up(a.to_dx.blocks, at.cut.dx) + kUnitCost, dw_time = up(a.to_dw.blocks, at.cut.dw) + kUnitCost;
+    bool dw_grid = true;
+    for (int i = 0; i < p.count; ++i) {
+        a.dw[i] = p.dw[i], a.lddw[i] = p.lddw[i], a.dw_rows[i] = addressable(p.dw[i], p.lddw[i], 2);
+        dw_grid = dw_grid && (a.dw_rows[i] || at.cut.dw > 1);    // (shares are on the grid)
+    }
+    const long long dx_time = up(a.to_dx.blocks, at.cut.dx) + kUnitCost;
+    const long long dw_time = up(a.to_dw.blocks, at.cut.dw) + (dw_grid ? kUnitCost : kOffGridCost);
     a.dw_first = dw_time > dx_time;
     a.walk = a.dw_first ? make_back_walk((int)dw_units, (int)dx_units, pairs, dw_time, dx_time)
                         : make_back_walk((int)dx_units, (int)dw_units, pairs, dx_time, dw_time);
@@ -202,7 +210,6 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     a.err = ds->err;
     bool ok = operand_map(&maps.x, p.x, p.dt, p.M, p.K, p.ldx, 64);
     for (int i = 0; i < p.count; ++i) {
-        a.dw[i] = p.dw[i], a.lddw[i] = p.lddw[i], a.dw_rows[i] = addressable(p.dw[i], p.lddw[i], 2);
         ok = ok && operand_map(&maps.d[i], d[i], p.dt, p.M, p.N, ldd[i], 64) &&
              operand_map(&maps.w[i], p.w[i], p.dt, p.N, p.K, p.ldw[i], 64) &&
              (!a.dw_rows[i] || at.cut.dw > 1 || box_map(&maps.dw[i], p.dw[i], p.dt, p.N, p.K, p.lddw[i], 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
