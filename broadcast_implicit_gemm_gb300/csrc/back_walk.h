@@ -4,7 +4,7 @@
 // There are long units, 0 to dx - 1, and short ones, dx to dx + dw - 1 (where dw's units
 // are the longer ones they come first).  The pairs take the long ones in turn; the `late`
 // ones that get one fewer take `ahead` short units each meanwhile, and then all walk the
-// rest in turn.
+// rest in turn, the late ones first: each unit goes to the pair that is free first.
 //
 // No CUDA dependency on the host side, so that a plain C++ test can check it.
 #pragma once
@@ -45,9 +45,10 @@ BIGEMM_BW_HD int back_unit(const BackWalk &w, int turn, int pair, int pairs)
     int k;
     if (pair >= first && j < w.ahead) {
         k = j * w.late + (pair - first);
+    } else if (pair >= first) {
+        k = w.ahead * w.late + (j - w.ahead) * pairs + (pair - first);
     } else {
-        if (pair >= first) j -= w.ahead;
-        k = w.ahead * w.late + j * pairs + pair;
+        k = w.ahead * w.late + j * pairs + w.late + pair;
     }
     return k < w.dw ? w.dx + k : -1;
 }

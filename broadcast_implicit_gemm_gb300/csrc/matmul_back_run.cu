@@ -26,13 +26,14 @@ struct Problem {
 // blocks' time (0.33 us): a unit takes its blocks and kUnitCost more, all units together
 // what they take over the pairs, no less than the longest or the waves of the longer kind,
 // and each result's shares are written and read again in fp32 (at about 5 TB/s from L2)
-// and joined.  Fewer shares where it makes no difference.  dx, 100 x 4096 x 4096: 30.1 us
-// whole, 25.7 in 2, 25.3 in 4, 27.4 in 8; 777 x 5001 x 1000: 43.3, 32.8, 27.5 and 36.6;
-// 1024 x 4096 x 4096: 47.0, 64, 73 and 103.  (kUnitCost 2, 4, 6, 10: 64 x 8192 x 8192 82,
-// 60, 64 and 71 us.)  A dw unit whose rows are off the 16-byte grid, written by plain
-// stores, counts kOffGridCost when the pairs share the units out (4, 6, 8, 12, 16:
-// 32 x 8782 x 1845 52, 42, 42, 42 and 44; 103 x 9152 x 12238 246, 228, 218, 226 and 228).
-constexpr int kUnitCost = 4, kOffGridCost = 8;
+// and joined.  Fewer shares where it makes no difference.  dx, 100 x 4096 x 4096: 26.9 us
+// whole, 21.3 in 2, 22.8 in 4, 24.6 in 8; 777 x 5001 x 1000: 37.2, 27.5, 27.3 and 30.8;
+// 1024 x 4096 x 4096: 45.1 whole, 62.3 in 2.  dw, 8192 x 512 x 512: 40.2 whole, 18.1 in 4,
+// 15.4 in 8, 18.5 in 16.  (kUnitCost 4, 5, 6: 1 x 4096 x 4096 25.1, 21.6, 21.7 us;
+// 64 x 8192 x 8192 57.4, 58.7, 60.8.)  A dw unit whose rows are off the 16-byte grid, written
+// by plain stores, counts kOffGridCost when the pairs share the units out (5, 10, 14, 20, 32:
+// 32 x 8782 x 1845 51, 47, 42, 42 and 42; 16 x 5632 x 7449 109, 95, 94, 97 and 103).
+constexpr int kUnitCost = 5, kOffGridCost = 14;
 struct Cut {
     int dx, dw;
 };

@@ -36,7 +36,7 @@ int main()
         }
         for (int u = 0; u < dx + dw; ++u)
             if (seen[u] != 1) return printf("%d %d %d: unit %d %d times\n", dx, dw, pairs, u, seen[u]), 1;
-        if (longest > all / pairs + 2 * one) return printf("%d %d %d: %lld of %lld\n", dx, dw, pairs, longest, all / pairs), 1;
+        if (longest > all / pairs + one) return printf("%d %d %d: %lld of %lld\n", dx, dw, pairs, longest, all / pairs), 1;
     }
     printf("ok\n");
     return 0;
