@@ -2,8 +2,8 @@
 
 Each translation unit is compiled by nvcc in parallel; the objects are linked
 into one shared library next to this file, and layer_py.c and layer_tensor.cpp
-are compiled into the extension module _layer.so beside it.  Rebuilds only when a source or a header
-is newer than the libraries.
+are compiled into the extension module _layer.so beside it.  Rebuilds only when
+a source or a header is newer than the libraries.
 """
 from __future__ import annotations
 
