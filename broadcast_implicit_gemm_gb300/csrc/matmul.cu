@@ -59,7 +59,11 @@ struct Choice {
 // Weights that fill the machine come at 6.8 TB/s: 1 x 4096 x 4096 in 8: 8.1 us.
 // Rows of the output or of other off the 16-byte grid go element by element, 60
 // ns a token (777 x 5001 x 1000: 34 us, 128 tokens to a tile).
-// GATED: tiles of 64 channels, and twice the weights.
+// GATED: tiles of 64 channels, and twice the weights.  Its terms were fitted to every cut of
+// 99 gated layers (1 to 1024 tokens, 256 to 14336 channels): a block in 0.2 us, rows at 1.3 ns,
+// 7, 15 and 4 ns for the others.  What is chosen takes 1.3 % more than the least of them in
+// the mean (5.2 with the terms above: 16 x 2048 -> 2048 6.2 us with K in 8, 5.1 in 4;
+// 256 x 1000 -> 1000 8.2 in tiles of 32, 6.8 of 64).
 template <bool GATED>
 long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 {
@@ -67,8 +71,10 @@ long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
     const long long beside = c.alone ? 1 : std::min<long long>(2, up(grid, sms)), waves = up(grid, beside * sms);
     const long long mine = up(std::min(a.M, c.bn), c.split);
     const bool ragged = !a.vec_out || (a.combine != BIGEMM_COMBINE_NONE && !a.vec_other);
-    const long long one = up(a.k_blocks, c.split) * std::max<long long>(165, beside * (128 + c.bn)) + 23 * mine + 22 * c.bn +
-                          2 * (c.split - 1) * beside * c.bn + (ragged ? 60 * mine * beside : 0);
+    const long long block = GATED ? std::max<long long>(200, beside * (128 + c.bn) * 13 / 10)
+                                  : std::max<long long>(165, beside * (128 + c.bn));
+    const long long one = up(a.k_blocks, c.split) * block + (GATED ? 7 : 23) * mine + (GATED ? 15 : 22) * c.bn +
+                          (GATED ? 4 : 2) * (c.split - 1) * beside * c.bn + (ragged ? 60 * mine * beside : 0);
     const long long memory = (long long)a.k_blocks * kRow * a.N * (GATED ? 2 : 1) / 6800;
     return 3600 + std::max(memory, waves * one);
 }
@@ -77,12 +83,13 @@ long long few_cost(const MatmulArgs &a, int sms, const FewCut &c)
 // and block of K 0.33 us at 256 channels and 0.26 at 128 (where shared memory,
 // not the tensor core, sets the pace), with MXFP8 operands 0.44 and 0.36.
 // 4096 x 4096 x 4096 bf16: 79.6 us in 4 waves of 256, 110 in 7 of 128; 512 x 4096
-// x 4096 24.7 in one wave of 256, 20.9 in one of 128.
-long long many_cost(const MatmulArgs &a, int sms, int bn, int channels)
+// x 4096 24.7 in one wave of 256, 20.9 in one of 128.  A gated tile's end takes 3.1 us
+// longer (256 x 256 -> 704 6.5 us, 4.2 for few tokens; 400 x 1000 -> 1000 11.5 and 8.5).
+long long many_cost(const MatmulArgs &a, int sms, int bn, int channels, bool gated)
 {
     const long long waves = up(up(a.M, kManyTokens) * up(a.N, channels), sms / 2);
     const bool mx = a.in_dt == BIGEMM_MXF8;
-    return 3500 + waves * a.k_blocks * (bn == 256 ? (mx ? 440 : 330) : (mx ? 360 : 260));
+    return (gated ? 6600 : 3500) + waves * a.k_blocks * (bn == 256 ? (mx ? 440 : 330) : (mx ? 360 : 260));
 }
 
 // 256 x 4096 x 4096 bf16: 17.9 us for few (64 tokens, K in 2) against 20.4 and
@@ -105,7 +112,10 @@ Choice choose(const MatmulArgs &a, int sms)
         // 7, 8.9 in 4)
         for (int split : {1, 2, 3, 4, 8}) {
             if (split > 1 && (split * 4 > a.k_blocks || tiles * split > 2ll * sms)) break;
-            for (int alone = 0; alone <= (bn >= 64 && tiles * split <= sms ? 1 : 0); ++alone) {
+            // clusters of 3 and 8 CTAs that want an SM each do not fit the machine's groups of SMs (gated,
+            // 80 x 3000 -> 3000 in 3: 20.0 us, 15.7 beside each other; 128 CTAs in 8: 1.3 to 1.6 times as long)
+            const bool fits = split == 1 || split == 2 || split == 4;
+            for (int alone = 0; alone <= (bn >= 64 && fits && tiles * split <= sms ? 1 : 0); ++alone) {
                 const FewCut cut = {bn, split, alone != 0};
                 const long long cost = few_cost<GATED>(a, sms, cut);
                 if (least < 0 || cost <= least) c.few = cut, least = cost;
@@ -115,7 +125,7 @@ Choice choose(const MatmulArgs &a, int sms)
     }
     if (a.M > 128)
         for (int bn = GATED ? 256 : 128; bn <= 256; bn += 128) {
-            const long long cost = many_cost(a, sms, bn, GATED ? bn / 2 : bn);
+            const long long cost = many_cost(a, sms, bn, GATED ? bn / 2 : bn, GATED);
             if (least < 0 || cost < least) c.many = true, c.bn = bn, least = cost;
         }
     return c;
