@@ -61,12 +61,16 @@ Cut cut_of(const Problem &p)
     return best;
 }
 
-// Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least, and
+// Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least (16
+// without sums, which its warps have in flight at once, where that makes less than two
+// waves: gated, 64 x 256 -> 704 11.8 us with 32, 10.3 with 16; 1024 x 1024 -> 2816 31.0 and
+// 31.9), and
 // no second wave that is not a whole one (777 x 5001: 22 runs, not 25).
-int gate_runs(const Problem &p, bool vec)
+int gate_runs(const Problem &p, bool vec, bool sums)
 {
     const long long across = up(p.N, kGateColumns), wave = 2ll * kPairs * kGateBeside(vec);
-    const long long want = std::min(std::max<long long>(1, 8 * 2 * kPairs / across), up(p.M, 32));
+    const int rows = !sums && up(p.M, 16) * across < 2 * wave ? 16 : 32;
+    const long long want = std::min(std::max<long long>(1, 8 * 2 * kPairs / across), up(p.M, rows));
     return (int)(want * across > wave && want * across < 2 * wave && across <= wave ? wave / across : want);
 }
 
@@ -79,7 +83,7 @@ struct Space {
 Space space_of(const Problem &p)
 {
     Space s = {};
-    s.cut = cut_of(p), s.runs = std::max(gate_runs(p, false), gate_runs(p, true));
+    s.cut = cut_of(p), s.runs = std::max(gate_runs(p, false, true), gate_runs(p, true, true));
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -158,13 +162,13 @@ bigemm_status gradients(Problem &p, void *workspace, uint64_t bytes, void *strea
     const void *d[2] = {p.dout, nullptr};
     long long ldd[2] = {p.ldd, 0};
     GateBackArgs g = {};
+    const bool biases = p.dbias[0] || p.dbias[1];
     const bool vec = on_grid(p.dout, p.ldd, 2, 16) && (p.count == 1 || (on_grid(p.gate, p.ldg, 2, 16) && on_grid(p.up, p.ldu, 2, 16)));
-    g.M = p.M, g.N = p.N, g.runs = gate_runs(p, vec), g.act = -1;
+    g.M = p.M, g.N = p.N, g.runs = gate_runs(p, vec, biases), g.act = -1;
     g.dout = p.dout, g.gate = p.gate, g.up = p.up, g.ldd = p.ldd, g.ldg = p.ldg, g.ldu = p.ldu;
     float *sums = reinterpret_cast<float *>(space + at.sums);
     for (int i = 0; i < p.count; ++i)        // (a single run's sums are the result)
         g.sums[i] = p.dbias[i] && g.runs > 1 ? sums + i * g.runs * sum_pitch(p.N) : p.dbias[i];
-    const bool biases = p.dbias[0] || p.dbias[1];
     if (p.count == 2) {
         g.act = p.act, g.pitch = (long long)at.pitch;
         g.dg = space + at.d, g.du = space + at.d + at.pitch * (uint64_t)p.M * 2;
