@@ -74,9 +74,9 @@ cudaError_t launch_back_join(JoinArgs &a, int dt, cudaStream_t stream);
 // same of d_u.
 // Or, for a plain product of more than kSumsBeside tokens, the sums of d alone.  Those of
 // fewer are taken by two warps of each block that the products leave idle, a column a lane
-// (100 x 4096 x 4096 f16 30 us with a launch for them, 23.7 so; 64 x 4096 x 256 9.7 and 8.0,
-// 128 x 4096 x 256 11.6 and 9.5, 7.5 to 9.1 without sums; more rows take those warps longer
-// than the launch: 256 x 4096 x 256 12.8 in a launch, 24 beside).
+// (100 x 4096 x 4096 f16 21.4 us, 21.3 without sums, 6 more with a launch for them;
+// 64 x 4096 x 256 8.0, 7.9 and 9.7; 128 x 4096 x 256 9.5, 9.1 and 11.6; more rows take
+// those warps longer than the launch: 256 x 4096 x 256 12.8 in a launch, 24 beside).
 struct GateBackArgs {
     int M, N, runs;
     int act;                         // -1: sums of dout alone

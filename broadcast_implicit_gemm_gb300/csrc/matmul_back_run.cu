@@ -61,11 +61,10 @@ Cut cut_of(const Problem &p)
     return best;
 }
 
-// Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least (16
-// without sums, which its warps have in flight at once, where that makes less than two
-// waves: gated, 64 x 256 -> 704 11.8 us with 32, 10.3 with 16; 1024 x 1024 -> 2816 31.0 and
-// 31.9), and
-// no second wave that is not a whole one (777 x 5001: 22 runs, not 25).
+// Runs of rows of the elementwise kernel: eight blocks per SM, of 32 rows at least, and
+// no second wave that is not a whole one (777 x 5001: 22 runs, not 25).  Without sums 16
+// rows, which a block's warps have in flight at once, where those make less than two waves
+// (gated, 64 x 256 -> 704: 11.8 us with 32, 10.3 with 16; 1024 x 1024 -> 2816 31.0 and 31.9).
 int gate_runs(const Problem &p, bool vec, bool sums)
 {
     const long long across = up(p.N, kGateColumns), wave = 2ll * kPairs * kGateBeside(vec);
