@@ -35,6 +35,10 @@ int layer_tensor(PyObject *o, const char *name, LayerTensor *out)
     // (a tensor without memory of its own, a fake one for instance, throws)
     try {
         const at::Tensor &t = THPVariable_Unpack(o);
+        if (t.is_neg()) {
+            PyErr_Format(PyExc_ValueError, "%s: its values are still to be negated (resolve_neg does it)", name);
+            return -1;
+        }
         out->dims = (int)t.dim();
         const at::IntArrayRef size = t.sizes(), stride = t.strides();
         for (int i = 0; i < 2; ++i) {

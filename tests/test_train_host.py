@@ -181,3 +181,11 @@ def test_what_is_no_tensor_or_has_no_memory():
     for t in (torch.zeros(4, dtype=torch.float16), torch.zeros(2, 2, 2), torch.zeros(())):
         with pytest.raises(ValueError, match="2-D CUDA"):
             bg._layer().quantize(t, t, t, None)
+
+
+def test_a_view_that_is_still_to_be_negated_is_refused():
+    """Its memory holds the values' negatives."""
+    x = torch._neg_view(torch.ones(2, 8))
+    for call in (lambda: bg.layernorm(x), lambda: bg.rmsnorm(x), lambda: bg.matmul(x, torch.ones(3, 8))):
+        with pytest.raises(ValueError, match="negated"):
+            call()
