@@ -69,18 +69,29 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 }
 
 // Test the phase; if it is not complete the thread may be suspended until it
-// completes or about `hint_ns` pass, whichever comes first.
+// completes or about `hint_ns` pass, whichever comes first.  CLUSTER: what it waits
+// for was stored by another block of the cluster.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity,
                                               uint32_t hint_ns = 1000000u)
 {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+            : "memory");
     return ok != 0;
 }
 
@@ -88,13 +99,14 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity,
 // gives up after timeout_ns of wall time (or 2^30 polls), or as soon as another
 // warp of the block has raised *abort.  On a timeout it raises *abort and the
 // global error word.  Returns true when the phase completed.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
                                           volatile int *abort, int *err)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1; it < (1u << 30); ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
         if ((it & 31u) == 0) {
             if (*abort) return false;
             if (globaltimer_ns() - t0 > timeout_ns) break;
@@ -107,13 +119,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 
 // Warp-converged form: lane 0 waits, every lane of the warp gets the outcome.
 // Keeps role warps converged (their other lanes never idle at a CTA barrier
-// while one lane works).
+// while one lane works).  The shuffle passes a value and orders no memory: the
+// barrier of the warp does, so that what lane 0 waited for is there for all.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
                                                uint64_t timeout_ns, volatile int *abort, int *err)
 {
     int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, timeout_ns, abort, err) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait<CLUSTER>(bar, parity, timeout_ns, abort, err) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
 }
 
 // ----------------------------------------------------------------------- TMA

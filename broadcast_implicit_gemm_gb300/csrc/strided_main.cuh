@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(kStridedThreads, 1)
                     okw = mbar_wait(&stg_empty[t], tph ^ 1u, p.timeout_ns, abort_flag, p.err);
                     if (okw) mbar_arrive_expect_tx(&stg_full[t], (uint32_t)nbox * 16384u);
                 }
-                if (!__shfl_sync(0xffffffffu, okw, 0)) { ok = false; break; }
+                okw = __shfl_sync(0xffffffffu, okw, 0);
+                __syncwarp();            // (the shuffle orders no memory)
+                if (!okw) { ok = false; break; }
                 t_iss[t] = true, t_par[t] = tph;
                 if (lane < nbox)
                     tma_load_4d(stg + t * kStridedStage + lane * 16384, &map_a, &stg_full[t], bx, by,

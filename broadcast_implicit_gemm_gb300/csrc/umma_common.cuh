@@ -264,9 +264,7 @@ __device__ __forceinline__ void epilogue_warp(const UmmaParams &p, const CUtenso
             gok = ((okm >> ((lane & 7) * 4)) & 0xFu) == 0xFu;
         }
         if (m == 0) {
-            int okw = 0;
-            if (lane == 0) okw = mbar_wait(&tfull[acc], acc_phase, p.timeout_ns, abort_flag, p.err);
-            if (!__shfl_sync(0xffffffffu, okw, 0)) {
+            if (!mbar_wait_warp(&tfull[acc], acc_phase, p.timeout_ns, abort_flag, p.err)) {
                 alive = false;
                 break;
             }

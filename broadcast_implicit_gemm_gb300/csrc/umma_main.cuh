@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(main_threads<NEPI>(), 1)
                         okw = mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.err);
                         if (okw) mbar_arrive_expect_tx(&full[stage], tx);
                     }
-                    if (!__shfl_sync(0xffffffffu, okw, 0)) { ok = false; break; }
+                    okw = __shfl_sync(0xffffffffu, okw, 0);
+                    __syncwarp();            // (the shuffle orders no memory)
+                    if (!okw) { ok = false; break; }
                     issued[stage] = true;
                     last_parity[stage] = phase;
                     uint8_t *a_dst = sa + stage * kABytes;
