@@ -481,14 +481,21 @@ def _layer():
         import importlib.util
 
         import torch
+
+        from . import _build
         path = os.path.join(_HERE, "_layer.so")
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+            raise RuntimeError(f"{path} is missing: build the CUDA library first, with the torch that is to use it "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         lib = load_library()
         loader = importlib.machinery.ExtensionFileLoader("_layer", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_layer", path, loader=loader))
         loader.exec_module(module)
+        # it reads tensors by the layout of the torch that it was compiled with
+        here = _build.layer_name(torch.__version__, torch.version.git_version)
+        if module.built_for != here:
+            raise RuntimeError(f"{path} was built for {module.built_for}, this is {here}: build it again "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
         module.init(_workspace, torch._C._cuda_cudaCachingAllocator_raw_alloc,
                     torch._C._cuda_cudaCachingAllocator_raw_delete,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value

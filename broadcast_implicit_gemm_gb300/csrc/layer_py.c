@@ -513,4 +513,10 @@ static PyMethodDef methods[] = {
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit__layer(void) { return PyModule_Create(&module); }
+/* built_for: the torch and the Python whose tensors layer_tensor.cpp was compiled to read. */
+PyMODINIT_FUNC PyInit__layer(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", LAYER_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}
