@@ -664,8 +664,9 @@ def layernorm(x, weight=None, bias=None, residual=None, eps=1e-5, out_dtype=None
               mean_out=None, rstd_out=None, stream=None):
     """h = x + residual; y = (h - mean(h)) * rsqrt(var(h) + eps) * weight + bias over the last axis of a matrix.
 
-    Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.  mean_out and
-    rstd_out, float32 vectors of a value per row, receive what layernorm_backward takes.
+    Returns y; (y, scales) for out_dtype float8_e4m3fn; and h after those when a residual is given.  out (of x's type) and
+    sum_out may be x or residual themselves.  mean_out and rstd_out, float32 vectors of a value per row, receive what
+    layernorm_backward takes.
     """
     if residual is not None and sum_out is None:
         sum_out = _output(None, None, x.dtype, *x.shape, x.device, stream)
@@ -700,7 +701,7 @@ def _sums(out, like, stream):
 
 def layernorm_backward(dout, x, mean, rstd, weight=None, dsum=None, dx=None, dweight=None, dbias=None, stream=None):
     """(dx, dweight, dbias) of layernorm, x the rows that were normed (h where there was a residual), mean and rstd
-    from its call.  dsum, the gradient that reaches h along the residual stream, is added to dx, which may be dout or
+    from its call.  dsum, the gradient that reaches h along the residual stream, is added to dx, which may be dout, x or
     dsum itself.  dout, dsum and dx are of x's dtype, dweight and dbias float32."""
     dx = _gradient(dx, x, stream)
     dweight, dbias = _sums(dweight, x, stream), _sums(dbias, x, stream)

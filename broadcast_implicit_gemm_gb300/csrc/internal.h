@@ -16,6 +16,23 @@ namespace bigemm {
 
 inline size_t dtype_size(int dt) { return dt == BIGEMM_F32 ? 4 : 2; }
 
+// Whether no address (but null) is there twice, the second time at place `from` or later:
+// outputs of one call that are the same buffer, or an input, would race.
+template <int N>
+inline bool distinct(const void *const (&p)[N], int from = 0)
+{
+    for (int i = 0; i < N; ++i)
+        for (int j = i + 1 > from ? i + 1 : from; j < N; ++j)
+            if (p[i] && p[i] == p[j]) return false;
+    return true;
+}
+
+// Whether an output is another buffer than an input, or takes its place row by row.
+inline bool apart_or_in_place(const void *out, long long ldo, const void *in, long long ldi, long long rows)
+{
+    return !out || out != in || ldo == ldi || rows == 1;
+}
+
 inline int out_extent(int in, int k, int s, int p)
 {
     const int span = in + 2 * p - k;

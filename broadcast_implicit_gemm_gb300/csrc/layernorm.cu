@@ -43,11 +43,15 @@ bigemm_status norm_backward(NormBackArgs &a, bool layer, int dtype, void *worksp
         return launch_column_sums(sums, s) == cudaSuccess ? BIGEMM_OK : BIGEMM_ERR_CUDA;
     }
     const size_t es = dtype_size(dtype);
-    if (a.dweight == a.dbias) return BIGEMM_ERR_INVALID_ARG;
     if (!a.dout || !a.x || !a.dx || (layer && (!a.mean || !a.rstd))) return BIGEMM_ERR_INVALID_ARG;
     if (a.ldd < a.cols || a.ldx < a.cols || a.ldo < a.cols || (a.dsum && a.lds < a.cols)) return BIGEMM_ERR_INVALID_ARG;
     if (!aligned(a.dout, 0, 1, es) || !aligned(a.x, 0, 1, es) || !aligned(a.dx, 0, 1, es) || !aligned(a.dsum, 0, 1, es) ||
         !aligned(a.weight, 0, 1, 4) || !aligned(a.mean, 0, 1, 4) || !aligned(a.rstd, 0, 1, 4))
+        return BIGEMM_ERR_INVALID_ARG;
+    // dx takes the place of what a thread has read; the sums are written while other rows are still read
+    if (!distinct({a.dout, a.x, a.dsum, a.weight, a.mean, a.rstd, a.dx, a.dweight, a.dbias}, 7) ||
+        !distinct({a.weight, a.mean, a.rstd, a.dx}, 3) || !apart_or_in_place(a.dx, a.ldo, a.dout, a.ldd, a.rows) ||
+        !apart_or_in_place(a.dx, a.ldo, a.x, a.ldx, a.rows) || !apart_or_in_place(a.dx, a.ldo, a.dsum, a.lds, a.rows))
         return BIGEMM_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 0, 1, 16) || bytes < back_workspace(a.rows, a.cols)) return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();
@@ -93,7 +97,12 @@ bigemm_status layernorm_run(int rows, int cols, bigemm_dtype in_dtype, const voi
         !aligned(weight, 0, 1, 4) || !aligned(bias, 0, 1, 4) || !aligned(out_scale, 0, 1, 16) || !aligned(mean, 0, 1, 4) ||
         !aligned(rstd, 0, 1, 4))
         return BIGEMM_ERR_INVALID_ARG;
-    if (out == sum_out || (mean && mean == rstd)) return BIGEMM_ERR_INVALID_ARG;
+    // out (of x's type) and sum_out may take the place of what a thread has read, row by row
+    if (!distinct({weight, bias, out, sum_out, out_scale, mean, rstd}, 2) || !distinct({x, residual, out_scale, mean, rstd}, 2) ||
+        !apart_or_in_place(sum_out, lds, x, ldx, rows) || !apart_or_in_place(sum_out, lds, residual, ldr, rows) ||
+        !apart_or_in_place(out, ldo, x, ldx, rows) || !apart_or_in_place(out, ldo, residual, ldr, rows) ||
+        (out_dtype != in_dtype && (out == x || out == residual)))
+        return BIGEMM_ERR_INVALID_ARG;
     DeviceState *ds = device_state();
     if (!ds) return BIGEMM_ERR_CUDA;
     const bool vec = aligned(x, ldx, es, 16) && aligned(residual, ldr, es, 16) && aligned(sum_out, lds, es, 16) &&

@@ -23,17 +23,6 @@ inline bool addressable(const void *p, long long ld, long long es) { return on_g
 
 inline long long packed_bytes(long long rows, long long cols, long long es) { return up(rows * up(cols * es, 16) * 16, 256) * 256; }
 
-// Whether no address (but null) is there twice: outputs of one call that are the same
-// buffer, or an input, would race.
-template <int N>
-inline bool distinct(const void *const (&p)[N], int from = 0)
-{
-    for (int i = 0; i < N; ++i)
-        for (int j = i + 1 > from ? i + 1 : from; j < N; ++j)
-            if (p[i] && p[i] == p[j]) return false;
-    return true;
-}
-
 // A row-major matrix as boxes of box_rows rows by box_cols columns.
 inline bool box_map(CUtensorMap *map, const void *p, int dt, long long rows, long long cols, long long ld, int box_rows,
                     int box_cols, CUtensorMapSwizzle swizzle)

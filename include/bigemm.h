@@ -433,9 +433,10 @@ bigemm_status rmsnorm_run(int rows, int cols, bigemm_dtype in_dtype, const void 
  * layernorm_run -- h = x + residual; out = (h - mean(h)) * rsqrt(var(h) + eps) *
  * weight + bias, row by row over `cols` columns, var the mean square of h - mean(h);
  * in fp32 from the inputs to one rounding of each output.
- *   x, residual (NULL: none), sum_out (NULL: not wanted; receives h; it may be x or
- *   residual itself) of in_dtype (F32, F16, BF16); weight, bias [cols] fp32, each or
- *   NULL (ones, zeros); out of in_dtype, F32, or MXF8 (then out_scale, else NULL)
+ *   x, residual (NULL: none), sum_out (NULL: not wanted; receives h) of in_dtype (F32,
+ *   F16, BF16); weight, bias [cols] fp32, each or NULL (ones, zeros); out of in_dtype,
+ *   F32, or MXF8 (then out_scale, else NULL).  sum_out, and out of in_dtype, may be x or
+ *   residual itself (same rows); outputs share no memory with anything else
  *   mean, rstd [rows] fp32, each or NULL (not wanted): of h before it is rounded,
  *   what layernorm_backward_run takes
  * Errors: INVALID_ARG, UNSUPPORTED (another out_dtype; cols above 2^30), CUDA.
@@ -454,7 +455,8 @@ bigemm_status layernorm_run(int rows, int cols, bigemm_dtype in_dtype, const voi
  * in fp32, dx rounded once; the sums' order does not depend on timing.
  *   dout, x (the normed rows: h where there was a residual), dsum (NULL: none; the
  *   gradient that reaches h along the residual stream) and dx of dtype (F32, F16,
- *   BF16); dx may be dout or dsum itself
+ *   BF16); dx may be dout, x or dsum itself (same rows); outputs share no memory with
+ *   anything else
  *   mean, rstd [rows] of the forward pass; weight [cols] or NULL (ones); dweight,
  *   dbias [cols], all fp32.  rows = 0 writes zeros to dweight and dbias.
  *   workspace: norm_backward_workspace_bytes of device memory on a 16-byte boundary,
