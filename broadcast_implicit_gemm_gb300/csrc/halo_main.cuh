@@ -332,7 +332,7 @@ cudaError_t launch_halo(const UmmaParams &p, const CUtensorMap &ma, const CUtens
     auto kern = which == 0   ? umma_conv_halo_kernel<BN, FMT, true, 1, FORM>
                 : which == 1 ? umma_conv_halo_kernel<BN, FMT, false, 1, FORM>
                              : umma_conv_halo_kernel<BN, FMT, false, (BN <= 128 ? 2 : 1), FORM>;
-    static unsigned long long attr_set[3] = {0, 0, 0};   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set[3] = {{0}, {0}, {0}};   // bit per device: smem opt-in done
     if (dev >= 64 || !(attr_set[which] >> dev & 1ull)) {
         DeviceState *ds = device_state();
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -230,7 +230,7 @@ cudaError_t launch_halo_pair_one(const UmmaParams &p, const CUtensorMap &ma, con
 {
     if (grid < 2 || grid % 2) return cudaErrorInvalidValue;
     auto kern = umma_conv_halo_pair_kernel<BN, FMT, FORM>;
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

@@ -1,5 +1,6 @@
 // internal.h -- types shared by the library's translation units (host side).
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <string>

@@ -401,7 +401,7 @@ cudaError_t launch_one(FewArgs<GATED> a, int split, bool alone, const FewMaps<GA
     a.stages = alone ? FewCfg<BN>::whole : FewCfg<BN>::half;
     auto kern = matmul_few_kernel<BN, MX, FULL, GATED>;
     constexpr int channels = GATED ? 64 : 128;
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

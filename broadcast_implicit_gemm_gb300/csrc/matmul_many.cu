@@ -528,7 +528,7 @@ cudaError_t launch_one(const MatmulArgs &a, int grid, const ManyMaps &maps, cuda
 {
     auto kern = matmul_many_kernel<BN, MX, FULL>;
     constexpr int smem = ManyCfg<BN, MX, FULL>::smem;
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

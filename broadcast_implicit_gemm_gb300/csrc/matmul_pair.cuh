@@ -276,7 +276,7 @@ cudaError_t launch_pairs(const typename Job::Args &a, const typename Job::Maps &
 {
     auto kern = matmul_pair_kernel<Job>;
     constexpr int smem = PairCfg::smem(Job::stages, Job::per_warp);
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

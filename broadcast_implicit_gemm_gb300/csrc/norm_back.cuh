@@ -727,7 +727,7 @@ cudaError_t launch_back_tpr(NormBackArgs a, const BackGrid &g, cudaStream_t s)
     auto kern = norm_back_kernel<T, LAYER, SUM, TPR, VEC, WIDE>;
     using R = Ring<T, SUM>;
     constexpr int rows = norm_threads(TPR) / TPR, most = rows * R::bytes(VEC, TPR);
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

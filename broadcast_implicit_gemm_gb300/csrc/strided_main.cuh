@@ -283,7 +283,7 @@ cudaError_t launch_strided_one(const UmmaParams &p, const CUtensorMap &ma, const
                                const CUtensorMap &mc, int grid, cudaStream_t stream)
 {
     auto kern = umma_conv_strided_kernel<BN, FMT, FORM>;
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(attr_set >> dev & 1ull)) {

@@ -275,7 +275,7 @@ cudaError_t launch_one(const UmmaParams &p, const CUtensorMap &ma, const CUtenso
                        const CUtensorMap &mc, int grid, cudaStream_t stream)
 {
     auto kern = umma_conv_kernel<BN, AMODE, FMT, RB, NEPI, FORM>;
-    static unsigned long long attr_set = 0;   // bit per device: smem opt-in done
+    static std::atomic<unsigned long long> attr_set{0};   // bit per device: smem opt-in done
     int dev = 0;
     cudaGetDevice(&dev);
     const size_t smem = RB ? (size_t)p.halo_smem : (size_t)Cfg<BN>::smem;
