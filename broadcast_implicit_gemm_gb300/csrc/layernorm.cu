@@ -13,13 +13,22 @@ bool aligned(const void *p, long long ld, size_t size, size_t to)
     return !p || (reinterpret_cast<uintptr_t>(p) % to == 0 && (ld * (long long)size) % (long long)to == 0);
 }
 
-// Rows of partial sums that the gradients of these rows leave: one per block of the
+// Rows of partial sums that the gradients of these rows leave at most: one per block of the
 // one-pass kernels (or cluster), or of the runs of long rows, eight blocks of 256 columns per SM.
 int back_parts(long long rows, int cols)
 {
     if (cols <= kBackMaxCols) return back_grid(rows, cols).parts;
     const long long wide = (cols + 255ll) / 256, want = (8ll * kBackSms + wide - 1) / wide;
     return (int)(rows < want ? rows : want);
+}
+
+// Of those, what the device runs at once: a cluster's walk over its rows is as long as any, so
+// that one that begins late ends as late.
+int resident_parts(long long rows, int cols)
+{
+    const int most = back_parts(rows, cols), cluster = cols <= kBackMaxCols ? back_grid(rows, cols).cluster : 1;
+    const int fit = cluster > 1 ? back_clusters(cluster) : 0;
+    return fit > 0 && fit < most ? fit : most;
 }
 
 uint64_t back_workspace(long long rows, int cols)
@@ -61,7 +70,7 @@ bigemm_status norm_backward(NormBackArgs &a, bool layer, int dtype, void *worksp
     const bool vec = aligned(a.dout, a.ldd, es, 16) && aligned(a.x, a.ldx, es, 16) && aligned(a.dx, a.ldo, es, 16) &&
                      aligned(a.dsum, a.lds, es, 16);
     a.inv_cols = 1.0f / (float)a.cols;
-    const int parts = back_parts(a.rows, a.cols);
+    const int parts = resident_parts(a.rows, a.cols);
     float *space = static_cast<float *>(workspace);
     if (parts > 1) {             // (one row of sums is the result)
         a.dweight = space, a.dbias = space + parts * sum_pitch(a.cols);

@@ -43,8 +43,14 @@ constexpr int kBackMaxCols = 8 * kBackCtaCols;   // of the one-pass kernels: of 
 // Blocks of the one-pass kernels: at most 1024 threads per SM.
 struct BackGrid {
     int threads, rows, cluster;       // rows: that a block takes at once; cluster: blocks on a row
-    int parts;                        // rows of partial sums: one per block or cluster
+    int parts;                        // rows of partial sums, at most: one per block or cluster
 };
+
+// Clusters of so many blocks, each with an SM to itself, that run at once on the current
+// device: 36 of 4 and 15 of 8, not 38 and 19, since a cluster's SMs are neighbours (4096 x
+// 40000 bf16 layer 712 us with 19, whose last four begin when others have done all their rows,
+// and 456 with 15; 4096 x 20000 358 with 38, 197 with 36).  0: not known.
+int back_clusters(int cluster);
 
 inline BackGrid back_grid(long long rows, int cols)
 {
@@ -756,9 +762,10 @@ cudaError_t launch_back_tpr(NormBackArgs a, const BackGrid &g, cudaStream_t s)
 }
 
 template <typename T, bool LAYER, bool SUM, bool VEC>
-cudaError_t launch_back_rows(const NormBackArgs &a, cudaStream_t s)
+cudaError_t launch_back_rows(const NormBackArgs &a, int parts, cudaStream_t s)
 {
-    const BackGrid g = back_grid(a.rows, a.cols);
+    BackGrid g = back_grid(a.rows, a.cols);
+    g.parts = parts;
     if (g.rows > 1) return launch_back_tpr<T, LAYER, SUM, 32, VEC>(a, g, s);
     if (g.cluster > 1)
         return launch_back_tpr<T, LAYER, SUM, kBackCtaCols / kPiece, VEC, true>(a, g, s);
@@ -772,7 +779,7 @@ cudaError_t launch_back_vec(const NormBackArgs &a, float *rstds, int parts, cuda
 {
     ProfScope prof(LAYER ? "layernorm_backward" : "rmsnorm_backward", s);
     if (a.cols <= kBackMaxCols)
-        return a.dsum ? launch_back_rows<T, LAYER, true, VEC>(a, s) : launch_back_rows<T, LAYER, false, VEC>(a, s);
+        return a.dsum ? launch_back_rows<T, LAYER, true, VEC>(a, parts, s) : launch_back_rows<T, LAYER, false, VEC>(a, parts, s);
     const dim3 rows((unsigned)a.rows);
     const float *roots = LAYER ? a.rstd : rstds;
     if (!LAYER) {
@@ -788,7 +795,7 @@ cudaError_t launch_back_vec(const NormBackArgs &a, float *rstds, int parts, cuda
 }  // namespace
 
 // The gradients of one type (norm_back_*.cu): dx, and partial sums in a.dweight and
-// a.dbias; rstds: [rows] for the roots of long RMS rows; parts: of long rows.
+// a.dbias; rstds: [rows] for the roots of long RMS rows; parts: rows of partial sums.
 cudaError_t launch_norm_back_f32(const NormBackArgs &a, bool layer, bool vec, float *rstds, int parts, cudaStream_t s);
 cudaError_t launch_norm_back_f16(const NormBackArgs &a, bool layer, bool vec, float *rstds, int parts, cudaStream_t s);
 cudaError_t launch_norm_back_bf16(const NormBackArgs &a, bool layer, bool vec, float *rstds, int parts, cudaStream_t s);
