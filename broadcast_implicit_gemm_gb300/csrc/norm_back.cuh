@@ -631,12 +631,20 @@ __global__ void __launch_bounds__(256) norm_back_columns_kernel(const NormBackAr
     if (c >= a.cols) return;
     const long long r0 = a.rows * blockIdx.y / parts, r1 = a.rows * (blockIdx.y + 1) / parts;
     const T *d = static_cast<const T *>(a.dout) + c, *x = static_cast<const T *>(a.x) + c;
+    // pieces of a run by themselves, so that no sum has more than some hundred additions behind it (up to
+    // some hundred thousand rows)
+    constexpr int kPieceRows = 256;
     float dw = 0.f, db = 0.f;
+    for (long long r = r0; r < r1;) {
+        const long long end = min(r + kPieceRows, r1);
+        float pw = 0.f, pb = 0.f;
 #pragma unroll 4
-    for (long long r = r0; r < r1; ++r) {
-        const float dv = to_f32<T>(d[r * a.ldd]), xv = to_f32<T>(x[r * a.ldx]);
-        dw = fmaf(dv, LAYER ? (xv - a.mean[r]) * rstds[r] : xv * rstds[r], dw);
-        if (LAYER) db += dv;
+        for (; r < end; ++r) {
+            const float dv = to_f32<T>(d[r * a.ldd]), xv = to_f32<T>(x[r * a.ldx]);
+            pw = fmaf(dv, LAYER ? (xv - a.mean[r]) * rstds[r] : xv * rstds[r], pw);
+            if (LAYER) pb += dv;
+        }
+        dw += pw, db += pb;
     }
     a.dweight[blockIdx.y * sum_pitch(a.cols) + c] = dw;
     if (LAYER) a.dbias[blockIdx.y * sum_pitch(a.cols) + c] = db;
