@@ -95,17 +95,17 @@ long long many_cost(const MatmulArgs &a, int sms, int bn, int channels, bool gat
 // 256 x 4096 x 4096 bf16: 17.9 us for few (64 tokens, K in 2) against 20.4 and
 // 24.4 in pairs; 512 x 4096 x 4096: 25 against 20.9 and 24.7; 1024 x 1024 x 8192:
 // 25.5 against 34.5 and 40.9.
-// GATED: the pairs' tiles have 128 channels of each product.
+// GATED: the pairs' tiles have 128 channels of each product, and sum K in one accumulator.
 template <bool GATED = false>
 Choice choose(const MatmulArgs &a, int sms)
 {
-    const bool mx = a.in_dt == BIGEMM_MXF8;
+    const bool mx = a.in_dt == BIGEMM_MXF8, pieces = GATED ? a.seg_blocks < a.k_blocks : matmul_in_pieces(a);
     Choice c = {};
     long long least = -1;
     for (int bn = 16; bn <= 128; bn *= 2) {
         // running sums over pieces are in registers, of at most 64 tokens; smaller MXFP8 tiles
         // would start inside a block of scales
-        if ((bn == 128 && matmul_in_pieces(a)) || (mx && bn < 64 && a.M > bn)) continue;
+        if ((bn == 128 && pieces) || (mx && bn < 64 && a.M > bn)) continue;
         if (up(a.M, bn) > 65535) continue;     // the grid's second axis
         const long long tiles = up(a.N, GATED ? 64 : 128) * up(a.M, bn);
         // clusters of 5 to 7 CTAs leave SMs of their neighbourhood idle (300 x 1000 x 2048: 13.6 us in
@@ -123,7 +123,7 @@ Choice choose(const MatmulArgs &a, int sms)
         }
         if (bn >= a.M) break;                  // larger tiles hold no more
     }
-    if (a.M > 128)
+    if (a.M > 128 && !(GATED && pieces))
         for (int bn = GATED ? 256 : 128; bn <= 256; bn += 128) {
             const long long cost = many_cost(a, sms, bn, GATED ? bn / 2 : bn, GATED);
             if (least < 0 || cost < least) c.many = true, c.bn = bn, least = cost;
@@ -254,7 +254,8 @@ bigemm_status gated(GatedArgs &a, void *workspace, uint64_t workspace_bytes, voi
     a.vec_gate = on_grid(a.gate, a.ldgate, 2, 16) && a.ldgate * 2 < kFar;
     a.vec_up = on_grid(a.up, a.ldup, 2, 16) && a.ldup * 2 < kFar;
     a.vec_bias = on_grid(a.bias, 0, 1, 16), a.vec_bias_up = on_grid(a.bias_up, 0, 1, 16);
-    a.k_blocks = a.seg_blocks = (int)up(a.K * 2ll, kRow);
+    a.k_blocks = (int)up(a.K * 2ll, kRow);
+    a.seg_blocks = a.K > kLongestSum ? full_segment(false) : a.k_blocks;
     a.timeout_ns = wait_timeout_ns();
     a.err = ds->err;
     PackList k(static_cast<uint8_t *>(workspace));

@@ -11,7 +11,8 @@
 // (64): the pairs share them as back_walk.h says (4096 x 4096 x 16384 gated: 3449
 // blocks' time per pair, 3776 in two launches).  Few tokens leave too few dx units, and
 // few channels too few dw units: each is cut along the summed axis then, the shares go to
-// a workspace in fp32, and launch_back_join adds them in their order.
+// a workspace in fp32, and launch_back_join adds them in their order.  So is a sum that is
+// longer than one accumulator takes (kLongestSum).
 #include "matmul_back.cuh"
 
 #include "matmul_pair.cuh"
@@ -81,8 +82,8 @@ struct BackJob {
     {
         uint32_t t;
         u.part = (int)fd_divmod((uint32_t)i, g.tiles, &t);
-        u.k0 = (int)fd_div((uint32_t)(g.blocks * u.part), g.shares);
-        u.k1 = (int)fd_div((uint32_t)(g.blocks * (u.part + 1)), g.shares);
+        u.k0 = share_start(g, u.part);
+        u.k1 = share_start(g, u.part + 1);
         uint32_t r;
         const int m = (int)fd_divmod(t, g.group, &r) * 8, rows = min(8, g.m - m);
         if (rows == 8) return {m + (int)(r & 7), (int)(r >> 3)};

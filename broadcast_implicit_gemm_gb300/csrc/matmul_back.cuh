@@ -18,11 +18,19 @@ namespace bigemm {
 // done in less time than divisions take (64 x 8192 x 8192: 60 us with some, 73 with more).
 struct UnitGrid {
     int m, n, split, blocks;
+    int whole, rest;                 // blocks by split
     FastDiv tiles, group, shares;    // by m * n, 8 * n and split
 };
+constexpr int kMostShares = 32768;   // rest times a share's number has 31 bits
 inline UnitGrid make_unit_grid(int m, int n, int split, int blocks)
 {
-    return {m, n, split, blocks, make_fastdiv((uint32_t)(m * n)), make_fastdiv(8u * (uint32_t)n), make_fastdiv((uint32_t)split)};
+    return {m, n, split, blocks, blocks / split, blocks % split, make_fastdiv((uint32_t)(m * n)), make_fastdiv(8u * (uint32_t)n),
+            make_fastdiv((uint32_t)split)};
+}
+// A share's first block (the number of blocks for share `split`).
+BIGEMM_FD_HD int share_start(const UnitGrid &g, int share)
+{
+    return g.whole * share + (int)fd_div((uint32_t)(g.rest * share), g.shares);
 }
 
 struct BackArgs {

@@ -21,6 +21,8 @@
 // accumulator short, so the error of one long sum grows with K (measured
 // 4.9e-6 relative at K = 4096, 1.9e-5 at 16384); sums of at most 512 elements
 // (2048 in 8 bits) are added up in registers instead, two accumulators taking turns.
+// So are a gated layer's past kLongestSum, whatever the number of tokens (64 x 65536 -> 1024
+// bf16 60 us, 61 in one sum; 4096 x 65536 -> 1024 1351, 668 by pairs of CTAs in one).
 //
 // GATED: a gated layer's two products (matmul_gated.cuh).  The 128 rows are 64 of the
 // gate's weights and the same 64 of the up product's, so that both sums of a channel
@@ -94,7 +96,7 @@ template <int BN, bool MX, bool FULL, bool GATED = false>
 __global__ void __launch_bounds__(kFewThreads)
     matmul_few_kernel(const __grid_constant__ FewMaps<GATED> maps, const FewArgs<GATED> p)
 {
-    static_assert(!GATED || (!MX && !FULL), "16-bit operands and outputs");
+    static_assert(!GATED || !MX, "16-bit operands and outputs");
     using C = FewCfg<BN>;
     constexpr int kChannels = GATED ? 64 : 128;      // of the output, per CTA
     constexpr int kPieces = kChannels / 8;           // of 8 channels, per token
@@ -464,11 +466,18 @@ cudaError_t launch_gated_few(const GatedArgs &a, FewCut cut, const CUtensorMap &
 {
     ProfScope prof("matmul_gated_few", stream);
     const FewMaps<true> maps = {map_w, map_x, map_up};
+    const bool pieces = a.seg_blocks < a.k_blocks;
     switch (cut.bn) {
-    case 16: return launch_one<16, false, false, true>(a, cut.split, cut.alone, maps, stream);
-    case 32: return launch_one<32, false, false, true>(a, cut.split, cut.alone, maps, stream);
-    case 64: return launch_one<64, false, false, true>(a, cut.split, cut.alone, maps, stream);
-    case 128: return launch_one<128, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 16:
+        return pieces ? launch_one<16, false, true, true>(a, cut.split, cut.alone, maps, stream)
+                      : launch_one<16, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 32:
+        return pieces ? launch_one<32, false, true, true>(a, cut.split, cut.alone, maps, stream)
+                      : launch_one<32, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 64:
+        return pieces ? launch_one<64, false, true, true>(a, cut.split, cut.alone, maps, stream)
+                      : launch_one<64, false, false, true>(a, cut.split, cut.alone, maps, stream);
+    case 128: return pieces ? cudaErrorInvalidValue : launch_one<128, false, false, true>(a, cut.split, cut.alone, maps, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -358,6 +358,9 @@ uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, cons
  *   x [M,K], w_gate and w_up [N,K], out [M,N] of dtype (F16 or BF16); bias_gate,
  *   bias_up [N] fp32, each or NULL; fp32 sums, out rounded once (g and u are not
  *   rounded on the way to it)
+ *   one tensor-core accumulator, which cuts each addition short, takes sums of up to
+ *   32768 products (off by at most 2e-4 of their magnitudes' sum, where all have one
+ *   sign); longer K is summed in pieces of 512
  *   gate, up [M,N] of dtype, each or NULL (not wanted): receive g and u, each rounded
  *   once, which matmul_gated_backward_run takes.  out, gate and up are buffers of their own
  *   workspace: matmul_gated_workspace_bytes of device memory on a 16-byte boundary,
@@ -380,9 +383,11 @@ uint64_t matmul_gated_workspace_bytes(int M, int N, int K, const void *x, int64_
 /*
  * matmul_backward_run -- gradients of out = x w^T + bias, of dout [M,N], that of out:
  *   dx [M,K] = dout w,  dw [N,K] = dout^T x,  dbias [N] = sum over tokens of dout
- *   all but dbias (fp32, or NULL: not wanted) of dtype (F16 or BF16); fp32 sums, each
- *   output rounded once; the sums' order does not depend on timing.  M = 0 writes zeros
- *   to dw and dbias.  The outputs are buffers of their own.
+ *   all but dbias (fp32, or NULL: not wanted) of dtype (F16 or BF16); fp32 sums, of at
+ *   most 32768 products in a tensor-core accumulator (as in matmul_gated_run) and the
+ *   shares of longer ones added in fp32; each output rounded once; the sums' order does
+ *   not depend on timing.  M = 0 writes zeros to dw and dbias.  The outputs are buffers of
+ *   their own.
  *   workspace: matmul_backward_workspace_bytes of device memory on a 16-byte boundary,
  *   the call's until it is done.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype F32; a size above 2^30), CUDA.
