@@ -3,8 +3,10 @@
 //   d_g = dout u act'(g),  d_u = dout act(g)
 //
 // rounded once to the operands' type, which is what the tensor core takes (a separate
-// multiplication would round them too), and their sums over the tokens, of the fp32
-// values before that.  Bound by memory: 10 bytes per element of 16-bit matrices.  A
+// multiplication would round them too; two 16-bit parts of each would keep 22 bits for
+// twice the products, which take 1.2 of 1.4 ms of 4096 x 4096 -> 16384.  dx and dw are off by 0.0024
+// in the 2-norm so, bf16, by 0.0017 with unrounded ones), and their sums over the tokens,
+// of the fp32 values before that.  Bound by memory: 10 bytes per element of 16-bit matrices.  A
 // warp takes 256 columns, 8 a lane, of every eighth row of its block's run, so that a
 // lane's sums stay in registers; two rows' loads are in flight.
 #include "column_sums.cuh"

@@ -48,8 +48,8 @@ struct BackGrid {
 
 // Clusters of so many blocks, each with an SM to itself, that run at once on the current
 // device: 36 of 4 and 15 of 8, not 38 and 19, since a cluster's SMs are neighbours (4096 x
-// 40000 bf16 layer 712 us with 19, whose last four begin when others have done all their rows,
-// and 456 with 15; 4096 x 20000 358 with 38, 197 with 36).  0: not known.
+// 40000 bf16 layer 720 us with 19, whose last four begin when others have done all their rows,
+// and 462 with 15; 4096 x 20000 358 with 38, 197 with 36).  0: not known.
 int back_clusters(int cluster);
 
 inline BackGrid back_grid(long long rows, int cols)

@@ -359,8 +359,8 @@ uint64_t matmul_workspace_bytes(int M, int N, int K, bigemm_dtype in_dtype, cons
  *   bias_up [N] fp32, each or NULL; fp32 sums, out rounded once (g and u are not
  *   rounded on the way to it)
  *   one tensor-core accumulator, which cuts each addition short, takes sums of up to
- *   32768 products (off by at most 2e-4 of their magnitudes' sum, where all have one
- *   sign); longer K is summed in pieces of 512
+ *   32768 products (terms of one sign come out 2e-4 too small at that length, 2e-5 at
+ *   4096); longer K is summed in pieces of 512
  *   gate, up [M,N] of dtype, each or NULL (not wanted): receive g and u, each rounded
  *   once, which matmul_gated_backward_run takes.  out, gate and up are buffers of their own
  *   workspace: matmul_gated_workspace_bytes of device memory on a 16-byte boundary,
@@ -403,7 +403,8 @@ uint64_t matmul_backward_workspace_bytes(int M, int N, int K, const void *dout, 
 /*
  * matmul_gated_backward_run -- gradients of matmul_gated_run, of dout [M,N], that of out,
  * and gate and up (g and u) as that call kept them:
- *   dg = dout u act'(g),  du = dout act(g)   in fp32, then rounded to dtype
+ *   dg = dout u act'(g),  du = dout act(g)   in fp32, then rounded to dtype, which the
+ *   tensor core takes (F16: infinite past 65504, fewer bits below 6e-5)
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  *   dbias_gate, dbias_up [N] fp32, each or NULL: sums over tokens of dg and du, not rounded
  *   (act' of relu is 0 at 0.)  Otherwise as matmul_backward_run.
