@@ -1,11 +1,17 @@
 """The grid of the norms' gradients of rows that a cluster of blocks shares: no more clusters than run at once, since each
 walks over an equal share of the rows (a cluster that began when another had ended doubled the time)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import broadcast_implicit_gemm_gb300 as bg
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def rows_of_sums(rows, cols, layer):
@@ -32,3 +38,25 @@ def test_clusters(layer):
     # eight neighbours each: groups of SMs are no multiples of eight
     assert 8 <= rows_of_sums(400, 40000, layer) < sms // 8
     assert rows_of_sums(5, 40000, layer) == 5
+
+
+FIRST_CALL = r'''
+import torch
+import broadcast_implicit_gemm_gb300 as bg
+x, d, out = (torch.randn((300, 40000), device="cuda").bfloat16() for _ in range(3))
+w, dw = torch.randn((64, 64), device="cuda").bfloat16(), torch.empty(40000, device="cuda")
+bg.matmul(w, w)                  # the library knows the device
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    bg.rmsnorm_backward(d, x, dx=out, dweight=dw)
+graph.replay()
+want = bg.rmsnorm_backward(d, x)
+assert torch.equal(out, want[0]) and torch.equal(dw, want[1]) and bg.bigemm_last_device_error() == 0
+print("same")
+'''
+
+
+def test_a_first_call_that_is_captured():
+    """How many clusters fit is asked for once, which may be while a stream is captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
