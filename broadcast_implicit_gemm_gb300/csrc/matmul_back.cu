@@ -143,7 +143,7 @@ struct BackJob {
             }
             return;
         }
-        // 64 columns, a row of 128 bytes, by one TMA store: what is past the matrix it leaves alone
+        // 64 columns, a row of 128 bytes, by one TMA store
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
 #pragma unroll
@@ -160,7 +160,7 @@ struct BackJob {
                 *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c * 4 + i) ^ (lane & 7)) << 4)) =
                     make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
         }
-        if (dx ? p.dx_rows : p.dw_rows[w]) {
+        if ((dx ? p.dx_rows : p.dw_rows[w]) && whole_words(p.K, n, 64)) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {

@@ -70,7 +70,8 @@ __device__ __forceinline__ void words_of(const float (&v)[32], int dt, uint32_t 
 }
 
 // A warp's 32 rows of WORDS 32-bit words of 16-bit values, in its staging as stage_words
-// leaves them, to a matrix of `rows` x `cols` whose rows are off the 16-byte grid: a lane
+// leaves them, to a matrix of `rows` x `cols` whose rows are off the 16-byte grid, or end inside
+// a 16-byte word: a lane
 // a word of a row, which a row that starts on an odd element shifts by its neighbour's.
 // (A lane a column of 16 rows: 16 x 5632 x 7449 gradients 84 us.)
 template <int WORDS>
@@ -101,8 +102,13 @@ __device__ __forceinline__ void put_off_grid(void *out, long long ld, long long 
     __syncwarp();                                // before the staging is written again
 }
 
+// Whether TMA may store a box of `box` 16-bit columns from column n on of a matrix of `cols`.  It
+// leaves alone rows past the matrix, but is not exact to the element at the end of a row (the
+// element behind the last of 15, in rows of 16, became 0): a row has to end with a 16-byte word.
+__device__ __forceinline__ bool whole_words(long long cols, int n, int box) { return cols % 8 == 0 || n + box <= cols; }
+
 // A warp's 32 x 32 sums, a lane's row in v, to a 16-bit matrix, on the 16-byte grid
-// (by_rows) by TMA, which leaves alone what is past the matrix.
+// (by_rows) by TMA.
 template <int PER_WARP>
 __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void *out, long long ld, int dt, long long rows,
                                       long long cols, uint8_t *stage, int &piece, int lane, long long m_warp, int n,
@@ -111,7 +117,7 @@ __device__ __forceinline__ void put16(const CUtensorMap *map, bool by_rows, void
     uint32_t w[16];
     words_of(v, dt, w);
     const uint8_t *buf = stage_words<PER_WARP, 16>(stage, piece, lane, w);
-    if (!by_rows) {
+    if (!by_rows || !whole_words(cols, n, 32)) {
         put_off_grid<16>(out, ld, rows, cols, buf, lane, m_warp, n);
     } else if (lane == 0 && m_warp < rows) {
         tma_store_2d(map, buf, n, (int)m_warp);
